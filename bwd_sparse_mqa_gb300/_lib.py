@@ -23,6 +23,7 @@ SMQA_ERR_DEVICE_TIMEOUT = 4
 FLAG_RETURN_DKV_FP32 = 1
 FLAG_REFERENCE_ROUNDING = 2
 FLAG_DETERMINISTIC_DKV = 4
+FLAG_ZERO_PADDING = 16
 
 # Every symbol include/sparse_mqa.h declares (checked by the tests).
 EXPORTS = [
@@ -32,7 +33,8 @@ EXPORTS = [
     "smqa_fwd_workspace_bytes", "smqa_fwd_static_scratch", "smqa_bwd_sink_grad",
     "smqa_fwd_host_workspace_bytes", "smqa_fwd_bwd_host_workspace_bytes", "smqa_fwd_host",
     "smqa_fwd_bwd_host", "smqa_host_chunk_plan", "smqa_set_wait_limit_ns", "smqa_debug_stall",
-    "smqa_indexer_bwd", "smqa_batched_indexer_bwd",
+    "smqa_indexer_bwd", "smqa_batched_indexer_bwd", "smqa_paged_plan", "smqa_paged_release",
+    "smqa_paged_append", "smqa_paged_fwd_workspace_bytes", "smqa_paged_fwd",
 ]
 STATIC_SCRATCH_BYTES = 64 << 20
 
@@ -40,6 +42,12 @@ STATIC_SCRATCH_BYTES = 64 << 20
 class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("S", ctypes.c_int32), ("S_kv", ctypes.c_int32),
                 ("H", ctypes.c_int32), ("D", ctypes.c_int32), ("topk", ctypes.c_int32)]
+
+
+class PagedShape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("R", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("topk", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int32)]
 
 
 class SMQAError(RuntimeError):
@@ -88,6 +96,17 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.smqa_indexer_bwd.restype = st
     lib.smqa_batched_indexer_bwd.argtypes = [P, P, P, P, P, S, P, P]
     lib.smqa_batched_indexer_bwd.restype = st
+    I = ctypes.c_int32
+    lib.smqa_paged_plan.argtypes = [P] * 5 + [I] * 6 + [P] * 8
+    lib.smqa_paged_plan.restype = st
+    lib.smqa_paged_release.argtypes = [P, P, P, I, I, I, P, P, I, P]
+    lib.smqa_paged_release.restype = st
+    lib.smqa_paged_append.argtypes = [P, P, I, I, I, I, P, P, P]
+    lib.smqa_paged_append.restype = st
+    lib.smqa_paged_fwd_workspace_bytes.argtypes = [PagedShape]
+    lib.smqa_paged_fwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.smqa_paged_fwd.argtypes = [P] * 9 + [PagedShape, F, P, P, P, ctypes.c_size_t, U, P]
+    lib.smqa_paged_fwd.restype = st
     lib.smqa_debug_stall.argtypes = [ctypes.c_int]
     lib.smqa_debug_stall.restype = None
     lib.smqa_set_wait_limit_ns.argtypes = [ctypes.c_uint64]

@@ -206,6 +206,8 @@ void set_last_error(const char* msg) { std::snprintf(g_last_error, sizeof g_last
 
 smqa_status validate_shape(const smqa_shape& s) { return check_shape(s); }
 
+smqa_status cuda_failure(cudaError_t e, const char* where) { return cuda_fail(e, where); }
+
 float effective_scale(float sm_scale, int D) {
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return 1.0f / std::sqrt(static_cast<float>(D));
   return sm_scale;

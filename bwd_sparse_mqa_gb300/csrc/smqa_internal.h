@@ -125,6 +125,26 @@ inline size_t det_stats_offset(const smqa_shape& s) {
   return (elems * 8 + 255) & ~static_cast<size_t>(255);
 }
 
+// Attention over the 8-bit paged cache (smqa_paged_fwd).
+struct PagedFwdParams {
+  const __nv_bfloat16* q;    // [T,H,D]
+  const uint8_t* cache;      // e4m3 [n_pages, page, D]
+  const float* scales;       // [n_pages]
+  const float* sink;         // [H]
+  const int32_t* table;      // [R, max_pages]
+  const int32_t* seq_lens;   // [R]
+  const int32_t* token_req;  // [T]
+  const int32_t* positions;  // [T] (null allowed with an index list)
+  const int32_t* idx;        // [T, topk], null: every position up to the token's own
+  __nv_bfloat16* o;          // [T,H,D]
+  float* lse;                // [T,H]
+  int T, R, H, D, topk, max_pages, n_pages, page_shift;
+  float scale_log2;          // sm_scale * log2(e)
+  int zero_padding;
+};
+
+cudaError_t launch_paged_fwd(const PagedFwdParams& p, cudaStream_t stream);
+
 // Records `msg` as the text smqa_last_error() returns on this thread.
 void set_last_error(const char* msg);
 
@@ -164,6 +184,11 @@ smqa_status bwd_main_launch(const void* q, const void* kv, const void* dout, con
                             const float* lse, const float* delta, const smqa_shape& s,
                             float scale, void* dq, float* acc, unsigned long long* acc_fixed,
                             const int* fix_shift, void* exch, cudaStream_t stream);
+// Pointer alignment (a power of two), and the record of a failing CUDA call.
+inline bool is_aligned(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+smqa_status cuda_failure(cudaError_t e, const char* where);
 // The entry points' shape check (records the reason on failure).
 smqa_status validate_shape(const smqa_shape& s);
 // sm_scale as the entry points interpret it (<= 0 or NaN selects D^-1/2).

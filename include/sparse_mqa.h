@@ -356,6 +356,141 @@ smqa_status smqa_batched_indexer_bwd(const void* index_q, const float* weights,
                                      cudaStream_t stream);
 
 /*
+ * Serving: an 8-bit paged kv cache, and sparse MQA over it.  (The sparse MQA
+ * pages have no counterpart: their interfaces take one contiguous bf16 kv.)
+ *
+ * The cache is a pool of n_pages pages of page_size token rows,
+ *   kv_cache  [n_pages, page_size, D]  e4m3 (bit patterns of float8_e4m3fn)
+ *   kv_scales [n_pages]                fp32, one positive scale per page (and,
+ *                                      keys = values and one kv head, per head)
+ * a row stands for kv_scales[page] * codes.  Request r holds its tokens, in
+ * order, in the pages block_table[r, 0], block_table[r, 1], ...; an entry
+ * outside [0, n_pages) holds nothing.  A token's cache slot is
+ * page * page_size + (position mod page_size).
+ */
+typedef struct {
+    int32_t T;          /* token rows of the call (all requests together; may be 0) */
+    int32_t R;          /* requests: rows of block_table and seq_lens               */
+    int32_t H;          /* query heads sharing the one kv head                      */
+    int32_t D;          /* head dim of q, of the cache and of O                     */
+    int32_t topk;       /* index slots per token; 0: every position up to its own   */
+    int32_t page_size;  /* token rows per page: 16, 32, 64 or 128                   */
+    int32_t max_pages;  /* columns of block_table                                   */
+    int32_t n_pages;    /* pages in the pool                                        */
+} smqa_paged_shape;
+
+/*
+ * Block table, offsets and slots of one step, from the requests' lengths.
+ *   context_lens [R]  int32  tokens each request already has in the cache
+ *   query_lens   [R]  int32  tokens each request adds in this step
+ *   block_table  [R, max_pages] int32  pages held (the first
+ *                            ceil(context / page_size) entries are read)
+ *   free_pages   [pool] int32, free_count [1] int32: a stack of free pages,
+ *                            entries [0, free_count) valid, its top the last
+ * Written:
+ *   block_table_out [R, max_pages]  block_table with the pages that the new
+ *                            tokens need; the k-th of these, counted over
+ *                            requests in order, is free_pages[free_count-1-k],
+ *                            or -1 once the stack is empty.  May be
+ *                            block_table itself (then only the new entries
+ *                            are written).
+ *   free_count_out [1]       free_count minus the pages needed: negative, it
+ *                            is the number of pages that were missing.  May be
+ *                            free_count itself.
+ *   seq_lens   [R]           context + query (may be context_lens itself only
+ *                            when free_count_out is free_count)
+ *   cu_query   [R + 1]       exclusive sum of query_lens, and the total
+ *   token_req, positions, slot_mapping [max_tokens]: request, position and
+ *                            cache slot of each new token, requests in order;
+ *                            a slot is -1 where there is no page for it
+ *                            (stack empty, or a position past max_pages
+ *                            pages); rows from the total on are -1 in all
+ *                            three.  Tokens past max_tokens are left out.
+ * Negative lengths and a negative free_count count as 0.  R <= 16384,
+ * n_pages * page_size < 2^31, context + query < 2^31.  One launch.
+ */
+smqa_status smqa_paged_plan(const int32_t* context_lens, const int32_t* query_lens,
+                            const int32_t* block_table, const int32_t* free_pages,
+                            const int32_t* free_count, int32_t R, int32_t max_pages,
+                            int32_t page_size, int32_t n_pages, int32_t pool,
+                            int32_t max_tokens, int32_t* block_table_out,
+                            int32_t* free_count_out, int32_t* seq_lens, int32_t* cu_query,
+                            int32_t* token_req, int32_t* positions, int32_t* slot_mapping,
+                            cudaStream_t stream);
+
+/*
+ * Gives the pages of finished requests back: every entry of block_table
+ * [R, max_pages] in [0, n_pages) of a row r with release[r] != 0 is pushed on
+ * the stack (rows in order, entries in order) and becomes -1, and
+ * seq_lens[r] becomes 0 (seq_lens may be NULL).  free_pages holds `pool`
+ * entries; pages that would not fit are dropped (which cannot happen when
+ * pool >= n_pages and each page has one owner).  A negative free_count
+ * counts as 0.
+ */
+smqa_status smqa_paged_release(int32_t* block_table, int32_t* seq_lens, const uint8_t* release,
+                               int32_t R, int32_t max_pages, int32_t n_pages,
+                               int32_t* free_pages, int32_t* free_count, int32_t pool,
+                               cudaStream_t stream);
+
+/*
+ * Writes T new kv rows into the cache.
+ *   kv_new       bf16  [T, D]
+ *   slot_mapping int32 [T]   cache slot per row (-1, or anything outside the
+ *                            pool: the row is skipped)
+ *   kv_cache, kv_scales      written in place
+ * The new rows of one page are consecutive in the batch and their slots
+ * ascend by one, as smqa_paged_plan lists them (a page with two separate runs
+ * of rows in one call is left in an undefined state).  A page's scale is the
+ * smallest power of two s >= 2^-60 with |x| <= 448 s for every finite x written
+ * to it since its first row (row 0 starts the page afresh; rows before the run
+ * count through the scale they have).  A new row becomes e4m3(x / s), rounded
+ * to nearest even; when a run makes the scale grow from s0 to s, the page's
+ * earlier rows become e4m3(code * s0 / s) (exact, but for codes that fall into
+ * e4m3's subnormals).  NaN and infinities are stored as NaN and do not enter
+ * the scale.  Rows behind the run keep their bits.  D in {64, 512}.
+ */
+smqa_status smqa_paged_append(const void* kv_new, const int32_t* slot_mapping, int32_t T,
+                              int32_t D, int32_t page_size, int32_t n_pages, void* kv_cache,
+                              float* kv_scales, cudaStream_t stream);
+
+/* smqa_paged_fwd: write O = 0 and lse = -inf for tokens of no request
+ * (padding); without it their rows of o and lse are left as they were. */
+#define SMQA_FLAG_ZERO_PADDING 16u
+
+/*
+ * Sparse MQA over the cache, for single tokens and for prompts.
+ *   q            [T, H, D]  bf16
+ *   attn_sink    [H]        fp32
+ *   block_table  [R, max_pages] int32, seq_lens [R] int32
+ *   token_req    [T]        int32  request of each token; outside [0, R): padding
+ *   positions    [T]        int32  position of each token; may be NULL when topk > 0
+ *   topk_idxs    [T, topk]  int32  positions in the token's own request (NULL
+ *                           when topk = 0); slots outside [0, seq_lens[req])
+ *                           are masked, a position listed twice counts twice
+ *   o            [T, H, D]  bf16, lse [T, H] fp32: as in smqa_fwd
+ * With topk = 0 a token attends to the positions j <= positions[t],
+ * j < seq_lens[req].  A position whose block-table entry is outside
+ * [0, n_pages) is masked.  A token with nothing to attend to gets O = 0 and
+ * lse = sink / ln 2.  A head whose q row holds a NaN or an infinity gets NaN.
+ * kv_scales lie in [2^-60, 2^120]. 
+ *   workspace    at least smqa_paged_fwd_workspace_bytes(shape) bytes, 256-byte
+ *                aligned (NULL allowed when that is 0); needs no
+ *                initialisation; calls whose kernels may overlap must not
+ *                share it
+ *   flags        0 or SMQA_FLAG_ZERO_PADDING
+ * 1 <= H <= 128, D in {64, 512}, n_pages * page_size < 2^31,
+ * T * max(H, topk) < 2^31.
+ */
+size_t smqa_paged_fwd_workspace_bytes(smqa_paged_shape shape);
+smqa_status smqa_paged_fwd(const void* q, const void* kv_cache, const float* kv_scales,
+                           const float* attn_sink, const int32_t* block_table,
+                           const int32_t* seq_lens, const int32_t* token_req,
+                           const int32_t* positions, const int32_t* topk_idxs,
+                           smqa_paged_shape shape, float sm_scale, void* o, float* lse,
+                           void* workspace, size_t workspace_bytes, unsigned flags,
+                           cudaStream_t stream);
+
+/*
  * Reads the device status word that kernels set when a bounded wait runs out
  * (SMQA_OK if none did).  Synchronizes the current device first.  A nonzero
  * `clear` resets the word afterwards.
