@@ -208,6 +208,12 @@ smqa_status validate_shape(const smqa_shape& s) { return check_shape(s); }
 
 smqa_status cuda_failure(cudaError_t e, const char* where) { return cuda_fail(e, where); }
 
+int* device_status_word(cudaError_t* err) { return status_ptr(err); }
+
+uint64_t current_wait_limit_ns() { return wait_limit_ns(); }
+
+int current_stall_cta() { return g_stall_cta.load(std::memory_order_relaxed); }
+
 float effective_scale(float sm_scale, int D) {
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return 1.0f / std::sqrt(static_cast<float>(D));
   return sm_scale;

@@ -141,9 +141,15 @@ struct PagedFwdParams {
   int T, R, H, D, topk, max_pages, n_pages, page_shift;
   float scale_log2;          // sm_scale * log2(e)
   int zero_padding;
+  uint8_t* ws;               // workspace (paged_fwd_workspace bytes)
+  int* status;
+  uint64_t limit_ns;
+  int stall_cta;             // test hook: this CTA stalls after its first MMA (-1: none)
 };
 
-cudaError_t launch_paged_fwd(const PagedFwdParams& p, cudaStream_t stream);
+size_t paged_fwd_workspace(const smqa_paged_shape& s);
+cudaError_t launch_paged_fwd(const PagedFwdParams& p, const smqa_paged_shape& s,
+                             cudaStream_t stream);
 
 // Records `msg` as the text smqa_last_error() returns on this thread.
 void set_last_error(const char* msg);
@@ -189,6 +195,11 @@ inline bool is_aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 smqa_status cuda_failure(cudaError_t e, const char* where);
+// The current device's status word (null and *err on failure), the limit of
+// bounded waits and the CTA of the stall hook.
+int* device_status_word(cudaError_t* err);
+uint64_t current_wait_limit_ns();
+int current_stall_cta();
 // The entry points' shape check (records the reason on failure).
 smqa_status validate_shape(const smqa_shape& s);
 // sm_scale as the entry points interpret it (<= 0 or NaN selects D^-1/2).

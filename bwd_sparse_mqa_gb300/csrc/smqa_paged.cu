@@ -7,7 +7,7 @@
 #include <cstdio>
 
 #include "smqa_internal.h"
-#include "smqa_ptx.cuh"
+#include "smqa_paged.cuh"
 
 namespace smqa {
 
@@ -203,18 +203,6 @@ __global__ void __launch_bounds__(1024)
 // ---------------------------------------------------------------------------
 // Append: new rows into the cache, one power-of-two scale per page
 // ---------------------------------------------------------------------------
-// e4m3 of two values, saturating, `lo` in the low byte.
-__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
-  uint16_t d;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ float2 e4m3x2_value(uint16_t v) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
-  return __half22float2(*reinterpret_cast<__half2*>(&h));
-}
-
 // The least k >= -60 with amax <= 448 * 2^k, from amax's exponent and
 // mantissa (448 = 1.75 * 2^8): amax = m 2^e with 1 <= m < 2.
 __device__ __forceinline__ int scale_exponent(float amax) {
@@ -439,8 +427,7 @@ smqa_status smqa_paged_append(const void* kv_new, const int32_t* slot_mapping, i
 }
 
 size_t smqa_paged_fwd_workspace_bytes(smqa_paged_shape shape) {
-  if (check_paged(shape) != SMQA_OK) return 0;
-  return 0;
+  return check_paged(shape) == SMQA_OK && shape.T > 0 ? paged_fwd_workspace(shape) : 0;
 }
 
 smqa_status smqa_paged_fwd(const void* q, const void* kv_cache, const float* kv_scales,
@@ -489,7 +476,13 @@ smqa_status smqa_paged_fwd(const void* q, const void* kv_cache, const float* kv_
   p.page_shift = page_shift_of(shape.page_size);
   p.scale_log2 = effective_scale(sm_scale, shape.D) * 1.4426950408889634f;
   p.zero_padding = (flags & SMQA_FLAG_ZERO_PADDING) ? 1 : 0;
-  const cudaError_t e = launch_paged_fwd(p, stream);
+  p.ws = static_cast<uint8_t*>(workspace);
+  cudaError_t e;
+  p.status = device_status_word(&e);
+  if (!p.status) return cuda_failure(e, "status word");
+  p.limit_ns = current_wait_limit_ns();
+  p.stall_cta = current_stall_cta();
+  e = launch_paged_fwd(p, shape, stream);
   if (e != cudaSuccess) return cuda_failure(e, "paged fwd launch");
   return SMQA_OK;
 }

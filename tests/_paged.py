@@ -7,9 +7,10 @@ of fp32):
           (q as two e4m3 pieces of its scaled row leave at most 2^-22 of the
           row's largest value; the fp32 sum of D products adds the rest) +
           4 eps |x_j| (scale factors, and the running maximum's subtraction)
-  weight  two e4m3 pieces: 2^-4 of 2^-4 of the weight, halved never assumed:
-          2^-8 relative, and 2^-16 of the token's largest weight (p_j s_j)
-          where the second piece is subnormal; 2^-21 for exp2
+  weight  two e4m3 pieces of its value in fp16: 2^-4 of 2^-4 of the weight, and
+          2^-11 for the step through fp16, relative; and 2^-16 of the token's
+          largest weight (p_j s_j) where the second piece is subnormal; 2^-21
+          for exp2
   O       2^-9 relative for its own rounding to bf16, the weights' error times
           |k_jd|, n eps for the fp32 sums
   lse     max_j |dx_j| / ln 2, exp2 and sums (2^-21 + n eps) / ln 2, and
@@ -123,7 +124,7 @@ def attn(q, val, scale, sink, table, seq, req, pos=None, idx=None, sm_scale=None
         qmax = q[t].abs().amax(1, keepdim=True)
         dx = (sm * (2.0 ** -22 + 2 * D * eps) * qmax * k.abs().sum(1)[None, :] + 4 * eps * x.abs())
         w = p * s
-        rel = torch.expm1(dx) + 2.0 ** -8 + 2.0 ** -21 + j.numel() * eps
+        rel = torch.expm1(dx) + 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -21 + j.numel() * eps
         bo[t] = (2.0 ** -9 * o[t].abs() + (rel * p) @ k.abs() / l
                  + 2.0 ** -16 * w.amax(1, keepdim=True) / l * c.abs().sum(0)[None, :]
                  + o[t].abs() * (torch.expm1(dx.amax(1, keepdim=True)) + 2.0 ** -21 + j.numel() * eps))
