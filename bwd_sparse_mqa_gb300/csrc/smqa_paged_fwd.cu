@@ -13,11 +13,15 @@
 //   q  = 2^-k (hi + lo / 32), k per row so that the largest value of 2^k q
 //        lies in [128, 256): bf16's 8 bits fit the two pieces exactly down to
 //        2^-22 of the row's largest value;
-//   w' = 2^(6 + y_j - m), y_j = x_j + log2 s_j the weight that multiplies the
-//        codes, m the running maximum of y, w' = hi + lo: a relative error of
-//        2^-8 + 2^-11 at most, down to 2^-16 of the largest weight.  m may lag
-//        behind the true maximum by 2.75 (w' <= 2^8.75 < 448, e4m3's largest),
-//        so that O is seldom rescaled.  l adds w' / s_j in fp32.
+//   w  = 2^(y_j - m - 2), y_j = x_j + log2 s_j: the weight that multiplies the
+//        codes, m the running maximum of y, 2^8 w = hi + lo: a relative error
+//        of 2^-8 + 2^-11 at most, down to 2^-16 of the largest weight.  m may
+//        lag behind the true maximum by 2.75 (2^8 w <= 2^8.75 < 448, e4m3's
+//        largest), so that O is seldom rescaled.  l adds w / s_j in fp32.
+//        An fp16 number below 2 holds an e4m3 code of its 2^8-fold in bits
+//        7-13 (and the sign), subnormals included, so both pieces come from
+//        integer operations on pairs of fp16: the conversion instructions
+//        share the unit that exp2 needs (a block took 2300 cycles with them).
 //
 // Work: the tokens' blocks of 128 slots form one sequence, cut into equal
 // ranges; a CTA takes one range for one group of up to 64 heads, so a lone
@@ -27,19 +31,20 @@
 // and a second kernel joins them.  The two head groups of a token run side by
 // side in neighbouring CTAs, so its rows come from HBM once.
 //
-// Per block (D = 512), 288 threads, one CTA per SM:
-//   gather (warps 5-8)   slot -> page -> row, and the rows by 16-byte cp.async
+// Per block (D = 512), 512 threads, one CTA per SM:
+//   gather (warps 12-15) slot -> page -> row, and the rows by 16-byte cp.async
 //                        into a 128-byte-swizzled tile [D/128][128 slots][128],
 //                        three tiles in a ring, a warp's 32 rows freed and
 //                        refilled on their own; the slots' scale factors;
-//   MMA (warp 4)         S = Q.K^T: M = 128 (64 heads x 2 pieces, A in TMEM),
+//   MMA (warp 8)         S = Q.K^T: M = 128 (64 heads x 2 pieces, A in TMEM),
 //                        N = 128 slots; O^T += V^T.P^T: M = 128 of D (A: the
-//                        same tile read MN-major), N = 64 heads, K = 128 slots,
-//                        for both pieces of P;
-//   softmax (warps 0-3)  two lanes per head (piece hi / lo of its row of S,
-//                        then slots 0-63 / 64-127): weights, their two pieces
-//                        to shared memory, Q's pieces into TMEM at the start of
-//                        a token and O^T out of it at the end.
+//                        same tile read MN-major, kept in the collector for
+//                        the second piece), N = 64 heads, K = 128 slots, for
+//                        both pieces of P;
+//   softmax (warps 0-7)  a warp reads 16 heads x 64 slots of S, four lanes per
+//                        head, both pieces of a row in one lane; weights, their
+//                        two pieces to shared memory, Q's pieces into TMEM at
+//                        the start of a token and O^T out of it at the end.
 // TMEM: S 128 columns, O^T D/2, Q D/4.
 #include <cuda_runtime.h>
 
@@ -55,11 +60,16 @@ namespace {
 
 constexpr int kBlk = 128;                 // slots per block
 constexpr int kHeads = 64;                // heads per CTA
-constexpr int kThreads = 288;
-constexpr int kSoftmaxThreads = 128;
-constexpr int kMmaWarp = 4, kGatherWarp0 = 5;
-constexpr float kShift = 6.f;             // weights are 2^6 at the running maximum
+constexpr int kThreads = 512;
+constexpr int kSoftmaxThreads = 256;
+constexpr int kMmaWarp = 8, kGatherWarp0 = 12;
+// Registers per thread of the softmax warpgroups and of the other two: their
+// sum is what the block is launched with (128 a thread).
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
+static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs <= 512, "registers of the launch");
+constexpr float kShift = 2.f;             // weights are 2^-2 at the running maximum
 constexpr float kLag = 2.75f;             // how far the maximum may lag behind
+constexpr float kCodeUnit = 0x1p-8f;      // what the tensor core's P counts
 
 template <int D>
 struct PagedLayout {
@@ -68,14 +78,19 @@ struct PagedLayout {
   static constexpr uint32_t kStageBytes = kChunks * kChunkBytes;
   static constexpr int kStages = D == 512 ? 3 : 6;
   static constexpr uint32_t kPieceBytes = kHeads * 128;      // one piece of P^T: 64 heads x 128 slots
-  static constexpr uint32_t kQStage = 32 * 64;               // per warp: 32 rows x 64 bytes
-  static constexpr int kMeta = 132;                          // floats per array (halves 16 bytes apart)
+  static constexpr uint32_t kQStage = 32 * 64;               // per softmax warp, in P's place: 32 rows x 64 bytes
+  static_assert(8 * kQStage <= 2 * kPieceBytes, "Q staging fits P");
+  // Per stage and slot pair (a0, a1, c0, c1), then the r of all slots, two
+  // pairs of one lane together (meta_at, rec_at).
+  static constexpr int kMeta = 4 * kBlk / 2 + kBlk;          // floats
   static constexpr uint32_t kOffP = kStages * kStageBytes;
-  static constexpr uint32_t kOffQ = kOffP + 2 * kPieceBytes;
-  static constexpr uint32_t kOffA = kOffQ + 4 * kQStage;     // [kStages][3][kMeta]: a, c, r
-  static constexpr uint32_t kOffFlags = kOffA + kStages * 3 * kMeta * 4;  // [kStages]
+  static constexpr uint32_t kOffA = kOffP + 2 * kPieceBytes; // [kStages][kMeta]: a, c, r
+  static constexpr uint32_t kOffFlags = kOffA + kStages * kMeta * 4;  // [kStages]
   static constexpr uint32_t kOffHead = (kOffFlags + kStages * 4 + 15) & ~15u;  // float [64]
-  static constexpr uint32_t kOffBar = kOffHead + kHeads * 4;
+  static constexpr uint32_t kOffMax = kOffHead + kHeads * 4;   // float [2][2][64]
+  static constexpr uint32_t kOffSum = kOffMax + 4 * kHeads * 4;  // float [2][64]
+  static constexpr uint32_t kOffEnd = kOffSum + 2 * kHeads * 4;  // float [64]
+  static constexpr uint32_t kOffBar = kOffEnd + kHeads * 4;
   static constexpr int kBarFull = 0;                         // [kStages]
   static constexpr int kBarEmpty = kBarFull + kStages;       // [kStages][4], a gather warp's rows
   static constexpr int kBarSFull = kBarEmpty + 4 * kStages;
@@ -87,7 +102,8 @@ struct PagedLayout {
   static constexpr int kNumBars = kBarDrain + 1;
   static constexpr uint32_t kOffCtl = kOffBar + 8 * kNumBars;  // TMEM base, abort flag
   static constexpr uint32_t kOffRange = kOffCtl + 8;         // range of the CTA, scan space
-  static constexpr uint32_t kSmem = kOffRange + 160 + 1024;  // + alignment
+  static constexpr uint32_t kSmem = kOffRange + 192 + 1024;  // + alignment
+  static_assert(kOffRange % 8 == 0, "alignment");
   static_assert(kSmem <= 232448, "shared memory budget");
   static constexpr uint32_t kTmemS = 0, kTmemO = 128;
   static constexpr uint32_t kTmemQ = kTmemO + kChunks * kHeads;
@@ -132,6 +148,117 @@ __device__ __forceinline__ int blocks_of(const PagedFwdParams& p, int t) {
   return max(1, (slots_of(p, t, req, __ldg(p.seq_lens + req)) + kBlk - 1) / kBlk);
 }
 
+// The two e4m3 pieces of 2^8 w for four weights 0 <= w <= 1.6875: hi the
+// nearest code (halves up), lo that of the rest.
+__device__ __forceinline__ void split_e4m3x4(float2 w01, float2 w23, uint32_t& hi, uint32_t& lo) {
+  const __half2 a = __floats2half2_rn(w01.x, w01.y), b = __floats2half2_rn(w23.x, w23.y);
+  const uint32_t ra = *reinterpret_cast<const uint32_t*>(&a) + 0x00400040u;
+  const uint32_t rb = *reinterpret_cast<const uint32_t*>(&b) + 0x00400040u;
+  hi = __byte_perm(ra << 1, rb << 1, 0x7531);
+  const uint32_t ka = ra & 0xff80ff80u, kb = rb & 0xff80ff80u;
+  const __half2 da = __hsub2(a, *reinterpret_cast<const __half2*>(&ka));
+  const __half2 db = __hsub2(b, *reinterpret_cast<const __half2*>(&kb));
+  const uint32_t sa = *reinterpret_cast<const uint32_t*>(&da) + 0x00400040u;
+  const uint32_t sb = *reinterpret_cast<const uint32_t*>(&db) + 0x00400040u;
+  // The sign next to the code (bit 14 is free: the values are below 2).
+  lo = __byte_perm((sa | ((sa >> 1) & 0x40004000u)) << 1, (sb | ((sb >> 1) & 0x40004000u)) << 1, 0x7531);
+}
+
+// Where slot n's factors a and c (+ 2) lie among a stage's floats, and its r:
+// the softmax lane q of a quad takes the slot pairs 8j + 2q, two j at a time.
+__device__ __forceinline__ int meta_at(int n) { return (n >> 1) * 4 + (n & 1); }
+__device__ __forceinline__ int rec_at(int n) {
+  return 2 * kBlk + (n >> 4) * 16 + ((n >> 1) & 3) * 4 + ((n >> 3) & 1) * 2 + (n & 1);
+}
+
+// Q of a token, heads h0.. (`heads` of them, zeros behind), by the eight softmax
+// warps: a warp takes 16 heads and half of D, two heads at a time (four columns
+// per lane of each 64-column piece).  fetch() loads it into registers; place()
+// writes both pieces of every row into TMEM lanes (of 16 lanes, 0-7 the hi
+// pieces of eight heads, 8-15 their lo pieces) once the MMAs that read the Q and
+// the P before are done, and returns 2^-k of the two heads whose S the lane
+// reads (NaN where a row is not finite).
+template <int D>
+struct QLoader {
+  using L = PagedLayout<D>;
+  static constexpr int kC = D < 128 ? 1 : D / 128;       // 64-column pieces per warp
+  uint2 v[8][kC];
+
+  __device__ __forceinline__ void fetch(const PagedFwdParams& p, int t, int h0, int heads, int quarter, int half,
+                                        int lane) {
+    const bool mine = D >= 128 || half == 0;             // (D = 64 is one piece)
+    const __nv_bfloat16* q0 = p.q + (static_cast<int64_t>(t) * p.H + h0) * D + half * kC * 64 + (lane & 15) * 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int h = 16 * quarter + 2 * i + (lane >> 4);
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+        v[i][c] = mine && h < heads ? __ldg(reinterpret_cast<const uint2*>(q0 + static_cast<int64_t>(h) * D + c * 64))
+                                    : make_uint2(0, 0);
+    }
+  }
+
+  __device__ __forceinline__ float2 place(uint32_t base, uint8_t* smem, uint32_t tmem, int quarter, int half,
+                                         int lane) {
+    const int sub = lane >> 4, l16 = lane & 15;
+    uint32_t* head_top = reinterpret_cast<uint32_t*>(smem + L::kOffMax);  // [2][64] largest magnitudes
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t m = 0;                                    // bf16 bit patterns order like values
+#pragma unroll
+      for (int c = 0; c < kC; ++c) m = __vmaxu2(m, __vmaxu2(v[i][c].x & 0x7fff7fffu, v[i][c].y & 0x7fff7fffu));
+      m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+      if (l16 == 0) head_top[half * kHeads + 16 * quarter + 2 * i + sub] = m;
+    }
+    bar_sync(4 + quarter, 64);
+    auto top_of = [&](int h) { return max(head_top[h], head_top[kHeads + h]); };
+    // floor(log2) of the largest magnitude, not below -100.
+    auto exponent = [](uint32_t m) { return max(static_cast<int>(m >> 7) - 127, -100); };
+    const uint32_t stage = base + L::kOffP + static_cast<uint32_t>(4 * half + quarter) * L::kQStage;
+    if (D >= 128 || half == 0) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = pow2f(7 - exponent(min(top_of(16 * quarter + 2 * i + sub), 0x7f7fu)));
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float x0 = __uint_as_float(v[i][c].x << 16) * f[i], x1 = __uint_as_float(v[i][c].x & 0xffff0000u) * f[i];
+          const float x2 = __uint_as_float(v[i][c].y << 16) * f[i], x3 = __uint_as_float(v[i][c].y & 0xffff0000u) * f[i];
+          const uint16_t a = e4m3x2(x0, x1), d = e4m3x2(x2, x3);
+          const float2 ra = e4m3x2_value(a), rd = e4m3x2_value(d);
+          const uint32_t hi = a | (static_cast<uint32_t>(d) << 16);
+          const uint32_t lo = e4m3x2((x0 - ra.x) * 32.f, (x1 - ra.y) * 32.f) |
+                              (static_cast<uint32_t>(e4m3x2((x2 - rd.x) * 32.f, (x3 - rd.y) * 32.f)) << 16);
+          const int hh = 2 * i + sub;                    // of the warp's 16 heads
+          const uint32_t r = static_cast<uint32_t>(hh + (hh & 8));  // rows r, r + 8
+          const uint32_t at = stage + r * 64u + ((static_cast<uint32_t>(l16 >> 2) ^ ((r >> 1) & 3u)) << 4) + (l16 & 3) * 4;
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(hi) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 512u), "r"(lo) : "memory");
+        }
+        __syncwarp();
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 x = *reinterpret_cast<const uint4*>(smem + (stage - base) + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4));
+          w[4 * k] = x.x;
+          w[4 * k + 1] = x.y;
+          w[4 * k + 2] = x.z;
+          w[4 * k + 3] = x.w;
+        }
+        tmem_st16u(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + L::kTmemQ + (half * kC + c) * 16, w);
+        __syncwarp();
+      }
+    }
+    const uint32_t t0 = top_of(16 * quarter + (lane >> 2)), t1 = top_of(16 * quarter + 8 + (lane >> 2));
+    bar_sync(4 + quarter, 64);                           // head_top's place is head_max's next
+    auto scale = [&](uint32_t m) { return m >= 0x7f80u ? __uint_as_float(0x7fffffffu) : pow2f(exponent(m) - 7); };
+    return make_float2(scale(t0), scale(t1));
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const PagedFwdParams p) {
   using L = PagedLayout<D>;
@@ -150,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffCtl + 4);
   const WaitCtl ctl{abort_flag, p.status, p.limit_ns};
   Range* range = reinterpret_cast<Range*>(smem + L::kOffRange);
-  int64_t* warp_sum = reinterpret_cast<int64_t*>(smem + L::kOffRange + 16);  // [9]
-  int* end_tok = reinterpret_cast<int*>(smem + L::kOffRange + 16 + 72);      // token, its end inside
+  int64_t* warp_sum = reinterpret_cast<int64_t*>(smem + L::kOffRange + 16);  // [16]
+  int* end_tok = reinterpret_cast<int*>(smem + L::kOffRange + 16 + 128);     // token, its end, its begin
 
   if (tid == 0) {
     for (int i = 0; i < L::kStages; ++i) mbar_init(bar(L::kBarFull + i), 256);
@@ -196,7 +323,10 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       if (w < warp) before += warp_sum[w];
       total += warp_sum[w];
     }
-    const int64_t begin = total * part / parts, end = total * (part + 1) / parts;
+    // Equal ranges, the first total mod parts of them one block longer.
+    const int64_t each = total / parts;
+    const int extra = static_cast<int>(total - each * parts);
+    const int64_t begin = each * part + min(part, extra), end = begin + each + (part < extra ? 1 : 0);
     if (begin < end) {
       if (before <= begin && begin < before + mine) {
         int64_t at = before;
@@ -240,90 +370,120 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
   }
 
   if (rg.count > 0 && warp >= kGatherWarp0) {
+    reg_dealloc<kOtherRegs>();
     // ------------------------------------------------------------ gather
+    // Looking a slot up takes three loads, one after another: while the rows
+    // of one block are copied, the next block's indices and then its pages
+    // arrive.
     const int pw = warp - kGatherWarp0;
-    const int my = 32 * pw + lane;                       // this thread's slot of the block
-    const int meta = my + (my >= 64 ? 4 : 0);
-    int64_t left = rg.count;
-    int e = 0;                                           // ring entries so far
-    bool ok = *abort_flag == 0;
-    for (int t = rg.tok, b = rg.off; ok && left > 0; ++t, b = 0) {
-      const int nb = blocks_of(p, t);
-      if (nb == 0) continue;
-      const int req = __ldg(p.token_req + t);
-      const int len = __ldg(p.seq_lens + req);
-      const int n = slots_of(p, t, req, len);
-      const int32_t* idx_row = p.idx ? p.idx + static_cast<int64_t>(t) * p.topk : nullptr;
-      const int32_t* tab = p.table + static_cast<int64_t>(req) * p.max_pages;
-      const int stop = static_cast<int>(min(static_cast<int64_t>(nb), b + left));
-      left -= stop - b;
-      int flags = kFirst;
-      for (; ok && b < stop; ++b) {
-        const bool last = b + 1 == stop;
-        int pos = -1;                                    // this slot's position, -1: masked
-        if (idx_row) {
-          // Every warp looks at all 128 slots: a block with none left is
-          // skipped (but for the last, which carries the token's end).
-          unsigned any = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int j = b * kBlk + 32 * k + lane;
-            const int i = j < n ? __ldg(idx_row + j) : -1;
-            const bool in = i >= 0 && i < len;
-            any |= __ballot_sync(0xffffffffu, in);
-            if (k == pw && in) pos = i;
-          }
-          if (any == 0 && !last) continue;
-        } else {
-          const int j = b * kBlk + my;
-          if (j < n) pos = j;
-        }
-        int row = -1;
-        float s = 1.f;
-        if (pos >= 0) {
-          const int col = pos >> p.page_shift;
-          const int pg = col < p.max_pages ? __ldg(tab + col) : -1;
-          if (static_cast<unsigned>(pg) < static_cast<unsigned>(p.n_pages)) {
-            row = (pg << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
-            s = __ldg(p.scales + pg);
-          }
-        }
-        const int st = e % L::kStages;
-        if (e >= L::kStages) {
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarEmpty + 4 * st + pw), ((e / L::kStages) - 1) & 1, ctl));
-          if (!ok) break;
-        }
-        // y = S a + c, l += w r: a masked slot's row is zero, its c -inf.
-        float* m = reinterpret_cast<float*>(smem + L::kOffA) + st * 3 * L::kMeta + meta;
-        m[0] = row >= 0 ? s * p.scale_log2 : 0.f;
-        m[L::kMeta] = row >= 0 ? log2f(s) : -INFINITY;
-        m[2 * L::kMeta] = row >= 0 ? 1.f / s : 0.f;
-        if (my == 0)
-          reinterpret_cast<int*>(smem + L::kOffFlags)[st] =
-              flags | (last ? kLast : 0) | (last && left == 0 ? kFinal : 0);
-        flags = 0;
-        const uint32_t tile = base + static_cast<uint32_t>(st) * L::kStageBytes;
-        constexpr int kLpr = D / 16;                     // lanes per row
-        constexpr int kRpi = 32 / kLpr;                  // rows per warp instruction
-        const int sub = lane / kLpr, cc = lane % kLpr;
-        const uint32_t col = static_cast<uint32_t>(cc / 8) * L::kChunkBytes;
-#pragma unroll 8
-        for (int k = 0; k < 32 / kRpi; ++k) {
-          const int rw = k * kRpi + sub;
-          const int rr = __shfl_sync(0xffffffffu, row, rw);
-          const uint32_t at = static_cast<uint32_t>(32 * pw + rw);
-          cp_async_16_or_zero(tile + col + at * 128u + ((static_cast<uint32_t>(cc % 8) ^ (at & 7u)) << 4),
-                              p.cache + static_cast<int64_t>(max(rr, 0)) * D + cc * 16, rr >= 0);
-        }
-        cp_async_arrive_noinc(bar(L::kBarFull + st));    // once the copies have landed
-        mbar_arrive(bar(L::kBarFull + st));              // releases the factors
-        ++e;
+    const int my = 32 * pw + lane;                       // this thread's slot of a block
+    int64_t left = rg.count;                             // blocks behind the current token's
+    int t = rg.tok - 1, b = 0, stop = 0, n = 0, len = 0;
+    const int32_t *idx_row = nullptr, *tab = nullptr;
+    bool fresh = true;                                   // no block of this token yet
+    int idx[4];                                          // of slots 32 k + lane
+    // Goes to the next block and asks for its indices.
+    auto ask = [&] {
+      if (++b >= stop) {
+        int nb;
+        do nb = blocks_of(p, ++t);
+        while (nb == 0);
+        const int req = __ldg(p.token_req + t);
+        b = t == rg.tok ? rg.off : 0;
+        stop = static_cast<int>(min(static_cast<int64_t>(nb), b + left));
+        left -= stop - b;
+        len = __ldg(p.seq_lens + req);
+        n = slots_of(p, t, req, len);
+        tab = p.table + static_cast<int64_t>(req) * p.max_pages;
+        idx_row = p.idx ? p.idx + static_cast<int64_t>(t) * p.topk : nullptr;
+        fresh = true;
       }
+      if (idx_row)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int j = b * kBlk + 32 * k + lane;
+          idx[k] = j < n ? __ldg(idx_row + j) : -1;
+        }
+    };
+    // This slot's position in its page and its page (-1: masked); the block's
+    // flags.  A block without any slot left is passed over, but for the last,
+    // which carries the token's end.
+    int in_page = 0, page = -1, flags = 0;
+    auto look = [&] {
+      int pos = -1;
+      while (true) {
+        if (!idx_row) {
+          if (b * kBlk + my < n) pos = b * kBlk + my;
+          break;
+        }
+        unsigned any = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool in = idx[k] >= 0 && idx[k] < len;
+          any |= __ballot_sync(0xffffffffu, in);
+          if (k == pw && in) pos = idx[k];
+        }
+        if (any != 0 || b + 1 == stop) break;
+        ask();
+      }
+      const bool last = b + 1 == stop;
+      flags = (fresh ? kFirst : 0) | (last ? kLast : 0) | (last && left == 0 ? kFinal : 0);
+      fresh = false;
+      const int col = pos >> p.page_shift;
+      in_page = pos & ((1 << p.page_shift) - 1);
+      page = pos >= 0 && col < p.max_pages ? __ldg(tab + col) : -1;
+    };
+    ask();
+    look();
+    for (int e = 0;; ++e) {
+      const bool live = static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages);
+      const int row = live ? (page << p.page_shift) + in_page : 0;
+      const float s = live ? __ldg(p.scales + page) : 1.f;
+      const unsigned mask = __ballot_sync(0xffffffffu, live);
+      const int now = flags;
+      if (!(now & kFinal)) ask();
+      const int st = e % L::kStages;
+      if (e >= L::kStages) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(L::kBarEmpty + 4 * st + pw), ((e / L::kStages) - 1) & 1, ctl))) break;
+      } else if (!__all_sync(0xffffffffu, *abort_flag == 0)) {
+        break;
+      }
+      const uint32_t tile = base + static_cast<uint32_t>(st) * L::kStageBytes;
+      constexpr int kLpr = D / 16;                       // lanes per row
+      constexpr int kRpi = 32 / kLpr;                    // rows per warp instruction
+      const int sub = lane / kLpr, cc = lane % kLpr;
+      const uint32_t col = static_cast<uint32_t>(cc / 8) * L::kChunkBytes + static_cast<uint32_t>(32 * pw + sub) * 128u;
+      const uint8_t* src = p.cache + cc * 16;
+      auto copy = [&](int k) {                           // rows k kRpi + sub of the warp's 32
+        const int rw = k * kRpi + sub;
+        const int rr = __shfl_sync(0xffffffffu, row, rw);
+        cp_async_16_or_zero(tile + col + static_cast<uint32_t>(k * kRpi) * 128u +
+                                ((static_cast<uint32_t>(cc % 8) ^ (static_cast<uint32_t>(rw) & 7u)) << 4),
+                            src + static_cast<int64_t>(rr) * D, (mask >> rw) & 1u);
+      };
+#pragma unroll
+      for (int k = 0; k < 16 / kRpi; ++k) copy(k);
+      if (!(now & kFinal)) look();
+#pragma unroll
+      for (int k = 16 / kRpi; k < 32 / kRpi; ++k) copy(k);
+      // y = S a + c, l += w r: a masked slot's row is zero, its c -inf.
+      float* m = reinterpret_cast<float*>(smem + L::kOffA) + st * L::kMeta;
+      m[meta_at(my)] = live ? s * p.scale_log2 : 0.f;
+      m[meta_at(my) + 2] = live ? log2f(s) : -INFINITY;
+      m[rec_at(my)] = live ? 1.f / s : 0.f;
+      if (my == 0) reinterpret_cast<int*>(smem + L::kOffFlags)[st] = now;
+      cp_async_arrive_noinc(bar(L::kBarFull + st));      // once the copies have landed
+      mbar_arrive(bar(L::kBarFull + st));                // releases the factors
+      if (now & kFinal) break;
     }
     cp_async_wait_all();
+  } else if (rg.count > 0 && warp > kMmaWarp) {
+    reg_dealloc<kOtherRegs>();                           // (the MMA warp's group)
   } else if (rg.count > 0 && warp == kMmaWarp) {
+    reg_dealloc<kOtherRegs>();
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    // The whole warp runs this, one lane of it issues.
+    {
       constexpr uint32_t idesc_s = idesc_e4m3_f32(128, kBlk, false);
       constexpr uint32_t idesc_o = idesc_e4m3_f32(128, kHeads, true);
       const uint64_t d_k = smem_desc(base, 16u, 1024u, kSwizzle128B);
@@ -336,35 +496,35 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
         for (int c = 0; c < D / 32; ++c)
           mma8_ts(tmem + L::kTmemS, tmem + L::kTmemQ + c * 8,
                   k + (((c / 4) * L::kChunkBytes + (c % 4) * 32u) >> 4), idesc_s, c != 0 ? 1u : 0u);
-        mma_commit(bar(L::kBarSFull));
+        mma_commit_elect(bar(L::kBarSFull));
       };
       auto issue_o = [&](int st, bool first) {
         const uint64_t v = d_v + ((static_cast<uint32_t>(st) * L::kStageBytes) >> 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
 #pragma unroll
-          for (int c = 0; c < L::kChunks; ++c)
-#pragma unroll
-            for (int piece = 0; piece < 2; ++piece)
-              mma8_ss(tmem + L::kTmemO + c * kHeads, v + ((c * L::kChunkBytes + k * 4096u) >> 4),
-                      d_p + ((piece * L::kPieceBytes + k * 32u) >> 4), idesc_o,
-                      (!first || k > 0 || piece > 0) ? 1u : 0u);
-          mma_commit(bar(L::kBarEmpty + 4 * st + k));
+          for (int c = 0; c < L::kChunks; ++c) {
+            const uint64_t ad = v + ((c * L::kChunkBytes + k * 4096u) >> 4);
+            const uint64_t bd = d_p + ((k * 32u) >> 4);
+            mma8_ss_keep(tmem + L::kTmemO + c * kHeads, ad, bd, idesc_o, (!first || k > 0) ? 1u : 0u);
+            mma8_ss_again(tmem + L::kTmemO + c * kHeads, ad, bd + (L::kPieceBytes >> 4), idesc_o, 1u);
+          }
+          mma_commit_elect(bar(L::kBarEmpty + 4 * st + k));
         }
-        mma_commit(bar(L::kBarPDone));
+        mma_commit_elect(bar(L::kBarPDone));
       };
       bool ok = *abort_flag == 0;
       int seg = 0, before = 0;                           // tokens so far, the previous entry's flags
       // O of entry e, once its P is written.
       auto do_o = [&](int e, int flags) {
-        ok = mbar_wait(bar(L::kBarPFull), e & 1, ctl);
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarPFull), e & 1, ctl));
         if (!ok) return;
         tc_fence_after();
         issue_o(e % L::kStages, (flags & kFirst) != 0);
       };
       for (int e = 0; ok; ++e) {
         const int st = e % L::kStages;
-        ok = mbar_wait(bar(L::kBarFull + st), (e / L::kStages) & 1, ctl);
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarFull + st), (e / L::kStages) & 1, ctl));
         if (!ok) break;
         const int flags = flags_of[st];
         const bool first = (flags & kFirst) != 0;
@@ -372,16 +532,16 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
         // the token before is finished: that one's last O goes first.
         if (first) {
           if (e > 0) do_o(e - 1, before);
-          if (ok) ok = mbar_wait(bar(L::kBarQFull), seg & 1, ctl);
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQFull), seg & 1, ctl));
           ++seg;
         }
-        if (ok && e > 0) ok = mbar_wait(bar(L::kBarSFree), (e - 1) & 1, ctl);
+        if (ok && e > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarSFree), (e - 1) & 1, ctl));
         if (!ok) break;
         fence_proxy_async_smem();                        // rows written by cp.async -> tensor core
         tc_fence_after();
         issue_s(st);
         if (e == 0 && static_cast<int>(blockIdx.x) == p.stall_cta) {  // test hook only
-          ok = stall_until_limit(ctl);
+          ok = __any_sync(0xffffffffu, stall_until_limit(ctl));
           break;
         }
         if (!first) do_o(e - 1, before);
@@ -391,110 +551,48 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
           break;
         }
       }
-      mma_commit(bar(L::kBarDrain));
+      mma_commit_elect(bar(L::kBarDrain));
       mbar_wait_drain(bar(L::kBarDrain), 0);
     }
     __syncwarp();
   } else if (rg.count > 0) {
+    reg_alloc<kSoftmaxRegs>();
     // ------------------------------------------------------------ softmax
-    // A failed wait sets `bad`; the four warps leave together at the next
-    // vote, so that none waits at a barrier that another has left.
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const int hl = 16 * warp + (lane >> 1);              // this lane's head within the CTA
-    const bool odd = lane & 1;
+    // Warps w and w + 4 own the TMEM lanes of quarter w: 16 heads, half of the
+    // block's slots each.  A failed wait sets `bad`; the eight warps leave
+    // together at the next vote, so that none waits at a barrier that another
+    // has left.
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const int hq = 16 * quarter + (lane >> 2);           // this lane's heads: hq, hq + 8
+    const int quad = lane & 3;                           // its slots: pairs 8 j + 2 quad
+    const bool lead = quad == 0;
+    // Byte selectors of the exchange between lanes of a pair (below).
+    const uint32_t sel_send = (lane & 1) ? 0x5410u : 0x7632u;
+    const uint32_t sel_hi = (lane & 1) ? 0x3254u : 0x5410u, sel_lo = (lane & 1) ? 0x3276u : 0x7610u;
     float* head_f = reinterpret_cast<float*>(smem + L::kOffHead);
+    float* head_max = reinterpret_cast<float*>(smem + L::kOffMax);
+    float* head_sum = reinterpret_cast<float*>(smem + L::kOffSum);  // at a token's end: l of each
+    float* head_end = reinterpret_cast<float*>(smem + L::kOffEnd);  // half, and m
     const volatile int* flags_of = reinterpret_cast<const volatile int*>(smem + L::kOffFlags);
     bool bad = *abort_flag != 0;
     int64_t left = rg.count;
     int e = 0;
     bool run = true;
-    for (int t = rg.tok, b = rg.off; run && left > 0; ++t, b = 0) {
-      const int nb = blocks_of(p, t);
-      if (nb == 0) continue;
+    // The CTA's tokens, or parts of tokens, one after another.
+    int t = rg.tok, b = rg.off, nb = blocks_of(p, t);
+    QLoader<D> q;
+    q.fetch(p, t, h0, heads, quarter, half, lane);
+    float2 rs = q.place(base, smem, tmem, quarter, half, lane);
+    tc_fence_before();
+    mbar_arrive(bar(L::kBarQFull));
+    while (true) {
       const int stop = static_cast<int>(min(static_cast<int64_t>(nb), b + left));
       const bool whole = b == 0 && stop == nb;
       const int slot = b == 0 ? 1 : 0;                   // of the CTA's two workspace parts
       left -= stop - b;
 
-      // Q: half-warps take heads in turn, 4 elements per lane of each
-      // 64-column piece; then both pieces of every row through shared memory
-      // into the row's TMEM lane (row 2h: hi, row 2h + 1: lo).
-      float rs;                                          // 2^-k of this lane's head
-      {
-        constexpr int kC = D / 64;
-        uint2 v[8][kC];
-        const int half = lane >> 4, l16 = lane & 15;
-        const __nv_bfloat16* q0 = p.q + (static_cast<int64_t>(t) * p.H + h0) * D + l16 * 4;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int h = 16 * warp + 2 * i + half;
-#pragma unroll
-          for (int c = 0; c < kC; ++c)
-            v[i][c] = h < heads ? __ldg(reinterpret_cast<const uint2*>(q0 + static_cast<int64_t>(h) * D + c * 64))
-                                : make_uint2(0, 0);
-        }
-        uint32_t top[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            m = max(m, max(v[i][c].x & 0x7fffu, (v[i][c].x >> 16) & 0x7fffu));
-            m = max(m, max(v[i][c].y & 0x7fffu, (v[i][c].y >> 16) & 0x7fffu));
-          }
-#pragma unroll
-          for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-          top[i] = m;
-        }
-        uint32_t mine = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t x = __shfl_sync(0xffffffffu, top[i], ((lane >> 1) & 1) * 16);
-          if ((lane >> 2) == i) mine = x;
-        }
-        // floor(log2) of the largest magnitude (bf16 bits), not below -100.
-        auto exponent = [](uint32_t m) { return max(static_cast<int>(m >> 7) - 127, -100); };
-        rs = mine >= 0x7f80u ? __uint_as_float(0x7fffffffu) : pow2f(exponent(mine) - 7);
-        const uint32_t stage = base + L::kOffQ + static_cast<uint32_t>(warp) * L::kQStage;
-        // The previous token's last S is done (its block was read above), so
-        // Q's columns are free.
-#pragma unroll
-        for (int c = 0; c < kC; ++c) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float f = pow2f(7 - exponent(min(top[i], 0x7f7fu)));
-            const float x0 = __uint_as_float(v[i][c].x << 16) * f, x1 = __uint_as_float(v[i][c].x & 0xffff0000u) * f;
-            const float x2 = __uint_as_float(v[i][c].y << 16) * f, x3 = __uint_as_float(v[i][c].y & 0xffff0000u) * f;
-            const uint16_t a = e4m3x2(x0, x1), d = e4m3x2(x2, x3);
-            const float2 ra = e4m3x2_value(a), rd = e4m3x2_value(d);
-            const uint32_t hi = a | (static_cast<uint32_t>(d) << 16);
-            const uint32_t lo = e4m3x2((x0 - ra.x) * 32.f, (x1 - ra.y) * 32.f) |
-                                (static_cast<uint32_t>(e4m3x2((x2 - rd.x) * 32.f, (x3 - rd.y) * 32.f)) << 16);
-            const uint32_t r = static_cast<uint32_t>(2 * (2 * i + half));  // rows r, r + 1
-            const uint32_t at = stage + r * 64u + ((static_cast<uint32_t>(l16 >> 2) ^ ((r >> 1) & 3u)) << 4) + (l16 & 3) * 4;
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(hi) : "memory");
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 64u), "r"(lo) : "memory");
-          }
-          __syncwarp();
-          uint32_t w[16];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 x = *reinterpret_cast<const uint4*>(
-                smem + L::kOffQ + warp * L::kQStage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4));
-            w[4 * k] = x.x;
-            w[4 * k + 1] = x.y;
-            w[4 * k + 2] = x.z;
-            w[4 * k + 3] = x.w;
-          }
-          tmem_st16u(tmem + lanes + L::kTmemQ + c * 16, w);
-          __syncwarp();
-        }
-        tc_fence_before();
-        mbar_arrive(bar(L::kBarQFull));
-      }
-
-      const float f_own = odd ? rs * 0.03125f : rs, f_peer = odd ? rs : rs * 0.03125f;
-      float m = -INFINITY, l = 0.f;
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
       for (bool last = false; run && !last; ++e) {
         const int st = e % L::kStages;
         if (!mbar_wait(bar(L::kBarSFull), e & 1, ctl)) bad = true;
@@ -504,88 +602,106 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
         tc_fence_after();
         const int flags = flags_of[st];
         last = (flags & kLast) != 0;
-        const float* a = reinterpret_cast<const float*>(smem + L::kOffA) + st * 3 * L::kMeta + (odd ? 68 : 0);
-        float y[64];
-        float mx = -INFINITY;
+        const float* meta = reinterpret_cast<const float*>(smem + L::kOffA) + st * L::kMeta;
+        float2 y[2][8];                                  // per head, of its slot pairs
+        float mx[2];
+        {
+          float x[2][32];
+          const uint32_t s0 = tmem + lanes + L::kTmemS + half * 64;
+          tmem_ld16x64x2(s0, s0 + (16u << 16), x[0], x[1]);
+          tc_fence_before();
+          mbar_arrive(bar(L::kBarSFree));
+          const float2 fh[2] = {make_float2(rs.x, rs.x), make_float2(rs.y, rs.y)};
+          const float2 fl[2] = {make_float2(rs.x * 0.03125f, rs.x * 0.03125f), make_float2(rs.y * 0.03125f, rs.y * 0.03125f)};
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float x0[32], x1[32];
-          const uint32_t s0 = tmem + lanes + L::kTmemS + g * 32;
-          tmem_ld32x2(s0, s0 + 64, x0, x1);
-          if (g == 1) {
-            tc_fence_before();
-            mbar_arrive(bar(L::kBarSFree));
-          }
+          for (int j = 0; j < 8; ++j) {
+            const float4 ac = *reinterpret_cast<const float4*>(meta + (32 * half + 4 * j + quad) * 4);
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 aj = *reinterpret_cast<const float4*>(a + g * 32 + i);
-            const float4 cj = *reinterpret_cast<const float4*>(a + L::kMeta + g * 32 + i);
-            const float as[4] = {aj.x, aj.y, aj.z, aj.w}, cs[4] = {cj.x, cj.y, cj.z, cj.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float own = odd ? x1[i + k] : x0[i + k], send = odd ? x0[i + k] : x1[i + k];
-              const float peer = __shfl_xor_sync(0xffffffffu, send, 1);
-              y[g * 32 + i + k] = fmaf(fmaf(own, f_own, peer * f_peer), as[k], cs[k]);
-              mx = fmaxf(mx, y[g * 32 + i + k]);
+            for (int g = 0; g < 2; ++g) {
+              const float2 hi = make_float2(x[g][4 * j], x[g][4 * j + 1]), lo = make_float2(x[g][4 * j + 2], x[g][4 * j + 3]);
+              y[g][j] = fma2(fma2(hi, fh[g], mul2(lo, fl[g])), make_float2(ac.x, ac.y), make_float2(ac.z, ac.w));
             }
           }
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            mx[g] = fmaxf(y[g][0].x, y[g][0].y);
+#pragma unroll
+            for (int j = 1; j < 8; ++j) mx[g] = fmax3f(mx[g], y[g][j].x, y[g][j].y);
+            mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], 1));
+            mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], 2));
+          }
         }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         const bool first = (flags & kFirst) != 0;
-        const bool grow = !first && mx > m + kLag;
-        const bool any = bar_any(1, kSoftmaxThreads, grow || bad);
+        float* peers = head_max + (e & 1) * 2 * kHeads;  // both warps' maxima of this block
+        if (lead) {
+          peers[half * kHeads + hq] = mx[0];
+          peers[half * kHeads + hq + 8] = mx[1];
+        }
+        const bool up = !first && (mx[0] > m[0] + kLag || mx[1] > m[1] + kLag);
+        const bool any = bar_any(1, kSoftmaxThreads, up || bad);
         if (any && bar_any(1, kSoftmaxThreads, bad)) {
           run = false;
           break;
+        }
+        if (first || any) {
+          mx[0] = fmaxf(peers[hq], peers[kHeads + hq]);
+          mx[1] = fmaxf(peers[hq + 8], peers[kHeads + hq + 8]);
         }
         // P and O are this thread's once the previous block's products are done.
         if (e > 0 && !mbar_wait(bar(L::kBarPDone), (e - 1) & 1, ctl)) bad = true;
         __syncwarp();
         if (any) {                                       // some head's O has to be rescaled
           tc_fence_after();
-          const float f = grow ? fast_exp2(m - mx) : 1.f;
-          if (grow) {
-            m = mx;
-            l *= f;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const bool grow = !first && mx[g] > m[g] + kLag;
+            const float f = grow ? fast_exp2(m[g] - mx[g]) : 1.f;
+            if (grow) {
+              m[g] = mx[g];
+              l[g] *= f;
+            }
+            if (lead && half == 0) head_f[hq + 8 * g] = f;
           }
-          if (!odd) head_f[hl] = f;
           bar_sync(1, kSoftmaxThreads);
 #pragma unroll 1
-          for (int c = 0; c < 2 * L::kChunks; ++c) {
+          for (int c = 0; c < L::kChunks; ++c) {
             float o[32];
-            const uint32_t at = tmem + lanes + L::kTmemO + c * 32;
+            const uint32_t at = tmem + lanes + L::kTmemO + c * kHeads + half * 32;
             tmem_ld32(at, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= head_f[(c & 1) * 32 + i];
+            for (int i = 0; i < 32; ++i) o[i] *= head_f[half * 32 + i];
             tmem_st32(at, o);
           }
           bar_sync(1, kSoftmaxThreads);                  // head_f is read
         }
-        if (first) m = mx;
-        const float shift = (m == -INFINITY ? 0.f : m) - kShift;
+        if (first) {
+          m[0] = mx[0];
+          m[1] = mx[1];
+        }
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {                 // 16 slots: 16 bytes of each piece
-          uint32_t hi[4], lo[4];
+        for (int j = 0; j < 8; j += 2) {
+          const float4 r = *reinterpret_cast<const float4*>(meta + 2 * kBlk + (4 * half + j / 2) * 16 + quad * 4);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 rj = *reinterpret_cast<const float4*>(a + 2 * L::kMeta + q4 * 16 + i * 4);
-            const float* yy = y + q4 * 16 + i * 4;
-            const float w0 = fast_exp2(yy[0] - shift), w1 = fast_exp2(yy[1] - shift);
-            const float w2 = fast_exp2(yy[2] - shift), w3 = fast_exp2(yy[3] - shift);
-            l = fmaf(w0, rj.x, l);
-            l = fmaf(w1, rj.y, l);
-            l = fmaf(w2, rj.z, l);
-            l = fmaf(w3, rj.w, l);
-            const __half2 u = __floats2half2_rn(w0, w1), v = __floats2half2_rn(w2, w3);
-            const uint16_t uh = e4m3x2(u), vh = e4m3x2(v);
-            hi[i] = uh | (static_cast<uint32_t>(vh) << 16);
-            lo[i] = e4m3x2(__hsub2(u, e4m3x2_half2(uh))) |
-                    (static_cast<uint32_t>(e4m3x2(__hsub2(v, e4m3x2_half2(vh)))) << 16);
+          for (int g = 0; g < 2; ++g) {
+            const float shift = (m[g] == -INFINITY ? 0.f : m[g]) + kShift;
+            const float2 w01 = make_float2(fast_exp2(y[g][j].x - shift), fast_exp2(y[g][j].y - shift));
+            const float2 w23 = make_float2(fast_exp2(y[g][j + 1].x - shift), fast_exp2(y[g][j + 1].y - shift));
+            l[g] = fmaf(w01.x, r.x, l[g]);
+            l[g] = fmaf(w01.y, r.y, l[g]);
+            l[g] = fmaf(w23.x, r.z, l[g]);
+            l[g] = fmaf(w23.y, r.w, l[g]);
+            uint32_t hi, lo;                             // codes of slots 8j + 2 quad, + 1; + 8, + 9
+            split_e4m3x4(w01, w23, hi, lo);
+            // Lanes of a pair trade, the even one for four slots in a row at
+            // 8j, the odd one at 8j + 8.
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, __byte_perm(hi, lo, sel_send), 1);
+            const int h = hq + 8 * g;
+            const uint32_t at = base + L::kOffP + static_cast<uint32_t>(h) * 128u +
+                                ((static_cast<uint32_t>(4 * half + j / 2) ^ static_cast<uint32_t>(h & 7)) << 4) +
+                                (lane & 1) * 8u + (quad >> 1) * 4u;
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(__byte_perm(hi, got, sel_hi)) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + L::kPieceBytes), "r"(__byte_perm(lo, got, sel_lo)) : "memory");
           }
-          const uint32_t piece = static_cast<uint32_t>((odd ? 4 : 0) + q4) ^ static_cast<uint32_t>(hl & 7);
-          const uint32_t at = base + L::kOffP + static_cast<uint32_t>(hl) * 128u + (piece << 4);
-          st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
-          st_shared_v4(at + L::kPieceBytes, lo[0], lo[1], lo[2], lo[3]);
         }
         tc_fence_before();
         fence_proxy_async_smem();
@@ -593,61 +709,91 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       }
       if (!run) break;
 
-      // The token's (or its part's) result, once its last products are done.
+      // The token's (or its part's) result, once its last products are done;
+      // before that the next token's Q, whose S then runs beside it.
+      const int done = t;
+      if (left > 0) {
+        do nb = blocks_of(p, ++t);
+        while (nb == 0);
+        b = 0;
+        q.fetch(p, t, h0, heads, quarter, half, lane);
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        l[g] += __shfl_xor_sync(0xffffffffu, l[g], 1);
+        l[g] += __shfl_xor_sync(0xffffffffu, l[g], 2);
+        if (lead) {
+          head_sum[half * kHeads + hq + 8 * g] = l[g];
+          if (half == 0) head_end[hq + 8 * g] = m[g];
+        }
+      }
       if (!mbar_wait(bar(L::kBarPDone), (e - 1) & 1, ctl)) bad = true;
-      __syncwarp();
+      bar_sync(1, kSoftmaxThreads);
       tc_fence_after();
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      if (left > 0) {
+        rs = q.place(base, smem, tmem, quarter, half, lane);
+        tc_fence_before();
+        mbar_arrive(bar(L::kBarQFull));
+      }
       float* ws = reinterpret_cast<float*>(p.ws + kLeftoverBytes) +
                   (static_cast<int64_t>(blockIdx.x) * 2 + slot) * part_floats(D);
-      if (whole) {
-        const float sink = hl < heads ? __ldg(p.sink + h0 + hl) * 1.4426950408889634f : 0.f;
-        const float top = fmaxf(m, sink);
-        float inv, lse;
-        if (top == -INFINITY) {                          // nothing at all (or only NaN)
-          inv = l * 0.f;
-          lse = l != l ? l : -INFINITY;
-        } else {
-          const float f = 0.015625f * exp2f(m - top);    // 2^-6: the weights' shift
-          const float total = l * f + exp2f(sink - top);
-          inv = f / total;
-          lse = log2f(total) + top;
-        }
-        if (!odd) {
-          head_f[hl] = inv;
-          if (hl < heads) p.lse[static_cast<int64_t>(t) * p.H + h0 + hl] = lse;
-        }
-      } else if (!odd) {
-        ws[kHeads * D + hl] = m;
-        ws[kHeads * D + kHeads + hl] = l;
-      }
-      bar_sync(1, kSoftmaxThreads);
-#pragma unroll 1
-      for (int c = 0; c < 2 * L::kChunks; ++c) {         // 128 of D, 32 heads at a time
-        float o[32];
-        tmem_ld32(tmem + lanes + L::kTmemO + c * 32, o);
-        const int d = (c >> 1) * 128 + tid;
-        const int hb = (c & 1) * 32;
-        if (D < 128 && warp >= D / 32) continue;         // rows that the tile does not have
+      if (tid < kHeads) {                                // thread = head
+        const int hl = tid;
+        const float m_end = head_end[hl], l_end = head_sum[hl] + head_sum[kHeads + hl];
         if (whole) {
-          // Lane pairs trade, so that each stores two columns of one head.
-          __nv_bfloat16* dst = p.o + (static_cast<int64_t>(t) * p.H + h0) * D + (d & ~1);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float u = o[i] * head_f[hb + i], v = o[i + 1] * head_f[hb + i + 1];
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? u : v, 1);
-            const int h = hb + i + (odd ? 1 : 0);
-            if (h < heads)
-              *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(h) * D) =
-                  odd ? pack_bf16x2(got, v) : pack_bf16x2(u, got);
+          const float sink = hl < heads ? __ldg(p.sink + h0 + hl) * 1.4426950408889634f : 0.f;
+          const float top = fmaxf(m_end, sink);
+          float inv, lse;
+          if (top == -INFINITY) {                        // nothing at all (or only NaN)
+            inv = l_end * 0.f;
+            lse = l_end != l_end ? l_end : -INFINITY;
+          } else {
+            const float f = exp2f(m_end - top);
+            const float total = fmaf(l_end, 4.f * f, exp2f(sink - top));
+            inv = 4.f * kCodeUnit * f / total;           // 4 = 2^kShift
+            lse = log2f(total) + top;
           }
+          head_f[hl] = inv;
+          if (hl < heads) p.lse[static_cast<int64_t>(done) * p.H + h0 + hl] = lse;
         } else {
+          ws[kHeads * D + hl] = m_end;
+          ws[kHeads * D + kHeads + hl] = l_end;
+        }
+      }
+      if (whole) bar_sync(1, kSoftmaxThreads);
+#pragma unroll 1
+      for (int c = 0; c < L::kChunks; ++c) {             // 128 of D, 32 heads per warp group
+        float o[32];
+        tmem_ld32(tmem + lanes + L::kTmemO + c * kHeads + half * 32, o);
+        const int dl = 32 * quarter + lane;              // this lane's column of the 128
+        if (whole) {
+          // Through shared memory (P's, which is free) to whole rows: 32 heads
+          // x 128 columns per warp group.
+          uint8_t* tile = smem + L::kOffP + half * L::kPieceBytes;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) ws[static_cast<int64_t>(hb + i) * D + d] = o[i];
+          for (int i = 0; i < 32; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(head_f + half * 32 + i);
+            const float fs[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<__nv_bfloat16*>(tile + (i + k) * 256 + dl * 2) = __float2bfloat16(o[i + k] * fs[k]);
+          }
+          bar_sync(2 + half, kSoftmaxThreads / 2);
+          constexpr int kRow16 = D < 128 ? D / 8 : 16;   // 16-byte pieces of a row in this tile
+          for (int i = 32 * quarter + lane; i < 32 * kRow16; i += kSoftmaxThreads / 2) {
+            const int h = half * 32 + i / kRow16;
+            if (h < heads)
+              *reinterpret_cast<uint4*>(p.o + (static_cast<int64_t>(done) * p.H + h0 + h) * D + c * 128 + (i % kRow16) * 8) =
+                  *reinterpret_cast<const uint4*>(tile + (i / kRow16) * 256 + (i % kRow16) * 16);
+          }
+          bar_sync(2 + half, kSoftmaxThreads / 2);
+        } else if (D >= 128 || quarter < D / 32) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) ws[static_cast<int64_t>(half * 32 + i) * D + c * 128 + dl] = o[i];
         }
       }
       tc_fence_before();
-      bar_sync(1, kSoftmaxThreads);                      // head_f and O are read
+      if (left == 0) break;
     }
   }
 
@@ -697,7 +843,7 @@ __global__ void __launch_bounds__(kJoinThreads) smqa_paged_join_kernel(const Pag
   float top = sink;
   for (int c = cta; c <= lastc; c += groups)
     if (c == cta || left[c].head_tok == tok) top = fmaxf(top, part(c)[kHeads * D + hl]);
-  float total = top == -INFINITY ? 0.f : 64.f * exp2f(sink - top);
+  float total = top == -INFINITY ? 0.f : 0.25f * exp2f(sink - top);  // in units of 2^kShift
   float o[kPer] = {};
   for (int c = cta; c <= lastc; c += groups) {
     if (c != cta && left[c].head_tok != tok) continue;   // an empty range
@@ -708,10 +854,10 @@ __global__ void __launch_bounds__(kJoinThreads) smqa_paged_join_kernel(const Pag
     for (int i = 0; i < kPer; ++i) o[i] = fmaf(w[static_cast<int64_t>(hl) * D + d + i], f, o[i]);
   }
   const int64_t row = static_cast<int64_t>(tok) * p.H + h0 + hl;
-  const float inv = total == 0.f ? 0.f : 1.f / total;
+  const float inv = total == 0.f ? 0.f : kCodeUnit / total;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) p.o[row * D + d + i] = __float2bfloat16(o[i] * inv);
-  if (d == 0) p.lse[row] = total == 0.f ? -INFINITY : log2f(total) - kShift + top;
+  if (d == 0) p.lse[row] = total == 0.f ? -INFINITY : log2f(total) + kShift + top;
 }
 
 // CTAs of a call: per head group, as many ranges as SMs (or as the tokens can
@@ -726,6 +872,15 @@ int ranges_of(const smqa_paged_shape& s) {
 template <int D>
 cudaError_t launch(const PagedFwdParams& p, int ctas, cudaStream_t stream) {
   using L = PagedLayout<D>;
+  // A split of registers above what the block is launched with would wait for
+  // ever: refuse to launch a kernel that was not built with 128 a thread.
+  static const cudaError_t built = [] {
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, smqa_paged_fwd_kernel<D>);
+    if (e != cudaSuccess) return e;
+    return a.numRegs * kThreads >= 2 * 128 * (kSoftmaxRegs + kOtherRegs) ? cudaSuccess : cudaErrorInvalidConfiguration;
+  }();
+  if (built != cudaSuccess) return built;
   cudaError_t e = cudaFuncSetAttribute(smqa_paged_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
   smqa_paged_fwd_kernel<D><<<ctas, kThreads, L::kSmem, stream>>>(p);
