@@ -103,6 +103,38 @@ __device__ __forceinline__ void tmem_ld16x64x2(uint32_t t0, uint32_t t1, float (
   }
 }
 
+// One 32-bit column of the warp's 32 lanes at N places (1 or 4), `step` columns
+// apart; one wait.
+template <int N, int kStep>
+__device__ __forceinline__ void tmem_ld1xn(uint32_t t, float (&v)[N]) {
+  static_assert(N == 1 || N == 4, "tmem_ld1xn: one or four columns");
+  uint32_t r[4] = {};
+  if constexpr (N == 4)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%4];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%1}, [%5];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%2}, [%6];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%3}, [%7];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(t), "r"(t + kStep), "r"(t + 2 * kStep), "r"(t + 3 * kStep)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0])
+        : "r"(t)
+        : "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+}
+// (A store: tmem_wait_st waits for it.)
+__device__ __forceinline__ void tmem_st1(uint32_t t, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(t), "r"(__float_as_uint(v)) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // Registers per thread of the calling warpgroup from here on (all its warps
 // call it).
 template <int N>

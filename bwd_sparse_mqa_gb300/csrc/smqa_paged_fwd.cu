@@ -41,14 +41,16 @@
 //                        same tile read MN-major, kept in the collector for
 //                        the second piece), N = 64 heads, K = 128 slots, for
 //                        both pieces of P;
-//   softmax (warps 0-7)  a warp reads 16 heads x 64 slots of S, four lanes per
-//                        head, both pieces of a row in one lane; weights, their
-//                        two pieces to shared memory, Q's pieces into TMEM at
-//                        the start of a token and O^T out of it at the end.
+//   softmax (warps 0-7)  two warpgroups take alternate blocks; a warp reads 16
+//                        heads of S, four lanes per head, both pieces of a row
+//                        in one lane; weights, their two pieces to shared
+//                        memory, Q's pieces into TMEM at the start of a token
+//                        and O^T out of it at the end.
 // TMEM: S 128 columns, O^T D/2, Q D/4.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "smqa_internal.h"
@@ -71,6 +73,19 @@ constexpr float kShift = 2.f;             // weights are 2^-2 at the running max
 constexpr float kLag = 2.75f;             // how far the maximum may lag behind
 constexpr float kCodeUnit = 0x1p-8f;      // what the tensor core's P counts
 
+// What the warpgroup that takes a block tells the other about it: whether it is
+// its token's last, and the heads whose maximum it has raised, to `to`, O and l
+// being multiplied by f (of a token's first block, `to` has every head's).
+struct Note {
+  unsigned heads[2];
+  int last, failed;
+  float to[kHeads], f[kHeads];
+};
+static_assert(sizeof(Note) % 8 == 0, "alignment of what follows");
+// A note is cleared four blocks before it is written (by the same warpgroup:
+// the vote of its block lies between) and four blocks after it was last read.
+constexpr int kNotes = 8;
+
 template <int D>
 struct PagedLayout {
   static constexpr int kChunks = D < 128 ? 1 : D / 128;      // 128-byte pieces of a row
@@ -87,17 +102,19 @@ struct PagedLayout {
   static constexpr uint32_t kOffA = kOffP + 2 * kPieceBytes; // [kStages][kMeta]: a, c, r
   static constexpr uint32_t kOffFlags = kOffA + kStages * kMeta * 4;  // [kStages]
   static constexpr uint32_t kOffHead = (kOffFlags + kStages * 4 + 15) & ~15u;  // float [64]
-  static constexpr uint32_t kOffMax = kOffHead + kHeads * 4;   // float [2][2][64]
-  static constexpr uint32_t kOffSum = kOffMax + 4 * kHeads * 4;  // float [2][64]
+  static constexpr uint32_t kOffMax = kOffHead + kHeads * 4;   // uint32 [2][64] (QLoader)
+  static constexpr uint32_t kOffSum = kOffMax + 2 * kHeads * 4;  // float [2][64]
   static constexpr uint32_t kOffEnd = kOffSum + 2 * kHeads * 4;  // float [64]
-  static constexpr uint32_t kOffBar = kOffEnd + kHeads * 4;
+  static constexpr uint32_t kOffNotes = kOffEnd + kHeads * 4;  // Note [kNotes]
+  static constexpr uint32_t kOffBar = kOffNotes + kNotes * sizeof(Note);
   static constexpr int kBarFull = 0;                         // [kStages]
   static constexpr int kBarEmpty = kBarFull + kStages;       // [kStages][4], a gather warp's rows
   static constexpr int kBarSFull = kBarEmpty + 4 * kStages;
   static constexpr int kBarSFree = kBarSFull + 1;
   static constexpr int kBarPFull = kBarSFree + 1;
   static constexpr int kBarPDone = kBarPFull + 1;            // P and its tile used, O up to date
-  static constexpr int kBarQFull = kBarPDone + 1;
+  static constexpr int kBarNote = kBarPDone + 1;             // [2] a warpgroup's note is written
+  static constexpr int kBarQFull = kBarNote + 2;
   static constexpr int kBarDrain = kBarQFull + 1;
   static constexpr int kNumBars = kBarDrain + 1;
   static constexpr uint32_t kOffCtl = kOffBar + 8 * kNumBars;  // TMEM base, abort flag
@@ -284,9 +301,11 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
     for (int i = 0; i < L::kStages; ++i) mbar_init(bar(L::kBarFull + i), 256);
     for (int i = 0; i < 4 * L::kStages; ++i) mbar_init(bar(L::kBarEmpty + i), 1);
     mbar_init(bar(L::kBarSFull), 1);
-    mbar_init(bar(L::kBarSFree), kSoftmaxThreads);
-    mbar_init(bar(L::kBarPFull), kSoftmaxThreads);
+    mbar_init(bar(L::kBarSFree), kSoftmaxThreads / 2);
+    mbar_init(bar(L::kBarPFull), kSoftmaxThreads / 2);
     mbar_init(bar(L::kBarPDone), 1);
+    mbar_init(bar(L::kBarNote), kSoftmaxThreads / 64);
+    mbar_init(bar(L::kBarNote + 1), kSoftmaxThreads / 64);
     mbar_init(bar(L::kBarQFull), kSoftmaxThreads);
     mbar_init(bar(L::kBarDrain), 1);
     *abort_flag = *reinterpret_cast<volatile int*>(p.status) != 0 ? 1 : 0;
@@ -449,23 +468,27 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
         break;
       }
       const uint32_t tile = base + static_cast<uint32_t>(st) * L::kStageBytes;
-      constexpr int kLpr = D / 16;                       // lanes per row
-      constexpr int kRpi = 32 / kLpr;                    // rows per warp instruction
-      const int sub = lane / kLpr, cc = lane % kLpr;
-      const uint32_t col = static_cast<uint32_t>(cc / 8) * L::kChunkBytes + static_cast<uint32_t>(32 * pw + sub) * 128u;
+      // An instruction copies 128 bytes (D = 64: 64) of each of several rows:
+      // a row's address is fetched from its lane once, its further pieces are
+      // at fixed distances (4 warps: 52 bytes a clock from L2, against 38 with
+      // one whole row per instruction).
+      constexpr int kLanes = D < 128 ? D / 16 : 8;       // lanes per row
+      constexpr int kRows = 32 / kLanes;                 // rows per instruction
+      const int sub = lane / kLanes, cc = lane % kLanes;
       const uint8_t* src = p.cache + cc * 16;
-      auto copy = [&](int k) {                           // rows k kRpi + sub of the warp's 32
-        const int rw = k * kRpi + sub;
-        const int rr = __shfl_sync(0xffffffffu, row, rw);
-        cp_async_16_or_zero(tile + col + static_cast<uint32_t>(k * kRpi) * 128u +
-                                ((static_cast<uint32_t>(cc % 8) ^ (static_cast<uint32_t>(rw) & 7u)) << 4),
-                            src + static_cast<int64_t>(rr) * D, (mask >> rw) & 1u);
+      auto copy = [&](int g) {                           // rows g kRows + sub of the warp's 32
+        const int rw = g * kRows + sub;
+        const uint8_t* from = src + static_cast<int64_t>(__shfl_sync(0xffffffffu, row, rw)) * D;
+        const bool on = (mask >> rw) & 1u;
+        const uint32_t to = tile + static_cast<uint32_t>(32 * pw + rw) * 128u + ((static_cast<uint32_t>(cc) ^ (static_cast<uint32_t>(rw) & 7u)) << 4);
+#pragma unroll
+        for (int c = 0; c < L::kChunks; ++c) cp_async_16_or_zero(to + c * L::kChunkBytes, from + c * 128, on);
       };
 #pragma unroll
-      for (int k = 0; k < 16 / kRpi; ++k) copy(k);
+      for (int g = 0; g < 16 / kRows; ++g) copy(g);
       if (!(now & kFinal)) look();
 #pragma unroll
-      for (int k = 16 / kRpi; k < 32 / kRpi; ++k) copy(k);
+      for (int g = 16 / kRows; g < 32 / kRows; ++g) copy(g);
       // y = S a + c, l += w r: a masked slot's row is zero, its c -inf.
       float* m = reinterpret_cast<float*>(smem + L::kOffA) + st * L::kMeta;
       m[meta_at(my)] = live ? s * p.scale_log2 : 0.f;
@@ -513,43 +536,46 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
         }
         mma_commit_elect(bar(L::kBarPDone));
       };
-      bool ok = *abort_flag == 0;
-      int seg = 0, before = 0;                           // tokens so far, the previous entry's flags
-      // O of entry e, once its P is written.
-      auto do_o = [&](int e, int flags) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarPFull), e & 1, ctl));
-        if (!ok) return;
-        tc_fence_after();
-        issue_o(e % L::kStages, (flags & kFirst) != 0);
-      };
-      for (int e = 0; ok; ++e) {
-        const int st = e % L::kStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarFull + st), (e / L::kStages) & 1, ctl));
-        if (!ok) break;
-        const int flags = flags_of[st];
-        const bool first = (flags & kFirst) != 0;
-        // A token's first S needs its Q, which the softmax warps bring once
-        // the token before is finished: that one's last O goes first.
-        if (first) {
-          if (e > 0) do_o(e - 1, before);
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQFull), seg & 1, ctl));
-          ++seg;
+      // Whichever is ready, the older work first: O of entry no, once its P is
+      // written; S of entry ns, once its rows are there, S's columns have been
+      // read and, at a token's start, its Q is in place.
+      bool ok = *abort_flag == 0, more = true;           // (more S to come)
+      int ns = 0, no = 0, seg = 0;
+      PollState ps = poll_start();
+      auto ready = [&](int i, int phase) { return __all_sync(0xffffffffu, mbar_probe(bar(i), phase & 1)); };
+      for (uint32_t spins = 0; ok && (more || no < ns);) {
+        if (no < ns && ready(L::kBarPFull, no)) {
+          const int st = no % L::kStages;
+          const bool first = (flags_of[st] & kFirst) != 0;
+          tc_fence_after();
+          issue_o(st, first);
+          ++no;
+        } else if (more && ns - no < L::kStages && ready(L::kBarFull + ns % L::kStages, ns / L::kStages) &&
+                   (ns == 0 || ready(L::kBarSFree, ns - 1))) {
+          const int st = ns % L::kStages;
+          const int flags = flags_of[st];
+          if (flags & kFirst) {
+            // The softmax warps bring Q once the token before is finished.
+            if (!ready(L::kBarQFull, seg)) {
+              if ((++spins & 63u) == 0u) ok = __all_sync(0xffffffffu, poll_check(ctl, ps));
+              continue;
+            }
+            ++seg;
+          }
+          fence_proxy_async_smem();                      // rows written by cp.async -> tensor core
+          tc_fence_after();
+          issue_s(st);
+          more = (flags & kFinal) == 0;
+          if (ns == 0 && static_cast<int>(blockIdx.x) == p.stall_cta) {  // test hook only
+            ok = __any_sync(0xffffffffu, stall_until_limit(ctl));
+            break;
+          }
+          ++ns;
+        } else {
+          if ((++spins & 63u) == 0u) ok = __all_sync(0xffffffffu, poll_check(ctl, ps));
+          continue;
         }
-        if (ok && e > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarSFree), (e - 1) & 1, ctl));
-        if (!ok) break;
-        fence_proxy_async_smem();                        // rows written by cp.async -> tensor core
-        tc_fence_after();
-        issue_s(st);
-        if (e == 0 && static_cast<int>(blockIdx.x) == p.stall_cta) {  // test hook only
-          ok = __any_sync(0xffffffffu, stall_until_limit(ctl));
-          break;
-        }
-        if (!first) do_o(e - 1, before);
-        before = flags;
-        if (flags & kFinal) {
-          if (ok) do_o(e, flags);
-          break;
-        }
+        ps.t0 = globaltimer_ns();                        // progress: the limit counts from here
       }
       mma_commit_elect(bar(L::kBarDrain));
       mbar_wait_drain(bar(L::kBarDrain), 0);
@@ -558,11 +584,11 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
   } else if (rg.count > 0) {
     reg_alloc<kSoftmaxRegs>();
     // ------------------------------------------------------------ softmax
-    // Warps w and w + 4 own the TMEM lanes of quarter w: 16 heads, half of the
-    // block's slots each.  A failed wait sets `bad`; the eight warps leave
-    // together at the next vote, so that none waits at a barrier that another
-    // has left.
-    const int quarter = warp & 3, half = warp >> 2;
+    // A warpgroup takes every other ring entry.  Its warp w owns the TMEM lanes
+    // of quarter w, 16 heads.  A thread whose wait failed keeps taking the same
+    // steps as the others and says so in its next note, which all read before
+    // they leave: none waits at a barrier that another has left.
+    const int quarter = warp & 3, half = warp >> 2;      // half: the warpgroup
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const int hq = 16 * quarter + (lane >> 2);           // this lane's heads: hq, hq + 8
     const int quad = lane & 3;                           // its slots: pairs 8 j + 2 quad
@@ -571,14 +597,16 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
     const uint32_t sel_send = (lane & 1) ? 0x5410u : 0x7632u;
     const uint32_t sel_hi = (lane & 1) ? 0x3254u : 0x5410u, sel_lo = (lane & 1) ? 0x3276u : 0x7610u;
     float* head_f = reinterpret_cast<float*>(smem + L::kOffHead);
-    float* head_max = reinterpret_cast<float*>(smem + L::kOffMax);
     float* head_sum = reinterpret_cast<float*>(smem + L::kOffSum);  // at a token's end: l of each
-    float* head_end = reinterpret_cast<float*>(smem + L::kOffEnd);  // half, and m
+    float* head_end = reinterpret_cast<float*>(smem + L::kOffEnd);  // warpgroup, and m
+    Note* notes = reinterpret_cast<Note*>(smem + L::kOffNotes);
     const volatile int* flags_of = reinterpret_cast<const volatile int*>(smem + L::kOffFlags);
-    bool bad = *abort_flag != 0;
     int64_t left = rg.count;
     int e = 0;
     bool run = true;
+    bool bad = *abort_flag != 0;                         // a wait of this thread has failed
+    if (tid < kNotes) notes[tid].heads[0] = notes[tid].heads[1] = notes[tid].failed = 0;
+    bar_sync(1, kSoftmaxThreads);
     // The CTA's tokens, or parts of tokens, one after another.
     int t = rg.tok, b = rg.off, nb = blocks_of(p, t);
     QLoader<D> q;
@@ -593,97 +621,101 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       left -= stop - b;
 
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-      for (bool last = false; run && !last; ++e) {
+      for (bool first = true, last = false; !last; first = false, ++e) {
+        Note* note = notes + e % kNotes;
+        // Every softmax warp comes here for every block, failed or not.
+        auto wait_note = [&] {
+          mbar_wait_drain(bar(L::kBarNote + (e & 1)), (e >> 1) & 1, 2 * p.limit_ns + 1000000000ull);
+          __syncwarp();
+        };
+        if ((e & 1) != half) {                           // the other warpgroup's block
+          wait_note();
+          if (*reinterpret_cast<volatile int*>(&note->failed) != 0) {
+            run = false;
+            break;
+          }
+          last = note->last != 0;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int h = hq + 8 * g;
+            if (first) {
+              m[g] = note->to[h];
+            } else if ((note->heads[h >> 5] >> (h & 31)) & 1u) {
+              m[g] = note->to[h];
+              l[g] *= note->f[h];
+            }
+          }
+          continue;
+        }
         const int st = e % L::kStages;
         if (!mbar_wait(bar(L::kBarSFull), e & 1, ctl)) bad = true;
         // (Completed before S was formed; orders the reads of the factors.)
         if (!mbar_wait(bar(L::kBarFull + st), (e / L::kStages) & 1, ctl)) bad = true;
         __syncwarp();
         tc_fence_after();
-        const int flags = flags_of[st];
-        last = (flags & kLast) != 0;
         const float* meta = reinterpret_cast<const float*>(smem + L::kOffA) + st * L::kMeta;
-        float2 y[2][8];                                  // per head, of its slot pairs
-        float mx[2];
-        {
+        float2 y[2][16];                                 // per head, of its slot pairs
+        const float2 fh[2] = {make_float2(rs.x, rs.x), make_float2(rs.y, rs.y)};
+        const float2 fl[2] = {make_float2(rs.x * 0.03125f, rs.x * 0.03125f), make_float2(rs.y * 0.03125f, rs.y * 0.03125f)};
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
           float x[2][32];
-          const uint32_t s0 = tmem + lanes + L::kTmemS + half * 64;
+          const uint32_t s0 = tmem + lanes + L::kTmemS + part * 64;
           tmem_ld16x64x2(s0, s0 + (16u << 16), x[0], x[1]);
-          tc_fence_before();
-          mbar_arrive(bar(L::kBarSFree));
-          const float2 fh[2] = {make_float2(rs.x, rs.x), make_float2(rs.y, rs.y)};
-          const float2 fl[2] = {make_float2(rs.x * 0.03125f, rs.x * 0.03125f), make_float2(rs.y * 0.03125f, rs.y * 0.03125f)};
+          if (part == 1) {
+            tc_fence_before();
+            mbar_arrive(bar(L::kBarSFree));
+          }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float4 ac = *reinterpret_cast<const float4*>(meta + (32 * half + 4 * j + quad) * 4);
+            const float4 ac = *reinterpret_cast<const float4*>(meta + (32 * part + 4 * j + quad) * 4);
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               const float2 hi = make_float2(x[g][4 * j], x[g][4 * j + 1]), lo = make_float2(x[g][4 * j + 2], x[g][4 * j + 3]);
-              y[g][j] = fma2(fma2(hi, fh[g], mul2(lo, fl[g])), make_float2(ac.x, ac.y), make_float2(ac.z, ac.w));
+              y[g][8 * part + j] = fma2(fma2(hi, fh[g], mul2(lo, fl[g])), make_float2(ac.x, ac.y), make_float2(ac.z, ac.w));
             }
           }
+        }
+        // The maxima: set by a token's first block, raised where this block's
+        // outran the lag.
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            mx[g] = fmaxf(y[g][0].x, y[g][0].y);
+        for (int g = 0; g < 2; ++g) {
+          const int h = hq + 8 * g;
+          float mx = fmaxf(y[g][0].x, y[g][0].y);
 #pragma unroll
-            for (int j = 1; j < 8; ++j) mx[g] = fmax3f(mx[g], y[g][j].x, y[g][j].y);
-            mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], 1));
-            mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], 2));
+          for (int j = 1; j < 16; ++j) mx = fmax3f(mx, y[g][j].x, y[g][j].y);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          if (first) {
+            if (lead) note->to[h] = mx;
+            m[g] = mx;
+          } else if (mx > m[g] + kLag) {
+            const float f = fast_exp2(m[g] - mx);
+            l[g] *= f;
+            m[g] = mx;
+            if (lead) {
+              note->to[h] = mx;
+              note->f[h] = f;
+              atomicOr(&note->heads[h >> 5], 1u << (h & 31));
+            }
           }
         }
-        const bool first = (flags & kFirst) != 0;
-        float* peers = head_max + (e & 1) * 2 * kHeads;  // both warps' maxima of this block
-        if (lead) {
-          peers[half * kHeads + hq] = mx[0];
-          peers[half * kHeads + hq + 8] = mx[1];
+        if (bad) note->failed = 1;
+        if (lane == 0 && quarter == 0) {
+          note->last = flags_of[st] & kLast;
+          Note* next = notes + (e + 4) % kNotes;
+          next->heads[0] = next->heads[1] = next->failed = 0;
         }
-        const bool up = !first && (mx[0] > m[0] + kLag || mx[1] > m[1] + kLag);
-        const bool any = bar_any(1, kSoftmaxThreads, up || bad);
-        if (any && bar_any(1, kSoftmaxThreads, bad)) {
-          run = false;
-          break;
-        }
-        if (first || any) {
-          mx[0] = fmaxf(peers[hq], peers[kHeads + hq]);
-          mx[1] = fmaxf(peers[hq + 8], peers[kHeads + hq + 8]);
-        }
-        // P and O are this thread's once the previous block's products are done.
-        if (e > 0 && !mbar_wait(bar(L::kBarPDone), (e - 1) & 1, ctl)) bad = true;
         __syncwarp();
-        if (any) {                                       // some head's O has to be rescaled
-          tc_fence_after();
+        if (lane == 0) mbar_arrive(bar(L::kBarNote + (e & 1)));
+        // The weights, their part of l, and their two pieces.
+        uint32_t out_hi[2][8], out_lo[2][8];
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const bool grow = !first && mx[g] > m[g] + kLag;
-            const float f = grow ? fast_exp2(m[g] - mx[g]) : 1.f;
-            if (grow) {
-              m[g] = mx[g];
-              l[g] *= f;
-            }
-            if (lead && half == 0) head_f[hq + 8 * g] = f;
-          }
-          bar_sync(1, kSoftmaxThreads);
-#pragma unroll 1
-          for (int c = 0; c < L::kChunks; ++c) {
-            float o[32];
-            const uint32_t at = tmem + lanes + L::kTmemO + c * kHeads + half * 32;
-            tmem_ld32(at, o);
+        for (int g = 0; g < 2; ++g) {
+          const float shift = (m[g] == -INFINITY ? 0.f : m[g]) + kShift;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= head_f[half * 32 + i];
-            tmem_st32(at, o);
-          }
-          bar_sync(1, kSoftmaxThreads);                  // head_f is read
-        }
-        if (first) {
-          m[0] = mx[0];
-          m[1] = mx[1];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float4 r = *reinterpret_cast<const float4*>(meta + 2 * kBlk + (4 * half + j / 2) * 16 + quad * 4);
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float shift = (m[g] == -INFINITY ? 0.f : m[g]) + kShift;
+          for (int j = 0; j < 16; j += 2) {
+            const float4 r = *reinterpret_cast<const float4*>(meta + 2 * kBlk + (j / 2) * 16 + quad * 4);
             const float2 w01 = make_float2(fast_exp2(y[g][j].x - shift), fast_exp2(y[g][j].y - shift));
             const float2 w23 = make_float2(fast_exp2(y[g][j + 1].x - shift), fast_exp2(y[g][j + 1].y - shift));
             l[g] = fmaf(w01.x, r.x, l[g]);
@@ -695,12 +727,57 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
             // Lanes of a pair trade, the even one for four slots in a row at
             // 8j, the odd one at 8j + 8.
             const uint32_t got = __shfl_xor_sync(0xffffffffu, __byte_perm(hi, lo, sel_send), 1);
-            const int h = hq + 8 * g;
-            const uint32_t at = base + L::kOffP + static_cast<uint32_t>(h) * 128u +
-                                ((static_cast<uint32_t>(4 * half + j / 2) ^ static_cast<uint32_t>(h & 7)) << 4) +
-                                (lane & 1) * 8u + (quad >> 1) * 4u;
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(__byte_perm(hi, got, sel_hi)) : "memory");
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + L::kPieceBytes), "r"(__byte_perm(lo, got, sel_lo)) : "memory");
+            out_hi[g][j / 2] = __byte_perm(hi, got, sel_hi);
+            out_lo[g][j / 2] = __byte_perm(lo, got, sel_lo);
+          }
+        }
+        wait_note();
+        if (*reinterpret_cast<volatile int*>(&note->failed) != 0) {
+          run = false;
+          break;
+        }
+        last = note->last != 0;
+        const unsigned raised[2] = {*reinterpret_cast<volatile unsigned*>(&note->heads[0]),
+                                    *reinterpret_cast<volatile unsigned*>(&note->heads[1])};
+        // P and O are this thread's once the previous block's products are done.
+        if (e > 0 && !mbar_wait(bar(L::kBarPDone), (e - 1) & 1, ctl)) bad = true;
+        __syncwarp();
+        if (raised[0] | raised[1]) {                     // O of these heads, rescaled
+          tc_fence_after();
+          const uint32_t o = tmem + lanes + L::kTmemO;
+          if (__popc(raised[0]) + __popc(raised[1]) <= 16) {  // column by column
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              for (unsigned some = raised[u]; some != 0; some &= some - 1) {
+                const int h = 32 * u + __ffs(some) - 1;
+                const float f = note->f[h];
+                float v[L::kChunks];
+                tmem_ld1xn<L::kChunks, kHeads>(o + h, v);
+#pragma unroll
+                for (int c = 0; c < L::kChunks; ++c) tmem_st1(o + c * kHeads + h, v[c] * f);
+              }
+            tmem_wait_st();
+          } else {                                       // all of it
+#pragma unroll 1
+            for (int c = 0; c < 2 * L::kChunks; ++c) {
+              float v[32];
+              tmem_ld32(o + c * 32, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if ((raised[c & 1] >> i) & 1u) v[i] *= note->f[(c & 1) * 32 + i];
+              tmem_st32(o + c * 32, v);
+            }
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int h = hq + 8 * g;
+          const uint32_t row = base + L::kOffP + static_cast<uint32_t>(h) * 128u + (lane & 1) * 8u + (quad >> 1) * 4u;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t at = row + ((static_cast<uint32_t>(j) ^ static_cast<uint32_t>(h & 7)) << 4);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(out_hi[g][j]) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + L::kPieceBytes), "r"(out_lo[g][j]) : "memory");
           }
         }
         tc_fence_before();

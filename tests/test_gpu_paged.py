@@ -509,3 +509,27 @@ def test_attn_writes_stay_in_bounds():
     assert o.intact() and lse.intact() and ws.intact()
     ref.check_attn((o.view(torch.bfloat16, (T, H, D))[:3], lse.view(torch.float32, (T, H))[:3]),
                    [w[:3] for w in _want(x)])
+
+
+@pytest.mark.parametrize("D,topk,cta", [(512, 300, 0), (512, 0, 3), (64, 0, 1), (512, 2048, 151)])
+def test_attn_bounded_wait_runs_out(D, topk, cta):
+    """One CTA is stopped after its first MMA: the call ends with the timeout status, by the wait
+    limit, and the next one computes as before."""
+    from bwd_sparse_mqa_gb300 import set_wait_limit_ns
+    x = _attn_case([3000], [(0, 2999 - i) for i in range(40)], 100, D, topk, 64, 80)
+    want = _run(x)
+    lib = _lib.load()
+    before = set_wait_limit_ns(20_000_000)
+    lib.smqa_debug_stall(cta)
+    try:
+        d = {k: (None if v is None else v.cuda()) for k, v in x.items()}
+        args = [d[k] for k in ("q", "kv_cache", "kv_scales", "attn_sink", "block_table", "seq_lens", "token_req", "positions")]
+        with pytest.raises(_lib.SMQAError) as err:
+            sparse_mqa_paged_fwd(*args, d["topk_idxs"], check_status=True)
+        assert err.value.status == _lib.SMQA_ERR_DEVICE_TIMEOUT
+    finally:
+        lib.smqa_debug_stall(-1)
+        set_wait_limit_ns(0)
+    assert before > 0 and device_status(clear=True) == _lib.SMQA_ERR_DEVICE_TIMEOUT
+    got = _run(x)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
