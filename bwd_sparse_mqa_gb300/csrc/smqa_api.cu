@@ -208,6 +208,17 @@ smqa_status validate_shape(const smqa_shape& s) { return check_shape(s); }
 
 smqa_status cuda_failure(cudaError_t e, const char* where) { return cuda_fail(e, where); }
 
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t{1} << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 int* device_status_word(cudaError_t* err) { return status_ptr(err); }
 
 uint64_t current_wait_limit_ns() { return wait_limit_ns(); }

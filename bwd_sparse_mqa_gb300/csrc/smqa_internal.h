@@ -2,6 +2,7 @@
 // translation units (not part of the public C ABI).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -141,6 +142,7 @@ struct PagedFwdParams {
   int T, R, H, D, topk, max_pages, n_pages, page_shift;
   float scale_log2;          // sm_scale * log2(e)
   int zero_padding;
+  int whole_tokens;          // no token is split between CTAs
   uint8_t* ws;               // workspace (paged_fwd_workspace bytes)
   int* status;
   uint64_t limit_ns;
@@ -195,6 +197,9 @@ inline bool is_aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 smqa_status cuda_failure(cudaError_t e, const char* where);
+// Raises a kernel's dynamic shared memory limit on the current device, once
+// per device (`done`: a bit per device, zero at first).
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 // The current device's status word (null and *err on failure), the limit of
 // bounded waits and the CTA of the stall hook.
 int* device_status_word(cudaError_t* err);

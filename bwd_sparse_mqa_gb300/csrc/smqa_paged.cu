@@ -363,8 +363,8 @@ smqa_status smqa_paged_plan(const int32_t* context_lens, const int32_t* query_le
                token_req, positions, slot_mapping};
   const size_t smem = (static_cast<size_t>(R) * 2 + 1) * sizeof(int32_t);
   const auto kern = in_place ? smqa_paged_plan_kernel<true> : smqa_paged_plan_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  static std::atomic<uint64_t> allowed[2];
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), (2 * kPlanMaxR + 1) * 4, allowed[in_place]);
   if (e != cudaSuccess) return cuda_failure(e, "paged plan launch");
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(kPlanThreads);

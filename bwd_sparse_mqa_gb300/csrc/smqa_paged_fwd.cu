@@ -145,7 +145,10 @@ struct Leftover {
 };
 constexpr size_t kLeftoverBytes = 4096;
 constexpr int kMaxCtas = static_cast<int>(kLeftoverBytes / sizeof(Leftover));
-__host__ __device__ constexpr size_t part_floats(int D) { return static_cast<size_t>(kHeads) * D + 2 * kHeads; }
+// A part: O as [D / 128][16 groups of 4 heads][128 columns][4 heads] (D = 64:
+// half of the columns unused), then m and l of the heads.
+__host__ __device__ constexpr int part_o(int D) { return kHeads * (D < 128 ? 128 : D); }
+__host__ __device__ constexpr size_t part_floats(int D) { return static_cast<size_t>(part_o(D)) + 2 * kHeads; }
 
 __device__ __forceinline__ bool live_token(const PagedFwdParams& p, int req) {
   return static_cast<unsigned>(req) < static_cast<unsigned>(p.R);
@@ -298,15 +301,15 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
   int* end_tok = reinterpret_cast<int*>(smem + L::kOffRange + 16 + 128);     // token, its end, its begin
 
   if (tid == 0) {
-    for (int i = 0; i < L::kStages; ++i) mbar_init(bar(L::kBarFull + i), 256);
+    for (int i = 0; i < L::kStages; ++i) mbar_init(bar(L::kBarFull + i), 128 + 4);  // copies landed, factors written
     for (int i = 0; i < 4 * L::kStages; ++i) mbar_init(bar(L::kBarEmpty + i), 1);
     mbar_init(bar(L::kBarSFull), 1);
-    mbar_init(bar(L::kBarSFree), kSoftmaxThreads / 2);
-    mbar_init(bar(L::kBarPFull), kSoftmaxThreads / 2);
+    mbar_init(bar(L::kBarSFree), kSoftmaxThreads / 64);  // (one arrival per warp)
+    mbar_init(bar(L::kBarPFull), kSoftmaxThreads / 64);
     mbar_init(bar(L::kBarPDone), 1);
     mbar_init(bar(L::kBarNote), kSoftmaxThreads / 64);
     mbar_init(bar(L::kBarNote + 1), kSoftmaxThreads / 64);
-    mbar_init(bar(L::kBarQFull), kSoftmaxThreads);
+    mbar_init(bar(L::kBarQFull), kSoftmaxThreads / 32);
     mbar_init(bar(L::kBarDrain), 1);
     *abort_flag = *reinterpret_cast<volatile int*>(p.status) != 0 ? 1 : 0;
     range->count = 0;
@@ -314,14 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc(base + L::kOffCtl, L::kTmemCols);
-  // Padding tokens belong to no range.
-  if (p.zero_padding)
-    for (int t = blockIdx.x; t < p.T; t += gridDim.x)
-      if (!live_token(p, __ldg(p.token_req + t))) {
-        uint4* o = reinterpret_cast<uint4*>(p.o + static_cast<int64_t>(t) * p.H * D);
-        for (int i = tid; i < p.H * D / 8; i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
-        for (int h = tid; h < p.H; h += kThreads) p.lse[static_cast<int64_t>(t) * p.H + h] = -INFINITY;
-      }
+  grid_dependents_launch();
   // The CTA's range: the total number of blocks, and the tokens in which the
   // range begins and ends (each thread sums a run of tokens).
   {
@@ -342,10 +338,13 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       if (w < warp) before += warp_sum[w];
       total += warp_sum[w];
     }
-    // Equal ranges, the first total mod parts of them one block longer.
-    const int64_t each = total / parts;
+    // Equal ranges, the first total mod parts of them one block (or token)
+    // longer.
+    const int unit = p.whole_tokens && p.idx ? (p.topk + kBlk - 1) / kBlk : 1;
+    total = static_cast<uint32_t>(total >> 32) != 0 ? total / unit : static_cast<uint32_t>(total) / static_cast<uint32_t>(unit);
+    const int64_t each = (total >> 32) != 0 ? total / parts : static_cast<uint32_t>(total) / static_cast<uint32_t>(parts);
     const int extra = static_cast<int>(total - each * parts);
-    const int64_t begin = each * part + min(part, extra), end = begin + each + (part < extra ? 1 : 0);
+    const int64_t begin = (each * part + min(part, extra)) * unit, end = begin + (each + (part < extra ? 1 : 0)) * unit;
     if (begin < end) {
       if (before <= begin && begin < before + mine) {
         int64_t at = before;
@@ -387,6 +386,15 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
     }
     reinterpret_cast<Leftover*>(p.ws)[blockIdx.x] = l;
   }
+
+  // Padding tokens belong to no range; warps without another role see to them.
+  if (p.zero_padding && warp > kMmaWarp && warp < kGatherWarp0)
+    for (int t = blockIdx.x + (warp - kMmaWarp - 1) * gridDim.x; t < p.T; t += gridDim.x * (kGatherWarp0 - kMmaWarp - 1))
+      if (!live_token(p, __ldg(p.token_req + t))) {
+        uint4* o = reinterpret_cast<uint4*>(p.o + static_cast<int64_t>(t) * p.H * D);
+        for (int i = lane; i < p.H * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+        for (int h = lane; h < p.H; h += 32) p.lse[static_cast<int64_t>(t) * p.H + h] = -INFINITY;
+      }
 
   if (rg.count > 0 && warp >= kGatherWarp0) {
     reg_dealloc<kOtherRegs>();
@@ -452,6 +460,15 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       in_page = pos & ((1 << p.page_shift) - 1);
       page = pos >= 0 && col < p.max_pages ? __ldg(tab + col) : -1;
     };
+    // This slot's row on its way to L2: the tile it will be copied to may be in
+    // use for longer than HBM takes.
+    auto prefetch = [&] {
+      if (static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages)) {
+        const uint8_t* r = p.cache + ((static_cast<int64_t>(page) << p.page_shift) + in_page) * D;
+#pragma unroll
+        for (int c = 0; c < L::kChunks; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + c * 128));
+      }
+    };
     ask();
     look();
     for (int e = 0;; ++e) {
@@ -495,8 +512,10 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       m[meta_at(my) + 2] = live ? log2f(s) : -INFINITY;
       m[rec_at(my)] = live ? 1.f / s : 0.f;
       if (my == 0) reinterpret_cast<int*>(smem + L::kOffFlags)[st] = now;
+      if (!(now & kFinal) && e >= L::kStages - 1) prefetch();
       cp_async_arrive_noinc(bar(L::kBarFull + st));      // once the copies have landed
-      mbar_arrive(bar(L::kBarFull + st));                // releases the factors
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kBarFull + st)); // releases the factors
       if (now & kFinal) break;
     }
     cp_async_wait_all();
@@ -605,6 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
     int e = 0;
     bool run = true;
     bool bad = *abort_flag != 0;                         // a wait of this thread has failed
+    const float sink = tid < heads ? __ldg(p.sink + h0 + tid) * 1.4426950408889634f : 0.f;  // (thread = head)
     if (tid < kNotes) notes[tid].heads[0] = notes[tid].heads[1] = notes[tid].failed = 0;
     bar_sync(1, kSoftmaxThreads);
     // The CTA's tokens, or parts of tokens, one after another.
@@ -613,7 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
     q.fetch(p, t, h0, heads, quarter, half, lane);
     float2 rs = q.place(base, smem, tmem, quarter, half, lane);
     tc_fence_before();
-    mbar_arrive(bar(L::kBarQFull));
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(L::kBarQFull));
     while (true) {
       const int stop = static_cast<int>(min(static_cast<int64_t>(nb), b + left));
       const bool whole = b == 0 && stop == nb;
@@ -625,7 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
         Note* note = notes + e % kNotes;
         // Every softmax warp comes here for every block, failed or not.
         auto wait_note = [&] {
-          mbar_wait_drain(bar(L::kBarNote + (e & 1)), (e >> 1) & 1, 2 * p.limit_ns + 1000000000ull);
+          if (!mbar_test(bar(L::kBarNote + (e & 1)), (e >> 1) & 1))
+            mbar_wait_drain(bar(L::kBarNote + (e & 1)), (e >> 1) & 1, 2 * p.limit_ns + 1000000000ull);
           __syncwarp();
         };
         if ((e & 1) != half) {                           // the other warpgroup's block
@@ -648,31 +670,27 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
           continue;
         }
         const int st = e % L::kStages;
+        if (!mbar_wait(bar(L::kBarFull + st), (e / L::kStages) & 1, ctl)) bad = true;  // the factors
         if (!mbar_wait(bar(L::kBarSFull), e & 1, ctl)) bad = true;
-        // (Completed before S was formed; orders the reads of the factors.)
-        if (!mbar_wait(bar(L::kBarFull + st), (e / L::kStages) & 1, ctl)) bad = true;
         __syncwarp();
         tc_fence_after();
         const float* meta = reinterpret_cast<const float*>(smem + L::kOffA) + st * L::kMeta;
         float2 y[2][16];                                 // per head, of its slot pairs
         const float2 fh[2] = {make_float2(rs.x, rs.x), make_float2(rs.y, rs.y)};
         const float2 fl[2] = {make_float2(rs.x * 0.03125f, rs.x * 0.03125f), make_float2(rs.y * 0.03125f, rs.y * 0.03125f)};
+        {
+          float x[2][64];
+          tmem_ld16x128x2(tmem + lanes + L::kTmemS, x[0], x[1]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kBarSFree));
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          float x[2][32];
-          const uint32_t s0 = tmem + lanes + L::kTmemS + part * 64;
-          tmem_ld16x64x2(s0, s0 + (16u << 16), x[0], x[1]);
-          if (part == 1) {
-            tc_fence_before();
-            mbar_arrive(bar(L::kBarSFree));
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 ac = *reinterpret_cast<const float4*>(meta + (32 * part + 4 * j + quad) * 4);
+          for (int j = 0; j < 16; ++j) {
+            const float4 ac = *reinterpret_cast<const float4*>(meta + (4 * j + quad) * 4);
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               const float2 hi = make_float2(x[g][4 * j], x[g][4 * j + 1]), lo = make_float2(x[g][4 * j + 2], x[g][4 * j + 3]);
-              y[g][8 * part + j] = fma2(fma2(hi, fh[g], mul2(lo, fl[g])), make_float2(ac.x, ac.y), make_float2(ac.z, ac.w));
+              y[g][j] = fma2(fma2(hi, fh[g], mul2(lo, fl[g])), make_float2(ac.x, ac.y), make_float2(ac.z, ac.w));
             }
           }
         }
@@ -782,7 +800,8 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
         }
         tc_fence_before();
         fence_proxy_async_smem();
-        mbar_arrive(bar(L::kBarPFull));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kBarPFull));
       }
       if (!run) break;
 
@@ -810,7 +829,8 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       if (left > 0) {
         rs = q.place(base, smem, tmem, quarter, half, lane);
         tc_fence_before();
-        mbar_arrive(bar(L::kBarQFull));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kBarQFull));
       }
       float* ws = reinterpret_cast<float*>(p.ws + kLeftoverBytes) +
                   (static_cast<int64_t>(blockIdx.x) * 2 + slot) * part_floats(D);
@@ -818,7 +838,6 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
         const int hl = tid;
         const float m_end = head_end[hl], l_end = head_sum[hl] + head_sum[kHeads + hl];
         if (whole) {
-          const float sink = hl < heads ? __ldg(p.sink + h0 + hl) * 1.4426950408889634f : 0.f;
           const float top = fmaxf(m_end, sink);
           float inv, lse;
           if (top == -INFINITY) {                        // nothing at all (or only NaN)
@@ -833,40 +852,53 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
           head_f[hl] = inv;
           if (hl < heads) p.lse[static_cast<int64_t>(done) * p.H + h0 + hl] = lse;
         } else {
-          ws[kHeads * D + hl] = m_end;
-          ws[kHeads * D + kHeads + hl] = l_end;
+          ws[part_o(D) + hl] = m_end;
+          ws[part_o(D) + kHeads + hl] = l_end;
         }
       }
-      if (whole) bar_sync(1, kSoftmaxThreads);
+      if (whole) {
+        bar_sync(1, kSoftmaxThreads);
+        // 32 heads x 32 columns a time through the warp's part of P's place
+        // (free now) to 64-byte rows: [head][4 pieces of 8 columns].
+        uint8_t* tile = smem + L::kOffP + warp * 2048;
+        const uint32_t tile_at = base + L::kOffP + warp * 2048;
+        float2 f[4];                                     // of heads 8 j + 2 quad, + 1
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = *reinterpret_cast<const float2*>(head_f + half * 32 + 8 * j + 2 * quad);
+        if (D >= 128 || quarter < D / 32) {
 #pragma unroll 1
-      for (int c = 0; c < L::kChunks; ++c) {             // 128 of D, 32 heads per warp group
-        float o[32];
-        tmem_ld32(tmem + lanes + L::kTmemO + c * kHeads + half * 32, o);
-        const int dl = 32 * quarter + lane;              // this lane's column of the 128
-        if (whole) {
-          // Through shared memory (P's, which is free) to whole rows: 32 heads
-          // x 128 columns per warp group.
-          uint8_t* tile = smem + L::kOffP + half * L::kPieceBytes;
+          for (int c = 0; c < L::kChunks; ++c) {
+            float v[2][16];                              // columns 0-15, 16-31 of the quarter's 32
+            tmem_ld16x32x2(tmem + lanes + L::kTmemO + c * kHeads + half * 32, v[0], v[1]);
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(head_f + half * 32 + i);
-            const float fs[4] = {f.x, f.y, f.z, f.w};
+            for (int j = 0; j < 4; ++j) {                // 8 heads: four 8-column matrices
+              uint32_t w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<__nv_bfloat16*>(tile + (i + k) * 256 + dl * 2) = __float2bfloat16(o[i + k] * fs[k]);
+              for (int o = 0; o < 4; ++o)
+                w[o] = pack_bf16x2(v[o >> 1][4 * j + 2 * (o & 1)] * f[j].x, v[o >> 1][4 * j + 2 * (o & 1) + 1] * f[j].y);
+              const uint32_t h = static_cast<uint32_t>(8 * j + (lane & 7));
+              stmatrix_trans_x4(tile_at + h * 64u + ((static_cast<uint32_t>(lane >> 3) ^ ((h >> 1) & 3u)) << 4), w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int h = 8 * i + (lane >> 2);
+              const uint4 x = *reinterpret_cast<const uint4*>(tile + h * 64 + ((quad ^ ((h >> 1) & 3)) << 4));
+              if (half * 32 + h < heads)
+                *reinterpret_cast<uint4*>(p.o + (static_cast<int64_t>(done) * p.H + h0 + half * 32 + h) * D + c * 128 + 32 * quarter + quad * 8) = x;
+            }
+            __syncwarp();
           }
-          bar_sync(2 + half, kSoftmaxThreads / 2);
-          constexpr int kRow16 = D < 128 ? D / 8 : 16;   // 16-byte pieces of a row in this tile
-          for (int i = 32 * quarter + lane; i < 32 * kRow16; i += kSoftmaxThreads / 2) {
-            const int h = half * 32 + i / kRow16;
-            if (h < heads)
-              *reinterpret_cast<uint4*>(p.o + (static_cast<int64_t>(done) * p.H + h0 + h) * D + c * 128 + (i % kRow16) * 8) =
-                  *reinterpret_cast<const uint4*>(tile + (i / kRow16) * 256 + (i % kRow16) * 16);
-          }
-          bar_sync(2 + half, kSoftmaxThreads / 2);
-        } else if (D >= 128 || quarter < D / 32) {
+        }
+      } else if (D >= 128 || quarter < D / 32) {
+        float4* part = reinterpret_cast<float4*>(ws) + half * 8 * 128 + 32 * quarter + lane;
+#pragma unroll 1
+        for (int c = 0; c < L::kChunks; ++c) {           // 128 of D, 32 heads per warpgroup
+          float o[32];
+          tmem_ld32(tmem + lanes + L::kTmemO + c * kHeads + half * 32, o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) ws[static_cast<int64_t>(half * 32 + i) * D + c * 128 + dl] = o[i];
+          for (int i = 0; i < 32; i += 4)
+            __stcg(part + (c * (kHeads / 4) + i / 4) * 128, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
         }
       }
       tc_fence_before();
@@ -882,68 +914,146 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
   }
 }
 
-// Joins the parts of a token that several CTAs hold.  One block per (CTA whose
-// range a token starts in and leaves, 4 heads): part i of n weighs
-// 2^(m_i - top).
-constexpr int kJoinHeads = 4, kJoinThreads = 256;
+// Joins the parts of a token that several CTAs hold: a block per CTA whose range
+// a token starts in and leaves and per 4 heads; a thread takes one column of
+// every 128 for the four heads, lane i of every warp also m and l of part i,
+// which weighs 2^(m_i - top).  Bound by latency: whose token and how many parts
+// is one trip to L2, m, l and the first kAhead parts of O together the second.
+// Small blocks with many loads each: four times larger ones, each warp with all
+// the reductions for a quarter of the columns, took 25 us where these take 6.
+constexpr int kJoinHeads = 4;
 
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) smqa_paged_join_kernel(const PagedFwdParams p, int ctas) {
+template <int D, int kAhead>
+__global__ void __launch_bounds__(D < 128 ? D : 128) smqa_paged_join_kernel(const PagedFwdParams p, int ctas) {
+  constexpr int kChunks = D < 128 ? 1 : D / 128;
   grid_dependency_wait();
   const int groups = (p.H + kHeads - 1) / kHeads;
-  const int cta = blockIdx.x / (kHeads / kJoinHeads);
-  const int hb = (blockIdx.x % (kHeads / kJoinHeads)) * kJoinHeads;
+  const int cta = blockIdx.x / (kHeads / kJoinHeads), hg = blockIdx.x % (kHeads / kJoinHeads);
   const int h0 = (cta % groups) * kHeads;
-  const Leftover* left = reinterpret_cast<const Leftover*>(p.ws);
-  const int tok = left[cta].tail_tok;
-  if (tok < 0 || h0 + hb >= p.H) return;
-  // The CTAs behind it that hold the rest: up to the first whose range the
-  // token does not leave.
   const int lane = threadIdx.x & 31;
-  int lastc = cta;
-  for (int c0 = cta + groups; c0 < ctas; c0 += 32 * groups) {
-    const int c = c0 + lane * groups;
-    const bool end = c < ctas && left[c].head_tok == tok && !left[c].head_more;
-    const unsigned b = __ballot_sync(0xffffffffu, end);
-    if (b) {
-      lastc = c0 + (__ffs(b) - 1) * groups;
-      break;
-    }
-  }
-  constexpr int kPer = kJoinHeads * D / kJoinThreads;    // consecutive columns per thread
-  const int hl = hb + static_cast<int>(threadIdx.x) / (kJoinThreads / kJoinHeads);
-  const int d = (static_cast<int>(threadIdx.x) % (kJoinThreads / kJoinHeads)) * kPer;
+  const int4* left = reinterpret_cast<const int4*>(p.ws);  // Leftover
   const float* parts = reinterpret_cast<const float*>(p.ws + kLeftoverBytes);
   auto part = [&](int c) { return parts + (static_cast<int64_t>(c) * 2 + (c == cta ? 1 : 0)) * part_floats(D); };
-  if (h0 + hl >= p.H) return;
-  const float sink = __ldg(p.sink + h0 + hl) * 1.4426950408889634f;
-  float top = sink;
-  for (int c = cta; c <= lastc; c += groups)
-    if (c == cta || left[c].head_tok == tok) top = fmaxf(top, part(c)[kHeads * D + hl]);
-  float total = top == -INFINITY ? 0.f : 0.25f * exp2f(sink - top);  // in units of 2^kShift
-  float o[kPer] = {};
-  for (int c = cta; c <= lastc; c += groups) {
-    if (c != cta && left[c].head_tok != tok) continue;   // an empty range
-    const float* w = part(c);
-    const float f = top == -INFINITY ? 0.f : exp2f(w[kHeads * D + hl] - top);
-    total = fmaf(w[kHeads * D + kHeads + hl], f, total);
+  // 32 CTAs at a time: this one and those behind it that hold the rest, up to
+  // the first whose range the token does not leave.  An empty range in between
+  // holds nothing.
+  int tok = -1;
+  auto chain = [&](int c0, bool& more) -> unsigned {
+    const int c = c0 + lane * groups;
+    const int4 x = c < ctas ? __ldcg(left + c) : make_int4(-1, 0, -1, 0);
+    if (c0 == cta) tok = __shfl_sync(0xffffffffu, x.z, 0);
+    const bool head = c != cta && x.x == tok;
+    const unsigned ends = __ballot_sync(0xffffffffu, head && !x.y);
+    more = ends == 0 && c0 + 32 * groups < ctas;
+    return __ballot_sync(0xffffffffu, head || c == cta) & (ends == 0 ? 0xffffffffu : (2u << (__ffs(ends) - 1)) - 1u);
+  };
+  const int hb = hg * kJoinHeads;
+  const int heads = min(kJoinHeads, p.H - h0 - hb);
+  if (heads <= 0) return;
+  bool more;
+  unsigned held = chain(cta, more);
+  if (tok < 0) return;
+  float top[kJoinHeads], total[kJoinHeads], o[kChunks][kJoinHeads] = {};
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = fmaf(w[static_cast<int64_t>(hl) * D + d + i], f, o[i]);
+  for (int h = 0; h < kJoinHeads; ++h) {
+    top[h] = h < heads ? __ldg(p.sink + h0 + hb + h) * 1.4426950408889634f : 0.f;
+    total[h] = top[h] == -INFINITY ? 0.f : 0.25f;        // in units of 2^kShift
   }
-  const int64_t row = static_cast<int64_t>(tok) * p.H + h0 + hl;
-  const float inv = total == 0.f ? 0.f : kCodeUnit / total;
+  for (int c0 = cta;;) {
+    const int c = c0 + lane * groups;
+    float4 m = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY), l = make_float4(0.f, 0.f, 0.f, 0.f);
+    if ((held >> lane) & 1u) {
+      m = __ldcg(reinterpret_cast<const float4*>(part(c) + part_o(D) + hb));
+      l = __ldcg(reinterpret_cast<const float4*>(part(c) + part_o(D) + kHeads + hb));
+    }
+    float4 v[kAhead][kChunks];
+    int who[kAhead];
+    auto load = [&] {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) p.o[row * D + d + i] = __float2bfloat16(o[i] * inv);
-  if (d == 0) p.lse[row] = total == 0.f ? -INFINITY : log2f(total) + kShift + top;
+      for (int i = 0; i < kAhead; ++i) {
+        who[i] = held != 0 ? __ffs(held) - 1 : -1;
+        held &= held - 1;
+        if (who[i] >= 0) {
+          const float4* src = reinterpret_cast<const float4*>(part(c0 + who[i] * groups)) + hg * 128 + threadIdx.x;
+#pragma unroll
+          for (int k = 0; k < kChunks; ++k) v[i][k] = __ldcg(src + k * (kHeads / kJoinHeads) * 128);
+        }
+      }
+    };
+    load();
+    const float ms[kJoinHeads] = {m.x, m.y, m.z, m.w}, ls[kJoinHeads] = {l.x, l.y, l.z, l.w};
+    float f[kJoinHeads];
+#pragma unroll
+    for (int h = 0; h < kJoinHeads; ++h) {
+      float t = ms[h];
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+      t = fmaxf(t, top[h]);
+      const float back = top[h] == -INFINITY ? 0.f : exp2f(top[h] - t);  // what came before, under the new maximum
+      f[h] = t == -INFINITY ? 0.f : exp2f(ms[h] - t);
+      top[h] = t;
+      float u = ls[h] * f[h];
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) u += __shfl_xor_sync(0xffffffffu, u, off);
+      total[h] = fmaf(total[h], back, u);
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) o[k][h] *= back;
+    }
+    while (true) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (who[i] < 0) break;
+        float w[kJoinHeads];
+#pragma unroll
+        for (int h = 0; h < kJoinHeads; ++h) w[h] = __shfl_sync(0xffffffffu, f[h], who[i]);
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+          o[k][0] = fmaf(v[i][k].x, w[0], o[k][0]);
+          o[k][1] = fmaf(v[i][k].y, w[1], o[k][1]);
+          o[k][2] = fmaf(v[i][k].z, w[2], o[k][2]);
+          o[k][3] = fmaf(v[i][k].w, w[3], o[k][3]);
+        }
+      }
+      if (held == 0) break;
+      load();
+    }
+    if (!more) break;
+    c0 += 32 * groups;
+    held = chain(c0, more);
+  }
+#pragma unroll
+  for (int h = 0; h < kJoinHeads; ++h) {
+    if (h >= heads) break;
+    const int64_t row = static_cast<int64_t>(tok) * p.H + h0 + hb + h;
+    const float inv = total[h] == 0.f ? 0.f : kCodeUnit / total[h];
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) p.o[row * D + k * 128 + threadIdx.x] = __float2bfloat16(o[k][h] * inv);
+    if (threadIdx.x == 0) p.lse[row] = total[h] == 0.f ? -INFINITY : log2f(total[h]) + kShift + top[h];
+  }
 }
 
+// The most blocks a token can have (one: no token is ever split).
+int64_t blocks_per_token(const smqa_paged_shape& s) {
+  const int64_t slots = s.topk > 0 ? s.topk : static_cast<int64_t>(s.max_pages) * s.page_size;
+  return (slots + kBlk - 1) / kBlk;
+}
+// Whether ranges are whole tokens (index lists: all tokens have the same number
+// of blocks).  Splitting tokens evens the ranges out but costs the parts' way
+// through the workspace and the joining kernel, together about as long as eight
+// blocks take (128 tokens of 16 blocks, 76 ranges: 32 blocks at most per range
+// whole, 27 split).
+bool whole_tokens(const smqa_paged_shape& s) {
+  if (s.topk == 0) return blocks_per_token(s) <= 1;
+  const int groups = (s.H + kHeads - 1) / kHeads;
+  const int64_t parts = 152 / groups, nb = blocks_per_token(s);
+  return (s.T + parts - 1) / parts * nb <= s.T * nb / parts + 8;
+}
 // CTAs of a call: per head group, as many ranges as SMs (or as the tokens can
 // have blocks).
 int ranges_of(const smqa_paged_shape& s) {
   const int groups = (s.H + kHeads - 1) / kHeads;
-  const int64_t slots = s.topk > 0 ? s.topk : static_cast<int64_t>(s.max_pages) * s.page_size;
-  const int64_t blocks = static_cast<int64_t>(s.T) * ((slots + kBlk - 1) / kBlk);
-  return static_cast<int>(std::min<int64_t>(152 / groups, std::max<int64_t>(blocks, 1)));
+  const int64_t most = whole_tokens(s) ? s.T : s.T * blocks_per_token(s);
+  return static_cast<int>(std::min<int64_t>(152 / groups, std::max<int64_t>(most, 1)));
 }
 
 template <int D>
@@ -958,21 +1068,23 @@ cudaError_t launch(const PagedFwdParams& p, int ctas, cudaStream_t stream) {
     return a.numRegs * kThreads >= 2 * 128 * (kSoftmaxRegs + kOtherRegs) ? cudaSuccess : cudaErrorInvalidConfiguration;
   }();
   if (built != cudaSuccess) return built;
-  cudaError_t e = cudaFuncSetAttribute(smqa_paged_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(smqa_paged_fwd_kernel<D>), L::kSmem, allowed);
   if (e != cudaSuccess) return e;
   smqa_paged_fwd_kernel<D><<<ctas, kThreads, L::kSmem, stream>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.whole_tokens) return e;  // nothing to join
+  const bool few = ctas <= 64;                           // then with many parts each
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas) * (kHeads / kJoinHeads));
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.blockDim = dim3(D < 128 ? D : 128);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, smqa_paged_join_kernel<D>, p, ctas);
+  return cudaLaunchKernelEx(&cfg, few ? smqa_paged_join_kernel<D, 8> : smqa_paged_join_kernel<D, 2>, p, ctas);
 }
 
 }  // namespace
@@ -980,12 +1092,15 @@ cudaError_t launch(const PagedFwdParams& p, int ctas, cudaStream_t stream) {
 size_t paged_fwd_workspace(const smqa_paged_shape& s) {
   const int groups = (s.H + kHeads - 1) / kHeads;
   static_assert(152 <= kMaxCtas, "a leftover per CTA");
+  if (whole_tokens(s)) return kLeftoverBytes;
   return kLeftoverBytes + static_cast<size_t>(ranges_of(s)) * groups * 2 * part_floats(s.D) * sizeof(float);
 }
 
 cudaError_t launch_paged_fwd(const PagedFwdParams& p, const smqa_paged_shape& s, cudaStream_t stream) {
   const int ctas = ranges_of(s) * ((s.H + kHeads - 1) / kHeads);
-  return p.D == 512 ? launch<512>(p, ctas, stream) : launch<64>(p, ctas, stream);
+  PagedFwdParams q = p;
+  q.whole_tokens = whole_tokens(s) ? 1 : 0;
+  return p.D == 512 ? launch<512>(q, ctas, stream) : launch<64>(q, ctas, stream);
 }
 
 }  // namespace smqa

@@ -36,25 +36,33 @@ class PagedPlan(NamedTuple):
     slot_mapping: torch.Tensor  # [max_tokens], -1 where there is no page
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+# A step of a server makes a handful of these calls between model layers, and a
+# call's kernel may take less time than Python needs to check its arguments:
+# the checks of a call are one expression, explained tensor by tensor only when
+# it fails, and the stream and device are read without building objects.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_I32, _BF16, _F32, _E4M3 = torch.int32, torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
 
-def _same_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> torch.device:
-    dev = first.device
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors must be on the same device")
-    return dev
+def _explain(why: str, *tensors: tuple) -> None:
+    """Raises what is wrong with the (tensor, name, dtype, ndim) given: the
+    first that is not a contiguous CUDA tensor of its type and rank, or that
+    lies on another device than the first, else ``why``."""
+    for t, name, dtype, ndim in tensors:
+        _need(t, name, dtype, ndim)
+    if len({t.device for t, *_ in tensors}) != 1:
+        raise ValueError("all tensors must be on the same device")
+    raise ValueError(why)
 
 
-def _call(fn: str, device: torch.device, f, *args) -> None:
+def _call(fn: str, device: int, f, *args) -> None:
     """f(*args, current stream of ``device``) with that device current."""
-    if torch.cuda.current_device() == device.index:
-        st = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    if _current_device() == device:
+        st = f(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
-            st = f(*args, torch.cuda.current_stream(device).cuda_stream)
+            st = f(*args, _raw_stream(device))
     if st != _lib.SMQA_OK:
         _lib.check(fn, st)
 
@@ -74,31 +82,45 @@ def paged_plan(context_lens: torch.Tensor, query_lens: torch.Tensor, block_table
     the token outputs; rows behind the last token are -1.  ``inplace`` updates
     block_table and free_count themselves instead of returning new ones.
     """
-    _need(context_lens, "context_lens", torch.int32, 1)
-    _need(query_lens, "query_lens", torch.int32, 1)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(free_pages, "free_pages", torch.int32, 1)
-    _need(free_count, "free_count", torch.int32, 1)
-    R, W = block_table.shape
-    if context_lens.shape[0] != R or query_lens.shape[0] != R or free_count.shape[0] != 1:
-        raise ValueError("context_lens, query_lens and block_table must have the same number of "
-                         "requests, free_count one element")
-    if max_tokens < 0:
-        raise ValueError("max_tokens must not be negative")
-    dev = _same_device(context_lens, query_lens, block_table, free_pages, free_count)
+    try:
+        dev = block_table.get_device()
+        R, W = block_table.shape
+        ok = (dev >= 0 and context_lens.dtype is query_lens.dtype is block_table.dtype
+              is free_pages.dtype is free_count.dtype is _I32
+              and context_lens.get_device() == query_lens.get_device() == free_pages.get_device()
+              == free_count.get_device() == dev
+              and context_lens.shape == query_lens.shape == (R,) and free_count.shape == (1,)
+              and free_pages.ndim == 1 and context_lens.is_contiguous()
+              and query_lens.is_contiguous() and block_table.is_contiguous()
+              and free_pages.is_contiguous() and max_tokens >= 0)
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _explain("context_lens, query_lens and block_table must have the same number of requests, "
+                 "free_count one element, and max_tokens must not be negative",
+                 (context_lens, "context_lens", _I32, 1), (query_lens, "query_lens", _I32, 1),
+                 (block_table, "block_table", _I32, 2), (free_pages, "free_pages", _I32, 1),
+                 (free_count, "free_count", _I32, 1))
     N = int(max_tokens)
     # One allocation: seq_lens, cu_query, token_req, positions, slot_mapping,
     # and the table and count unless they are updated in place.
-    sizes = [R, R + 1, N, N, N] + ([] if inplace else [R * W, 1])
-    out = torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes)
-    table_out, count_out = (block_table, free_count) if inplace else (out[5].view(R, W), out[6])
-    plan = PagedPlan(table_out, count_out, *out[:5])
-    _call("smqa_paged_plan", dev, _lib.load().smqa_paged_plan, _ptr(context_lens),
-          _ptr(query_lens), _ptr(block_table), _ptr(free_pages), _ptr(free_count), R, W,
-          int(page_size), int(n_pages), free_pages.shape[0], N, _ptr(plan.block_table),
-          _ptr(plan.free_count), _ptr(plan.seq_lens), _ptr(plan.cu_query), _ptr(plan.token_req),
-          _ptr(plan.positions), _ptr(plan.slot_mapping))
-    return plan
+    if inplace:
+        sizes, table, count = [R, R + 1, N, N, N], block_table, free_count
+        seq, cu, req, pos, slot = torch.empty(2 * R + 1 + 3 * N, dtype=_I32,
+                                              device=dev).split_with_sizes(sizes)
+    else:
+        sizes = [R, R + 1, N, N, N, 1, R * W]
+        seq, cu, req, pos, slot, count, table = torch.empty(
+            2 * R + 2 + 3 * N + R * W, dtype=_I32, device=dev).split_with_sizes(sizes)
+        table = table.view(R, W)
+    # (The outputs lie one behind another.)
+    at = seq.data_ptr()
+    _call("smqa_paged_plan", dev, _lib.load().smqa_paged_plan, context_lens.data_ptr(),
+          query_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
+          free_count.data_ptr(), R, W, int(page_size), int(n_pages), free_pages.shape[0], N,
+          table.data_ptr(), count.data_ptr(), at, at + 4 * R, at + 8 * R + 4,
+          at + 8 * R + 4 + 4 * N, at + 8 * R + 4 + 8 * N)
+    return PagedPlan(table, count, seq, cu, req, pos, slot)
 
 
 def paged_release(block_table: torch.Tensor, release: torch.Tensor, free_pages: torch.Tensor,
@@ -107,29 +129,21 @@ def paged_release(block_table: torch.Tensor, release: torch.Tensor, free_pages: 
     """Gives back the pages of the requests r with release[r] (bool [R]): in
     place, their block_table entries in [0, n_pages) go on the stack
     (free_pages, free_count) and become -1; their seq_lens, if given, 0."""
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(release, "release", torch.bool, 1)
-    _need(free_pages, "free_pages", torch.int32, 1)
-    _need(free_count, "free_count", torch.int32, 1)
-    R, W = block_table.shape
+    tensors = [(block_table, "block_table", _I32, 2), (release, "release", torch.bool, 1),
+               (free_pages, "free_pages", _I32, 1), (free_count, "free_count", _I32, 1)]
     if seq_lens is not None:
-        _need(seq_lens, "seq_lens", torch.int32, 1)
-        if seq_lens.shape[0] != R:
-            raise ValueError(f"seq_lens must have R={R} entries")
-    if release.shape[0] != R or free_count.shape[0] != 1:
-        raise ValueError(f"release must have R={R} entries, free_count one element")
-    dev = _same_device(block_table, release, free_pages, free_count, seq_lens)
-    _call("smqa_paged_release", dev, _lib.load().smqa_paged_release, _ptr(block_table),
-          _ptr(seq_lens), _ptr(release), R, W, int(n_pages), _ptr(free_pages), _ptr(free_count),
+        tensors.append((seq_lens, "seq_lens", _I32, 1))
+    for t in tensors:
+        _need(*t)
+    R, W = block_table.shape
+    if release.shape[0] != R or free_count.shape[0] != 1 or \
+            (seq_lens is not None and seq_lens.shape[0] != R) or \
+            len({t.device for t, *_ in tensors}) != 1:
+        _explain(f"release and seq_lens must have R={R} entries, free_count one element", *tensors)
+    _call("smqa_paged_release", block_table.get_device(), _lib.load().smqa_paged_release,
+          block_table.data_ptr(), None if seq_lens is None else seq_lens.data_ptr(),
+          release.data_ptr(), R, W, int(n_pages), free_pages.data_ptr(), free_count.data_ptr(),
           free_pages.shape[0])
-
-
-def _need_cache(kv_cache: torch.Tensor, kv_scales: torch.Tensor) -> tuple:
-    _need(kv_cache, "kv_cache", torch.float8_e4m3fn, 3)
-    _need(kv_scales, "kv_scales", torch.float32, 1)
-    if kv_scales.shape[0] != kv_cache.shape[0]:
-        raise ValueError("kv_scales must have one entry per page of kv_cache")
-    return kv_cache.shape
 
 
 def paged_kv_append(kv_new: torch.Tensor, slot_mapping: torch.Tensor, kv_cache: torch.Tensor,
@@ -143,16 +157,27 @@ def paged_kv_append(kv_new: torch.Tensor, slot_mapping: torch.Tensor, kv_cache: 
     rescaled) and starts afresh when the page's first row is written.  The rows
     of one page must be consecutive, with slots ascending by one, as
     paged_plan lists them."""
-    n_pages, page_size, D = _need_cache(kv_cache, kv_scales)
-    _need(kv_new, "kv_new", torch.bfloat16, 2)
-    _need(slot_mapping, "slot_mapping", torch.int32, 1)
-    T = kv_new.shape[0]
-    if kv_new.shape[1] != D or slot_mapping.shape[0] != T:
-        raise ValueError(f"kv_new {tuple(kv_new.shape)} does not match kv_cache "
-                         f"{tuple(kv_cache.shape)} and slot_mapping {tuple(slot_mapping.shape)}")
-    dev = _same_device(kv_cache, kv_scales, kv_new, slot_mapping)
-    _call("smqa_paged_append", dev, _lib.load().smqa_paged_append, _ptr(kv_new),
-          _ptr(slot_mapping), T, D, page_size, n_pages, _ptr(kv_cache), _ptr(kv_scales))
+    try:
+        dev = kv_cache.get_device()
+        n_pages, page_size, D = kv_cache.shape
+        T = kv_new.shape[0]
+        ok = (dev >= 0 and kv_cache.dtype is _E4M3 and kv_scales.dtype is _F32
+              and kv_new.dtype is _BF16 and slot_mapping.dtype is _I32
+              and kv_scales.get_device() == kv_new.get_device() == slot_mapping.get_device() == dev
+              and kv_scales.shape == (n_pages,) and kv_new.shape == (T, D)
+              and slot_mapping.shape == (T,) and kv_cache.is_contiguous()
+              and kv_scales.is_contiguous() and kv_new.is_contiguous()
+              and slot_mapping.is_contiguous())
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _explain("kv_cache [n_pages,page_size,D], kv_scales [n_pages], kv_new [T,D] and "
+                 "slot_mapping [T] do not have matching shapes",
+                 (kv_cache, "kv_cache", _E4M3, 3), (kv_scales, "kv_scales", _F32, 1),
+                 (kv_new, "kv_new", _BF16, 2), (slot_mapping, "slot_mapping", _I32, 1))
+    _call("smqa_paged_append", dev, _lib.load().smqa_paged_append, kv_new.data_ptr(),
+          slot_mapping.data_ptr(), T, D, page_size, n_pages, kv_cache.data_ptr(),
+          kv_scales.data_ptr())
     return kv_cache, kv_scales
 
 
@@ -185,55 +210,68 @@ def sparse_mqa_paged_fwd(q: torch.Tensor, kv_cache: torch.Tensor, kv_scales: tor
     ``check_status`` the call synchronizes and raises SMQAError
     (SMQA_ERR_DEVICE_TIMEOUT) if a kernel's bounded wait ran out.
     """
-    _need(q, "q", torch.bfloat16, 3)
-    n_pages, page_size, D = _need_cache(kv_cache, kv_scales)
-    _need(attn_sink, "attn_sink", torch.float32, 1)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    _need(token_req, "token_req", torch.int32, 1)
-    T, H, Dq = q.shape
-    R, W = block_table.shape
-    if Dq != D or attn_sink.shape[0] != H or seq_lens.shape[0] != R or token_req.shape[0] != T:
-        raise ValueError("q, kv_cache, attn_sink, block_table, seq_lens and token_req do not have "
-                         "matching shapes")
-    topk = 0
-    if positions is not None:
-        _need(positions, "positions", torch.int32, 1)
-        if positions.shape[0] != T:
-            raise ValueError(f"positions must have T={T} entries")
-    if topk_idxs is not None:
-        _need(topk_idxs, "topk_idxs", torch.int32, 2)
-        topk = topk_idxs.shape[1]
-        if topk_idxs.shape[0] != T or topk == 0:
-            raise ValueError(f"topk_idxs must be [T={T}, topk >= 1]")
-    elif positions is None:
-        raise ValueError("positions is needed without topk_idxs")
-    dev = _same_device(q, kv_cache, kv_scales, attn_sink, block_table, seq_lens, token_req,
-                       positions, topk_idxs, workspace)
-    scale = _scale(sm_scale, D)
+    try:
+        dev = q.get_device()
+        T, H, D = q.shape
+        n_pages, page_size, _ = kv_cache.shape
+        R, W = block_table.shape
+        topk = 0 if topk_idxs is None else topk_idxs.shape[1]
+        ok = (dev >= 0 and q.dtype is _BF16 and kv_cache.dtype is _E4M3
+              and kv_scales.dtype is attn_sink.dtype is _F32
+              and block_table.dtype is seq_lens.dtype is token_req.dtype is _I32
+              and kv_cache.get_device() == kv_scales.get_device() == attn_sink.get_device()
+              == block_table.get_device() == seq_lens.get_device() == token_req.get_device() == dev
+              and kv_cache.shape[2] == D and kv_scales.shape == (n_pages,)
+              and attn_sink.shape == (H,) and seq_lens.shape == (R,) and token_req.shape == (T,)
+              and q.is_contiguous() and kv_cache.is_contiguous() and kv_scales.is_contiguous()
+              and attn_sink.is_contiguous() and block_table.is_contiguous()
+              and seq_lens.is_contiguous() and token_req.is_contiguous()
+              and (topk_idxs is not None or positions is not None)
+              and (positions is None or (
+                  positions.dtype is _I32 and positions.get_device() == dev
+                  and positions.shape == (T,) and positions.is_contiguous()))
+              and (topk_idxs is None or (
+                  topk_idxs.dtype is _I32 and topk_idxs.get_device() == dev and topk > 0
+                  and topk_idxs.shape == (T, topk) and topk_idxs.is_contiguous()))
+              and (workspace is None or (
+                  workspace.dtype is torch.uint8 and workspace.get_device() == dev
+                  and workspace.ndim == 1 and workspace.is_contiguous())))
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        more = [(positions, "positions", _I32, 1), (topk_idxs, "topk_idxs", _I32, 2),
+                (workspace, "workspace", torch.uint8, 1)]
+        _explain("q [T,H,D], kv_cache [n_pages,page_size,D], kv_scales [n_pages], attn_sink [H], "
+                 "block_table [R,max_pages], seq_lens [R], token_req [T] and positions [T] or "
+                 "topk_idxs [T,topk >= 1] (one of them is needed) do not have matching shapes",
+                 (q, "q", _BF16, 3), (kv_cache, "kv_cache", _E4M3, 3),
+                 (kv_scales, "kv_scales", _F32, 1), (attn_sink, "attn_sink", _F32, 1),
+                 (block_table, "block_table", _I32, 2), (seq_lens, "seq_lens", _I32, 1),
+                 (token_req, "token_req", _I32, 1), *[t for t in more if t[0] is not None])
+    scale = D ** -0.5 if sm_scale is None else _scale(sm_scale, D)
     shp = _lib.PagedShape(T, R, H, D, topk, page_size, W, n_pages)
     lib = _lib.load()
     need = lib.smqa_paged_fwd_workspace_bytes(shp)
-    if workspace is not None:
-        _need(workspace, "workspace", torch.uint8, 1)
     if need > 0 and (workspace is None or workspace.numel() < need):
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if out is None:
         o = torch.empty_like(q)
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        lse = torch.empty((T, H), dtype=_F32, device=dev)
         flags = _lib.FLAG_ZERO_PADDING
     else:
         o, lse = out
-        _need(o, "out[0]", torch.bfloat16, 3)
-        _need(lse, "out[1]", torch.float32, 2)
-        if o.shape != q.shape or tuple(lse.shape) != (T, H):
-            raise ValueError("out must be (o like q, lse [T,H])")
-        _same_device(q, o, lse)
+        _need(o, "out[0]", _BF16, 3)
+        _need(lse, "out[1]", _F32, 2)
+        if o.shape != q.shape or lse.shape != (T, H) or o.device != q.device or \
+                lse.device != q.device:
+            raise ValueError("out must be (o like q, lse [T,H]) on q's device")
         flags = 0
-    _call("smqa_paged_fwd", dev, lib.smqa_paged_fwd, _ptr(q), _ptr(kv_cache), _ptr(kv_scales),
-          _ptr(attn_sink), _ptr(block_table), _ptr(seq_lens), _ptr(token_req), _ptr(positions),
-          _ptr(topk_idxs), shp, scale, _ptr(o), _ptr(lse), _ptr(workspace),
+    _call("smqa_paged_fwd", dev, lib.smqa_paged_fwd, q.data_ptr(), kv_cache.data_ptr(),
+          kv_scales.data_ptr(), attn_sink.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+          token_req.data_ptr(), None if positions is None else positions.data_ptr(),
+          None if topk_idxs is None else topk_idxs.data_ptr(), shp, scale, o.data_ptr(),
+          lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
           0 if workspace is None else workspace.numel(), flags)
     if check_status:
-        _check_device(dev, "smqa_paged_fwd")
+        _check_device(q.device, "smqa_paged_fwd")
     return o, lse
