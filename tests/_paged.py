@@ -8,9 +8,11 @@ of fp32):
           row's largest value; the fp32 sum of D products adds the rest) +
           4 eps |x_j| (scale factors, and the running maximum's subtraction)
   weight  two e4m3 pieces of its value in fp16: 2^-4 of 2^-4 of the weight, and
-          2^-11 for the step through fp16, relative; and 2^-16 of the token's
-          largest weight (p_j s_j) where the second piece is subnormal; 2^-21
-          for exp2
+          2^-11 for the step through fp16, relative; and 2^-14 of the token's
+          largest weight (p_j s_j) where the second piece is subnormal: codes
+          are multiples of 2^-9, so it is off by 2^-10 at most, and the largest
+          weight's code is at least 2^(8 - 2 - 2) = 2^4 (m starts 2 above the
+          first block's maximum, and weights are 2^-2 2^8 at m); 2^-21 for exp2
   O       2^-9 relative for its own rounding to bf16, the weights' error times
           |k_jd|, n eps for the fp32 sums
   lse     max_j |dx_j| / ln 2, exp2 and sums (2^-21 + n eps) / ln 2, and
@@ -126,7 +128,7 @@ def attn(q, val, scale, sink, table, seq, req, pos=None, idx=None, sm_scale=None
         w = p * s
         rel = torch.expm1(dx) + 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -21 + j.numel() * eps
         bo[t] = (2.0 ** -9 * o[t].abs() + (rel * p) @ k.abs() / l
-                 + 2.0 ** -16 * w.amax(1, keepdim=True) / l * c.abs().sum(0)[None, :]
+                 + 2.0 ** -14 * w.amax(1, keepdim=True) / l * c.abs().sum(0)[None, :]
                  + o[t].abs() * (torch.expm1(dx.amax(1, keepdim=True)) + 2.0 ** -21 + j.numel() * eps))
         bl[t] = (dx.amax(1) + 2.0 ** -21 + j.numel() * eps) / math.log(2.0) + 2.0 ** -22 * (1 + lse[t].abs())
     return o, lse, bo, bl
