@@ -18,10 +18,9 @@
 //        to 2^-14 of the largest weight.  m is set 2 above the maximum of y of
 //        the token's first block, so that the largest weight's code is 2^4 at
 //        least, and may fall 2.75 behind the running maximum (2^8.75 < 448,
-//        e4m3's largest) before O is rescaled, which holds the pipeline up:
-//        with page scales up to 2^3 apart a quarter of the blocks do it, with
-//        equal ones none (without the 2 above: 61 % and 13 %).  l adds w / s_j
-//        in fp32.
+//        e4m3's largest) before O is rescaled, which holds the pipeline up
+//        (128 tokens H=128 topk=2048, page scales up to 2^3 apart: 84.4 us
+//        with m at the maximum, 82.4 us so).  l adds w / s_j in fp32.
 //        An fp16 number below 2 holds an e4m3 code of its 2^8-fold in bits
 //        7-13 (and the sign), subnormals included, so both pieces come from
 //        integer operations on pairs of fp16: the conversion instructions
@@ -36,10 +35,10 @@
 // side in neighbouring CTAs, so its rows come from HBM once.
 //
 // Per block (D = 512), 512 threads, one CTA per SM:
-//   gather (warps 9-15)  slot -> page -> row, and the rows by 16-byte cp.async
+//   gather (warps 12-15) slot -> page -> row, and the rows by 16-byte cp.async
 //                        into a 128-byte-swizzled tile [D/128][128 slots][128],
-//                        three tiles in a ring, 32 rows of a tile freed and
-//                        refilled at a time; the slots' scale factors;
+//                        three tiles in a ring, a warp's 32 rows freed and
+//                        refilled on their own; the slots' scale factors;
 //   MMA (warp 8)         S = Q.K^T: M = 128 (64 heads x 2 pieces, A in TMEM),
 //                        N = 128 slots; O^T += V^T.P^T: M = 128 of D (A: the
 //                        same tile read MN-major, kept in the collector for
@@ -64,19 +63,18 @@ namespace smqa {
 
 namespace {
 
-constexpr int kBlk = 64;                  // slots per block
+constexpr int kBlk = 128;                 // slots per block
 constexpr int kHeads = 64;                // heads per CTA
 constexpr int kThreads = 512;
 constexpr int kSoftmaxThreads = 256;
-constexpr int kMmaWarp = 8, kGatherWarp0 = 12, kGatherWarps = 4;
+constexpr int kMmaWarp = 8, kGatherWarp0 = 12;
 // Registers per thread of the softmax warpgroups and of the other two: their
 // sum is what the block is launched with (128 a thread).
 constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
 static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs <= 512, "registers of the launch");
 // Warps 0-7 take more registers, 8-15 give some back: a warpgroup does one of
 // the two as a whole, or none of its warps would go on.
-static_assert(kSoftmaxThreads == 256 && kMmaWarp == 8 && kGatherWarp0 + kGatherWarps == 16 && kThreads == 512,
-              "roles by warpgroup");
+static_assert(kSoftmaxThreads == 256 && kMmaWarp == 8 && kGatherWarp0 == 12 && kThreads == 512, "roles by warpgroup");
 constexpr float kShift = 2.f;             // weights are 2^-2 at m
 constexpr float kAbove = 2.f;             // how far m is set above the maximum
 constexpr float kLag = 2.75f;             // and how far it may fall behind
@@ -100,15 +98,15 @@ struct PagedLayout {
   static constexpr int kChunks = D < 128 ? 1 : D / 128;      // 128-byte pieces of a row
   static constexpr uint32_t kChunkBytes = kBlk * 128;
   static constexpr uint32_t kStageBytes = kChunks * kChunkBytes;
-  static constexpr int kStages = D == 512 ? 6 : 8;
-  static constexpr uint32_t kPBytes = kHeads * 128;          // P^T: per head 64 slots' hi, then lo pieces
+  static constexpr int kStages = D == 512 ? 3 : 6;
+  static constexpr uint32_t kPieceBytes = kHeads * 128;      // one piece of P^T: 64 heads x 128 slots
   static constexpr uint32_t kQStage = 32 * 64;               // per softmax warp, in P's place: 32 rows x 64 bytes
-  static_assert(8 * kQStage <= 2 * kPBytes, "Q staging fits P");
+  static_assert(8 * kQStage <= 2 * kPieceBytes, "Q staging fits P");
   // Per stage and slot pair (a0, a1, c0, c1), then the r of all slots, two
   // pairs of one lane together (meta_at, rec_at).
   static constexpr int kMeta = 4 * kBlk / 2 + kBlk;          // floats
   static constexpr uint32_t kOffP = kStages * kStageBytes;
-  static constexpr uint32_t kOffA = kOffP + 2 * kPBytes; // [kStages][kMeta]: a, c, r
+  static constexpr uint32_t kOffA = kOffP + 2 * kPieceBytes; // [kStages][kMeta]: a, c, r
   static constexpr uint32_t kOffFlags = kOffA + kStages * kMeta * 4;  // [kStages]
   static constexpr uint32_t kOffHead = (kOffFlags + kStages * 4 + 15) & ~15u;  // float [64]
   static constexpr uint32_t kOffMax = kOffHead + kHeads * 4;   // uint32 [2][64] (QLoader)
@@ -117,12 +115,12 @@ struct PagedLayout {
   static constexpr uint32_t kOffNotes = kOffEnd + kHeads * 4;  // Note [kNotes]
   static constexpr uint32_t kOffBar = kOffNotes + kNotes * sizeof(Note);
   static constexpr int kBarFull = 0;                         // [kStages]
-  static constexpr int kBarEmpty = kBarFull + kStages;       // [kStages][2], 32 rows each
-  static constexpr int kBarSFull = kBarEmpty + 2 * kStages;  // [2], as the rest: of even and odd entries
-  static constexpr int kBarSFree = kBarSFull + 2;
-  static constexpr int kBarPFull = kBarSFree + 2;
-  static constexpr int kBarPDone = kBarPFull + 2;            // P and its tile used, O up to date
-  static constexpr int kBarNote = kBarPDone + 2;             // [2] a warpgroup's note is written
+  static constexpr int kBarEmpty = kBarFull + kStages;       // [kStages][4], a gather warp's rows
+  static constexpr int kBarSFull = kBarEmpty + 4 * kStages;
+  static constexpr int kBarSFree = kBarSFull + 1;
+  static constexpr int kBarPFull = kBarSFree + 1;
+  static constexpr int kBarPDone = kBarPFull + 1;            // P and its tile used, O up to date
+  static constexpr int kBarNote = kBarPDone + 1;             // [2] a warpgroup's note is written
   static constexpr int kBarQFull = kBarNote + 2;
   static constexpr int kBarDrain = kBarQFull + 1;
   static constexpr int kNumBars = kBarDrain + 1;
@@ -143,9 +141,8 @@ struct Range {
   int64_t count;
 };
 
-// Flags of a ring entry: its token's first, its last, the CTA's last, and
-// whether the next entry is its token's last.
-enum : int { kFirst = 1, kLast = 2, kFinal = 4, kNextLast = 8 };
+// Flags of a ring entry.
+enum : int { kFirst = 1, kLast = 2, kFinal = 4 };
 
 // What a CTA leaves in the workspace: the token its range starts inside of
 // (-1: none) and whether that token goes on behind the range, and the token
@@ -178,6 +175,29 @@ __device__ __forceinline__ int blocks_of(const PagedFwdParams& p, int t) {
   return max(1, (slots_of(p, t, req, __ldg(p.seq_lens + req)) + kBlk - 1) / kBlk);
 }
 
+// The two e4m3 pieces of 2^8 w for four weights 0 <= w <= 1.6875: hi the
+// nearest code (halves up), lo that of the rest.
+__device__ __forceinline__ void split_e4m3x4(float2 w01, float2 w23, uint32_t& hi, uint32_t& lo) {
+  const __half2 a = __floats2half2_rn(w01.x, w01.y), b = __floats2half2_rn(w23.x, w23.y);
+  const uint32_t ra = *reinterpret_cast<const uint32_t*>(&a) + 0x00400040u;
+  const uint32_t rb = *reinterpret_cast<const uint32_t*>(&b) + 0x00400040u;
+  hi = __byte_perm(ra << 1, rb << 1, 0x7531);
+  const uint32_t ka = ra & 0xff80ff80u, kb = rb & 0xff80ff80u;
+  const __half2 da = __hsub2(a, *reinterpret_cast<const __half2*>(&ka));
+  const __half2 db = __hsub2(b, *reinterpret_cast<const __half2*>(&kb));
+  const uint32_t sa = *reinterpret_cast<const uint32_t*>(&da) + 0x00400040u;
+  const uint32_t sb = *reinterpret_cast<const uint32_t*>(&db) + 0x00400040u;
+  // The sign next to the code (bit 14 is free: the values are below 2).
+  lo = __byte_perm((sa | ((sa >> 1) & 0x40004000u)) << 1, (sb | ((sb >> 1) & 0x40004000u)) << 1, 0x7531);
+}
+
+// Where slot n's factors a and c (+ 2) lie among a stage's floats, and its r:
+// the softmax lane q of a quad takes the slot pairs 8j + 2q, two j at a time.
+__device__ __forceinline__ int meta_at(int n) { return (n >> 1) * 4 + (n & 1); }
+__device__ __forceinline__ int rec_at(int n) {
+  return 2 * kBlk + (n >> 4) * 16 + ((n >> 1) & 3) * 4 + ((n >> 3) & 1) * 2 + (n & 1);
+}
+
 // The e4m3 codes of 2^8 x for four fp16 values |x| <= 1.6875 (nearest, halves
 // away from 0), and the rounded values.
 __device__ __forceinline__ uint32_t round_e4m3x4(__half2 a, __half2 b, __half2& ra, __half2& rb) {
@@ -188,23 +208,6 @@ __device__ __forceinline__ uint32_t round_e4m3x4(__half2 a, __half2 b, __half2& 
   rb = *reinterpret_cast<const __half2*>(&kb);
   // The sign next to the code (bit 14 is free: the values are below 2).
   return __byte_perm((sa | ((sa >> 1) & 0x40004000u)) << 1, (sb | ((sb >> 1) & 0x40004000u)) << 1, 0x7531);
-}
-// Both pieces of four weights 0 <= w <= 1.6875: the code hi, and that of the rest.
-__device__ __forceinline__ void split_e4m3x4(float2 w01, float2 w23, uint32_t& hi, uint32_t& lo) {
-  const __half2 a = __floats2half2_rn(w01.x, w01.y), b = __floats2half2_rn(w23.x, w23.y);
-  const uint32_t sa = *reinterpret_cast<const uint32_t*>(&a) + 0x00400040u;
-  const uint32_t sb = *reinterpret_cast<const uint32_t*>(&b) + 0x00400040u;
-  hi = __byte_perm(sa << 1, sb << 1, 0x7531);            // (no sign to move)
-  const uint32_t ka = sa & 0xff80ff80u, kb = sb & 0xff80ff80u;
-  __half2 ra, rb;
-  lo = round_e4m3x4(__hsub2(a, *reinterpret_cast<const __half2*>(&ka)), __hsub2(b, *reinterpret_cast<const __half2*>(&kb)), ra, rb);
-}
-
-// Where slot n's factors a and c (+ 2) lie among a stage's floats, and its r:
-// the softmax lane q of a quad takes the slot pairs 8j + 2q, two j at a time.
-__device__ __forceinline__ int meta_at(int n) { return (n >> 1) * 4 + (n & 1); }
-__device__ __forceinline__ int rec_at(int n) {
-  return 2 * kBlk + (n >> 4) * 16 + ((n >> 1) & 3) * 4 + ((n >> 3) & 1) * 2 + (n & 1);
 }
 
 // Q of a token, heads h0.. (`heads` of them, zeros behind), by the eight softmax
@@ -323,15 +326,14 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
   int* end_tok = reinterpret_cast<int*>(smem + L::kOffRange + 16 + 128);     // token, its end, its begin
 
   if (tid == 0) {
-    for (int i = 0; i < L::kStages; ++i) mbar_init(bar(L::kBarFull + i), 66);  // copies landed, factors written
-    for (int i = 0; i < 2 * L::kStages; ++i) mbar_init(bar(L::kBarEmpty + i), 1);
-    for (int i = 0; i < 2; ++i) {                        // (one arrival per warp of a warpgroup)
-      mbar_init(bar(L::kBarSFull + i), 2);               // S formed; its rows' factors passed on
-      mbar_init(bar(L::kBarSFree + i), 4);
-      mbar_init(bar(L::kBarPFull + i), 4);
-      mbar_init(bar(L::kBarPDone + i), 1);
-      mbar_init(bar(L::kBarNote + i), 4);
-    }
+    for (int i = 0; i < L::kStages; ++i) mbar_init(bar(L::kBarFull + i), 128 + 4);  // copies landed, factors written
+    for (int i = 0; i < 4 * L::kStages; ++i) mbar_init(bar(L::kBarEmpty + i), 1);
+    mbar_init(bar(L::kBarSFull), 1);
+    mbar_init(bar(L::kBarSFree), kSoftmaxThreads / 64);  // (one arrival per warp)
+    mbar_init(bar(L::kBarPFull), kSoftmaxThreads / 64);
+    mbar_init(bar(L::kBarPDone), 1);
+    mbar_init(bar(L::kBarNote), kSoftmaxThreads / 64);
+    mbar_init(bar(L::kBarNote + 1), kSoftmaxThreads / 64);
     mbar_init(bar(L::kBarQFull), kSoftmaxThreads / 32);
     mbar_init(bar(L::kBarDrain), 1);
     *abort_flag = *reinterpret_cast<volatile int*>(p.status) != 0 ? 1 : 0;
@@ -410,28 +412,31 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
     reinterpret_cast<Leftover*>(p.ws)[blockIdx.x] = l;
   }
 
+  // Padding tokens belong to no range; warps without another role see to them.
+  if (p.zero_padding && warp > kMmaWarp && warp < kGatherWarp0)
+    for (int t = blockIdx.x + (warp - kMmaWarp - 1) * gridDim.x; t < p.T; t += gridDim.x * (kGatherWarp0 - kMmaWarp - 1))
+      if (!live_token(p, __ldg(p.token_req + t))) {
+        uint4* o = reinterpret_cast<uint4*>(p.o + static_cast<int64_t>(t) * p.H * D);
+        for (int i = lane; i < p.H * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+        for (int h = lane; h < p.H; h += 32) p.lse[static_cast<int64_t>(t) * p.H + h] = -INFINITY;
+      }
+
   if (rg.count > 0 && warp >= kGatherWarp0) {
     reg_dealloc<kOtherRegs>();
     // ------------------------------------------------------------ gather
     // Looking a slot up takes three loads, one after another: while the rows
     // of one block are copied, the next block's indices and then its pages
     // arrive.
-    // Blocks are looked up two at a time, 32 slots per warp; a warp copies rows
-    // of one of the two.
     const int pw = warp - kGatherWarp0;
-    const int my = 32 * pw + lane;                       // this lane's slot of the two blocks
-    const int second = pw >> 1;                          // the warp's block of the two
+    const int my = 32 * pw + lane;                       // this thread's slot of a block
     int64_t left = rg.count;                             // blocks behind the current token's
     int t = rg.tok - 1, b = 0, stop = 0, n = 0, len = 0;
     const int32_t *idx_row = nullptr, *tab = nullptr;
     bool fresh = true;                                   // no block of this token yet
-    bool done = false;                                   // these are the range's last blocks
     int idx[4];                                          // of slots 32 k + lane
-    b = -2;
-    // Goes to the next two blocks and asks for their indices.
+    // Goes to the next block and asks for its indices.
     auto ask = [&] {
-      b += 2;
-      if (b >= stop) {
+      if (++b >= stop) {
         int nb;
         do nb = blocks_of(p, ++t);
         while (nb == 0);
@@ -440,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
         stop = static_cast<int>(min(static_cast<int64_t>(nb), b + left));
         left -= stop - b;
         len = __ldg(p.seq_lens + req);
-        n = min(slots_of(p, t, req, len), stop * kBlk);
+        n = slots_of(p, t, req, len);
         tab = p.table + static_cast<int64_t>(req) * p.max_pages;
         idx_row = p.idx ? p.idx + static_cast<int64_t>(t) * p.topk : nullptr;
         fresh = true;
@@ -452,43 +457,30 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
           idx[k] = j < n ? __ldg(idx_row + j) : -1;
         }
     };
-    // This slot's position in its page and its page (-1: masked); how many
-    // entries the two blocks make, this warp's among them (-1: none) and its
-    // flags.  A block without any slot left makes none, but for a token's last,
+    // This slot's position in its page and its page (-1: masked); the block's
+    // flags.  A block without any slot left is passed over, but for the last,
     // which carries the token's end.
-    int in_page = 0, page = -1, flags = 0, entries = 0, entry = -1;
-    bool alone = false;                                  // they make one entry, the token's last
+    int in_page = 0, page = -1, flags = 0;
     auto look = [&] {
       int pos = -1;
-      bool any0, any1, last;
       while (true) {
-        last = b + 2 >= stop;
-        if (idx_row) {
-          bool in[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            in[k] = idx[k] >= 0 && idx[k] < len;
-            if (k == pw && in[k]) pos = idx[k];
-          }
-          any0 = __any_sync(0xffffffffu, in[0] || in[1]);
-          any1 = __any_sync(0xffffffffu, in[2] || in[3]);
-        } else {
-          any0 = b * kBlk < n;
-          any1 = (b + 1) * kBlk < n;
+        if (!idx_row) {
           if (b * kBlk + my < n) pos = b * kBlk + my;
+          break;
         }
-        if (any0 || any1 || last) break;
+        unsigned any = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool in = idx[k] >= 0 && idx[k] < len;
+          any |= __ballot_sync(0xffffffffu, in);
+          if (k == pw && in) pos = idx[k];
+        }
+        if (any != 0 || b + 1 == stop) break;
         ask();
       }
-      any0 = any0 || !any1;
-      entries = (any0 ? 1 : 0) + (any1 ? 1 : 0);
-      entry = second ? (any1 ? entries - 1 : -1) : (any0 ? 0 : -1);
-      const bool ends = last && entry == entries - 1;
-      flags = (fresh && entry == 0 ? kFirst : 0) | (ends ? kLast : 0) | (ends && left == 0 ? kFinal : 0);
-      if (last && entries == 2 && entry == 0) flags |= kNextLast;
+      const bool last = b + 1 == stop;
+      flags = (fresh ? kFirst : 0) | (last ? kLast : 0) | (last && left == 0 ? kFinal : 0);
       fresh = false;
-      done = last && left == 0;
-      alone = last && entries == 1;
       const int col = pos >> p.page_shift;
       in_page = pos & ((1 << p.page_shift) - 1);
       page = pos >= 0 && col < p.max_pages ? __ldg(tab + col) : -1;
@@ -504,30 +496,24 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
     };
     ask();
     look();
-    for (int e0 = 0;;) {                                 // the ring's entries so far
+    for (int e = 0;; ++e) {
       const bool live = static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages);
       const int row = live ? (page << p.page_shift) + in_page : 0;
       const float s = live ? __ldg(p.scales + page) : 1.f;
       const unsigned mask = __ballot_sync(0xffffffffu, live);
-      int now = flags;
-      const int e = e0 + entry;
-      const bool on = entry >= 0, over = done, tail = entry == entries - 1;
-      e0 += entries;
-      if (!over) ask();
+      const int now = flags;
+      if (!(now & kFinal)) ask();
       const int st = e % L::kStages;
-      if (on) {
-        bool ok = *abort_flag == 0;
-        if (e >= L::kStages)
-          ok = mbar_wait(bar(L::kBarEmpty + 2 * st + (pw & 1)), ((e / L::kStages) - 1) & 1, ctl);
-        if (!__all_sync(0xffffffffu, ok)) break;
+      if (e >= L::kStages) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(L::kBarEmpty + 4 * st + pw), ((e / L::kStages) - 1) & 1, ctl))) break;
       } else if (!__all_sync(0xffffffffu, *abort_flag == 0)) {
         break;
       }
+      const uint32_t tile = base + static_cast<uint32_t>(st) * L::kStageBytes;
       // An instruction copies 128 bytes (D = 64: 64) of each of several rows:
       // a row's address is fetched from its lane once, its further pieces are
       // at fixed distances (4 warps: 52 bytes a clock from L2, against 38 with
       // one whole row per instruction).
-      const uint32_t tile = base + static_cast<uint32_t>(st) * L::kStageBytes;
       constexpr int kLanes = D < 128 ? D / 16 : 8;       // lanes per row
       constexpr int kRows = 32 / kLanes;                 // rows per instruction
       const int sub = lane / kLanes, cc = lane % kLanes;
@@ -535,36 +521,31 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       auto copy = [&](int g) {                           // rows g kRows + sub of the warp's 32
         const int rw = g * kRows + sub;
         const uint8_t* from = src + static_cast<int64_t>(__shfl_sync(0xffffffffu, row, rw)) * D;
-        const bool is = (mask >> rw) & 1u;
-        const uint32_t to = tile + static_cast<uint32_t>(32 * (pw & 1) + rw) * 128u + ((static_cast<uint32_t>(cc) ^ (static_cast<uint32_t>(rw) & 7u)) << 4);
+        const bool on = (mask >> rw) & 1u;
+        const uint32_t to = tile + static_cast<uint32_t>(32 * pw + rw) * 128u + ((static_cast<uint32_t>(cc) ^ (static_cast<uint32_t>(rw) & 7u)) << 4);
 #pragma unroll
-        for (int c = 0; c < L::kChunks; ++c) cp_async_16_or_zero(to + c * L::kChunkBytes, from + c * 128, is);
+        for (int c = 0; c < L::kChunks; ++c) cp_async_16_or_zero(to + c * L::kChunkBytes, from + c * 128, on);
       };
-      if (on)
-#pragma unroll 2
-        for (int g = 0; g < 16 / kRows; ++g) copy(g);
-      if (!over) look();
-      if (!over && tail && !(now & kLast) && alone) now |= kNextLast;
-      if (on) {
-#pragma unroll 2
-        for (int g = 16 / kRows; g < 32 / kRows; ++g) copy(g);
-        // y = S a + c, l += w r: a masked slot's row is zero, its c -inf.
-        float* m = reinterpret_cast<float*>(smem + L::kOffA) + st * L::kMeta;
-        const int at = my & (kBlk - 1);
-        m[meta_at(at)] = live ? s * p.scale_log2 : 0.f;
-        m[meta_at(at) + 2] = live ? log2f(s) : -INFINITY;
-        m[rec_at(at)] = live ? 1.f / s : 0.f;
-        if (at == 0) reinterpret_cast<int*>(smem + L::kOffFlags)[st] = now;
-        cp_async_arrive_noinc(bar(L::kBarFull + st));    // once the copies have landed
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kBarFull + st));  // releases the factors
-      }
-      if (over) break;
-      prefetch();
+#pragma unroll
+      for (int g = 0; g < 16 / kRows; ++g) copy(g);
+      if (!(now & kFinal)) look();
+#pragma unroll
+      for (int g = 16 / kRows; g < 32 / kRows; ++g) copy(g);
+      // y = S a + c, l += w r: a masked slot's row is zero, its c -inf.
+      float* m = reinterpret_cast<float*>(smem + L::kOffA) + st * L::kMeta;
+      m[meta_at(my)] = live ? s * p.scale_log2 : 0.f;
+      m[meta_at(my) + 2] = live ? log2f(s) : -INFINITY;
+      m[rec_at(my)] = live ? 1.f / s : 0.f;
+      if (my == 0) reinterpret_cast<int*>(smem + L::kOffFlags)[st] = now;
+      if (!(now & kFinal) && e >= L::kStages - 1) prefetch();
+      cp_async_arrive_noinc(bar(L::kBarFull + st));      // once the copies have landed
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kBarFull + st)); // releases the factors
+      if (now & kFinal) break;
     }
     cp_async_wait_all();
   } else if (rg.count > 0 && warp > kMmaWarp) {
-    reg_dealloc<kOtherRegs>();                           // (no role: the MMA warp's warpgroup)
+    reg_dealloc<kOtherRegs>();                           // (the MMA warp's group)
   } else if (rg.count > 0 && warp == kMmaWarp) {
     reg_dealloc<kOtherRegs>();
     // ------------------------------------------------------------ MMA issuer
@@ -576,97 +557,69 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       const uint64_t d_v = smem_desc(base, L::kChunkBytes, 1024u, kSwizzle128B);
       const uint64_t d_p = smem_desc(base + L::kOffP, 16u, 1024u, kSwizzle128B);
       const volatile int* flags_of = reinterpret_cast<const volatile int*>(smem + L::kOffFlags);
-      // (Rolled loops: the other warps' code leaves this one's little room in
-      // the instruction cache.)
-      auto issue_s = [&](int st, int buf) {
+      auto issue_s = [&](int st) {
         const uint64_t k = d_k + ((static_cast<uint32_t>(st) * L::kStageBytes) >> 4);
-#pragma unroll 1
-        for (int c = 0; c < L::kChunks; ++c)
 #pragma unroll
-          for (int i = 0; i < (D < 128 ? D : 128) / 32; ++i)
-            mma8_ts(tmem + L::kTmemS + buf * kBlk, tmem + L::kTmemQ + c * 32 + i * 8,
-                    k + ((c * L::kChunkBytes + i * 32u) >> 4), idesc_s, c + i != 0 ? 1u : 0u);
-        mma_commit_elect(bar(L::kBarSFull + buf));
-        if (lane == 0) mbar_arrive(bar(L::kBarSFull + buf));  // releases what the rows' barrier gave
-        __syncwarp();
+        for (int c = 0; c < D / 32; ++c)
+          mma8_ts(tmem + L::kTmemS, tmem + L::kTmemQ + c * 8,
+                  k + (((c / 4) * L::kChunkBytes + (c % 4) * 32u) >> 4), idesc_s, c != 0 ? 1u : 0u);
+        mma_commit_elect(bar(L::kBarSFull));
       };
-      auto issue_o = [&](int st, int buf, bool first) {
+      auto issue_o = [&](int st, bool first) {
         const uint64_t v = d_v + ((static_cast<uint32_t>(st) * L::kStageBytes) >> 4);
-        const uint64_t pb = d_p + ((static_cast<uint32_t>(buf) * L::kPBytes) >> 4);
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll 2
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
           for (int c = 0; c < L::kChunks; ++c) {
             const uint64_t ad = v + ((c * L::kChunkBytes + k * 4096u) >> 4);
-            mma8_ss_keep(tmem + L::kTmemO + c * kHeads, ad, pb + ((k * 32u) >> 4), idesc_o, (!first || k > 0) ? 1u : 0u);
-            mma8_ss_again(tmem + L::kTmemO + c * kHeads, ad, pb + ((64u + k * 32u) >> 4), idesc_o, 1u);
+            const uint64_t bd = d_p + ((k * 32u) >> 4);
+            mma8_ss_keep(tmem + L::kTmemO + c * kHeads, ad, bd, idesc_o, (!first || k > 0) ? 1u : 0u);
+            mma8_ss_again(tmem + L::kTmemO + c * kHeads, ad, bd + (L::kPieceBytes >> 4), idesc_o, 1u);
           }
-          mma_commit_elect(bar(L::kBarEmpty + 2 * st + k));
+          mma_commit_elect(bar(L::kBarEmpty + 4 * st + k));
         }
-        mma_commit_elect(bar(L::kBarPDone + buf));
+        mma_commit_elect(bar(L::kBarPDone));
       };
-      // S runs ahead of O by two entries of the same token: O waits for the
-      // softmax, S only for its rows and for the S two entries before to have
-      // been read.  What the next step will wait for is tested before the
-      // present one is issued: a test takes some 300 cycles while rows are
-      // being copied, and as much tensor time was lost with each.
-      int no = 0;                                        // the next entry whose O is due
-      auto test = [&](int i, int phase) { return mbar_probe(bar(i), phase & 1); };
-      auto wait = [&](int i, int phase) { return __all_sync(0xffffffffu, mbar_wait(bar(i), phase & 1, ctl)); };
-      bool rows = false, read = true, weights = false;   // tested: for S of e, for S of e, for O of no
-      int next_flags = 0;
-      auto tests = [&](int e) {
-        rows = test(L::kBarFull + e % L::kStages, e / L::kStages);
-        next_flags = flags_of[e % L::kStages];
-        read = e < 2 || test(L::kBarSFree + (e & 1), (e >> 1) - 1);
-        weights = test(L::kBarPFull + (no & 1), no >> 1);
-      };
-      unsigned firsts = 0;                               // bit e % 32: entry e is its token's first
-      auto do_o = [&] {
-        if (!__all_sync(0xffffffffu, weights) && !wait(L::kBarPFull + (no & 1), no >> 1)) return false;
-        weights = false;
-        tc_fence_after();
-        issue_o(no % L::kStages, no & 1, (firsts >> (no & 31)) & 1u);
-        ++no;
-        return true;
-      };
-      bool ok = *abort_flag == 0;
-      int seg = 0;
-      for (int e = 0; ok; ++e) {
-        const int st = e % L::kStages;
-        int flags = next_flags;
-        if (!__all_sync(0xffffffffu, rows)) {
-          if (!(ok = wait(L::kBarFull + st, e / L::kStages))) break;
-          flags = flags_of[st];
-        }
-        firsts = (firsts & ~(1u << (e & 31))) | (static_cast<uint32_t>(flags & kFirst) << (e & 31));
-        // A token's first S needs its Q, which the softmax warps bring once the
-        // token before is finished.
-        if (flags & kFirst) {
-          while (ok && no < e) ok = do_o();
-          if (ok) ok = wait(L::kBarQFull, seg++);
-        }
-        if (ok && !__all_sync(0xffffffffu, read)) ok = wait(L::kBarSFree + (e & 1), (e >> 1) - 1);
-        if (!ok) break;
-        fence_proxy_async_smem();                        // rows written by cp.async -> tensor core
-        tc_fence_after();
-        issue_s(st, e & 1);
-        if (e == 0 && static_cast<int>(blockIdx.x) == p.stall_cta) {  // test hook only
-          ok = __any_sync(0xffffffffu, stall_until_limit(ctl));
-          break;
-        }
-        if (flags & kFinal) {
-          while (ok && no <= e) ok = do_o();
-          break;
-        }
-        if (e - no >= 2) {
-          const bool now = weights;
-          tests(e + 1);
-          weights = now;                                 // (for the entry issued here)
-          ok = do_o();
+      // Whichever is ready, the older work first: O of entry no, once its P is
+      // written; S of entry ns, once its rows are there, S's columns have been
+      // read and, at a token's start, its Q is in place.
+      bool ok = *abort_flag == 0, more = true;           // (more S to come)
+      int ns = 0, no = 0, seg = 0;
+      PollState ps = poll_start();
+      auto ready = [&](int i, int phase) { return __all_sync(0xffffffffu, mbar_probe(bar(i), phase & 1)); };
+      for (uint32_t spins = 0; ok && (more || no < ns);) {
+        if (no < ns && ready(L::kBarPFull, no)) {
+          const int st = no % L::kStages;
+          const bool first = (flags_of[st] & kFirst) != 0;
+          tc_fence_after();
+          issue_o(st, first);
+          ++no;
+        } else if (more && ns - no < L::kStages && ready(L::kBarFull + ns % L::kStages, ns / L::kStages) &&
+                   (ns == 0 || ready(L::kBarSFree, ns - 1))) {
+          const int st = ns % L::kStages;
+          const int flags = flags_of[st];
+          if (flags & kFirst) {
+            // The softmax warps bring Q once the token before is finished.
+            if (!ready(L::kBarQFull, seg)) {
+              if ((++spins & 63u) == 0u) ok = __all_sync(0xffffffffu, poll_check(ctl, ps));
+              continue;
+            }
+            ++seg;
+          }
+          fence_proxy_async_smem();                      // rows written by cp.async -> tensor core
+          tc_fence_after();
+          issue_s(st);
+          more = (flags & kFinal) == 0;
+          if (ns == 0 && static_cast<int>(blockIdx.x) == p.stall_cta) {  // test hook only
+            ok = __any_sync(0xffffffffu, stall_until_limit(ctl));
+            break;
+          }
+          ++ns;
         } else {
-          tests(e + 1);
+          if ((++spins & 63u) == 0u) ok = __all_sync(0xffffffffu, poll_check(ctl, ps));
+          continue;
         }
+        ps.t0 = globaltimer_ns();                        // progress: the limit counts from here
       }
       mma_commit_elect(bar(L::kBarDrain));
       mbar_wait_drain(bar(L::kBarDrain), 0);
@@ -715,57 +668,50 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
 
       float m[2] = {-INFINITY, -INFINITY};
       float2 l[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // (even and odd slots apart)
-      // Every softmax warp waits for every note, failed or not.
-      auto wait_note = [&](int i) {
-        if (!mbar_test(bar(L::kBarNote + (i & 1)), (i >> 1) & 1))
-          mbar_wait_drain(bar(L::kBarNote + (i & 1)), (i >> 1) & 1, 2 * p.limit_ns + 1000000000ull);
-        __syncwarp();
-        return *reinterpret_cast<volatile int*>(&notes[i % kNotes].failed) == 0;
-      };
-      // What the other warpgroup has done with entry i of this token.
-      auto hear = [&](int i, bool first) {
-        const Note* note = notes + i % kNotes;
-        if (!wait_note(i)) run = false;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int h = hq + 8 * g;
-          if (first) {
-            m[g] = note->to[h];
-          } else if ((note->heads[h >> 5] >> (h & 31)) & 1u) {
-            m[g] = note->to[h];
-            l[g] = mul2(l[g], make_float2(note->f[h], note->f[h]));
-          }
-        }
-      };
-      const int e0 = e;                                  // the token's first entry
-      bool last = false;
-      if ((e & 1) != half) {
-        hear(e, true);
-        if (!run) break;
-        last = notes[e % kNotes].last != 0;
-        ++e;
-      }
-      // This warpgroup's entries.  The other's in between are heard of as late
-      // as possible: S is read and its maxima are found meanwhile.
-      for (bool heard = true; run && !last; heard = false) {
+      for (bool first = true, last = false; !last; first = false, ++e) {
         Note* note = notes + e % kNotes;
-        const bool first = e == e0;
+        // Every softmax warp comes here for every block, failed or not.
+        auto wait_note = [&] {
+          if (!mbar_test(bar(L::kBarNote + (e & 1)), (e >> 1) & 1))
+            mbar_wait_drain(bar(L::kBarNote + (e & 1)), (e >> 1) & 1, 2 * p.limit_ns + 1000000000ull);
+          __syncwarp();
+        };
+        if ((e & 1) != half) {                           // the other warpgroup's block
+          wait_note();
+          if (*reinterpret_cast<volatile int*>(&note->failed) != 0) {
+            run = false;
+            break;
+          }
+          last = note->last != 0;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int h = hq + 8 * g;
+            if (first) {
+              m[g] = note->to[h];
+            } else if ((note->heads[h >> 5] >> (h & 31)) & 1u) {
+              m[g] = note->to[h];
+              l[g] = mul2(l[g], make_float2(note->f[h], note->f[h]));
+            }
+          }
+          continue;
+        }
         const int st = e % L::kStages;
-        if (!mbar_wait(bar(L::kBarSFull + half), (e >> 1) & 1, ctl)) bad = true;
+        if (!mbar_wait(bar(L::kBarFull + st), (e / L::kStages) & 1, ctl)) bad = true;  // the factors
+        if (!mbar_wait(bar(L::kBarSFull), e & 1, ctl)) bad = true;
         __syncwarp();
         tc_fence_after();
         const float* meta = reinterpret_cast<const float*>(smem + L::kOffA) + st * L::kMeta;
-        float2 y[2][8];                                  // per head, of its slot pairs
+        float2 y[2][16];                                 // per head, of its slot pairs
         const float2 fh[2] = {make_float2(rs.x, rs.x), make_float2(rs.y, rs.y)};
         const float2 fl[2] = {make_float2(rs.x * 0.03125f, rs.x * 0.03125f), make_float2(rs.y * 0.03125f, rs.y * 0.03125f)};
         {
-          float x[2][32];
-          tmem_ld16x64x2(tmem + lanes + L::kTmemS + half * kBlk, x[0], x[1]);
+          float x[2][64];
+          tmem_ld16x128x2(tmem + lanes + L::kTmemS, x[0], x[1]);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::kBarSFree + half));
+          if (lane == 0) mbar_arrive(bar(L::kBarSFree));
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 16; ++j) {
             const float4 ac = *reinterpret_cast<const float4*>(meta + (4 * j + quad) * 4);
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
@@ -774,28 +720,21 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
             }
           }
         }
-        float top[2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          top[g] = fmaxf(y[g][0].x, y[g][0].y);
-#pragma unroll
-          for (int j = 1; j < 8; ++j) top[g] = fmax3f(top[g], y[g][j].x, y[g][j].y);
-          top[g] = fmaxf(top[g], __shfl_xor_sync(0xffffffffu, top[g], 1));
-          top[g] = fmaxf(top[g], __shfl_xor_sync(0xffffffffu, top[g], 2));
-        }
-        const int flags = flags_of[st];
-        if (!heard) hear(e - 1, false);
-        if (!run) bad = true;                            // (this entry's note says so to the own warps)
         // The maxima: set by a token's first block, raised where this block's
         // outran the lag.
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const int h = hq + 8 * g;
-          const float mx = top[g] + kAbove;
+          float top = fmaxf(y[g][0].x, y[g][0].y);
+#pragma unroll
+          for (int j = 1; j < 16; ++j) top = fmax3f(top, y[g][j].x, y[g][j].y);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const float mx = top + kAbove;
           if (first) {
             if (lead) note->to[h] = mx;
             m[g] = mx;
-          } else if (top[g] > m[g] + kLag) {
+          } else if (top > m[g] + kLag) {
             const float f = fast_exp2(m[g] - mx);
             l[g] = mul2(l[g], make_float2(f, f));
             m[g] = mx;
@@ -808,20 +747,20 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
         }
         if (bad) note->failed = 1;
         if (lane == 0 && quarter == 0) {
-          note->last = flags & kLast;
+          note->last = flags_of[st] & kLast;
           Note* next = notes + (e + 4) % kNotes;
           next->heads[0] = next->heads[1] = next->failed = 0;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kBarNote + half));
+        if (lane == 0) mbar_arrive(bar(L::kBarNote + (e & 1)));
         // The weights, their part of l, and their two pieces.
-        uint32_t out_hi[2][4], out_lo[2][4];
+        uint32_t out_hi[2][8], out_lo[2][8];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const float shift = -((m[g] == -INFINITY ? 0.f : m[g]) + kShift);
           const float2 shift2 = make_float2(shift, shift);
 #pragma unroll
-          for (int j = 0; j < 8; j += 2) {
+          for (int j = 0; j < 16; j += 2) {
             const float4 r = *reinterpret_cast<const float4*>(meta + 2 * kBlk + (j / 2) * 16 + quad * 4);
             const float2 d01 = add2(y[g][j], shift2), d23 = add2(y[g][j + 1], shift2);
             const float2 w01 = make_float2(fast_exp2(d01.x), fast_exp2(d01.y));
@@ -837,48 +776,59 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
             out_lo[g][j / 2] = __byte_perm(lo, got, sel_lo);
           }
         }
-        if (!wait_note(e)) {
+        wait_note();
+        if (*reinterpret_cast<volatile int*>(&note->failed) != 0) {
           run = false;
           break;
         }
+        last = note->last != 0;
         const unsigned raised[2] = {*reinterpret_cast<volatile unsigned*>(&note->heads[0]),
                                     *reinterpret_cast<volatile unsigned*>(&note->heads[1])};
+        // P and O are this thread's once the previous block's products are done.
+        if (e > 0 && !mbar_wait(bar(L::kBarPDone), (e - 1) & 1, ctl)) bad = true;
+        __syncwarp();
         if (raised[0] | raised[1]) {                     // O of these heads, rescaled
-          if (e > 0 && !mbar_wait(bar(L::kBarPDone + (1 - half)), ((e - 1) >> 1) & 1, ctl)) bad = true;
-          __syncwarp();
           tc_fence_after();
           const uint32_t o = tmem + lanes + L::kTmemO;
-          for (uint64_t some = raised[0] | (static_cast<uint64_t>(raised[1]) << 32); some != 0; some &= some - 1) {
-            const int h = __ffsll(static_cast<long long>(some)) - 1;
-            const float f = note->f[h];
-            float v[L::kChunks];
-            tmem_ld1xn<L::kChunks, kHeads>(o + h, v);
+          if (__popc(raised[0]) + __popc(raised[1]) <= 16) {  // column by column
 #pragma unroll
-            for (int c = 0; c < L::kChunks; ++c) tmem_st1(o + c * kHeads + h, v[c] * f);
+            for (int u = 0; u < 2; ++u)
+              for (unsigned some = raised[u]; some != 0; some &= some - 1) {
+                const int h = 32 * u + __ffs(some) - 1;
+                const float f = note->f[h];
+                float v[L::kChunks];
+                tmem_ld1xn<L::kChunks, kHeads>(o + h, v);
+#pragma unroll
+                for (int c = 0; c < L::kChunks; ++c) tmem_st1(o + c * kHeads + h, v[c] * f);
+              }
+            tmem_wait_st();
+          } else {                                       // all of it
+#pragma unroll 1
+            for (int c = 0; c < 2 * L::kChunks; ++c) {
+              float v[32];
+              tmem_ld32(o + c * 32, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if ((raised[c & 1] >> i) & 1u) v[i] *= note->f[(c & 1) * 32 + i];
+              tmem_st32(o + c * 32, v);
+            }
           }
-          tmem_wait_st();
         }
-        // This P is free once the products of the entry before the last are done.
-        if (e > 1 && !mbar_wait(bar(L::kBarPDone + half), ((e >> 1) - 1) & 1, ctl)) bad = true;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const int h = hq + 8 * g;
-          const uint32_t row = base + L::kOffP + half * L::kPBytes + static_cast<uint32_t>(h) * 128u + (lane & 1) * 8u + (quad >> 1) * 4u;
+          const uint32_t row = base + L::kOffP + static_cast<uint32_t>(h) * 128u + (lane & 1) * 8u + (quad >> 1) * 4u;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 8; ++j) {
             const uint32_t at = row + ((static_cast<uint32_t>(j) ^ static_cast<uint32_t>(h & 7)) << 4);
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(out_hi[g][j]) : "memory");
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at ^ 64u), "r"(out_lo[g][j]) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + L::kPieceBytes), "r"(out_lo[g][j]) : "memory");
           }
         }
         tc_fence_before();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kBarPFull + half));
-        last = (flags & (kLast | kNextLast)) != 0;
-        e += 2;
-        if (flags & kLast) e -= 1;                       // e: behind the token's last entry
-        if (flags & kNextLast) hear(e - 1, false);
+        if (lane == 0) mbar_arrive(bar(L::kBarPFull));
       }
       if (!run) break;
 
@@ -901,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
           if (half == 0) head_end[hq + 8 * g] = m[g];
         }
       }
-      if (!mbar_wait(bar(L::kBarPDone + ((e - 1) & 1)), ((e - 1) >> 1) & 1, ctl)) bad = true;
+      if (!mbar_wait(bar(L::kBarPDone), (e - 1) & 1, ctl)) bad = true;
       bar_sync(1, kSoftmaxThreads);
       tc_fence_after();
       if (left > 0) {
@@ -981,17 +931,10 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       }
       tc_fence_before();
       if (left == 0) break;
+      // Both have read O and P's place before either brings the next token's.
+      bar_sync(1, kSoftmaxThreads);
     }
   }
-
-  // Padding tokens belong to no range: the gather warps see to them last.
-  if (p.zero_padding && warp >= kGatherWarp0)
-    for (int t = blockIdx.x + (warp - kGatherWarp0) * gridDim.x; t < p.T; t += gridDim.x * kGatherWarps)
-      if (!live_token(p, __ldg(p.token_req + t))) {
-        uint4* o = reinterpret_cast<uint4*>(p.o + static_cast<int64_t>(t) * p.H * D);
-        for (int i = lane; i < p.H * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
-        for (int h = lane; h < p.H; h += 32) p.lse[static_cast<int64_t>(t) * p.H + h] = -INFINITY;
-      }
 
   tc_fence_before();
   __syncthreads();
@@ -1126,14 +1069,14 @@ int64_t blocks_per_token(const smqa_paged_shape& s) {
 }
 // Whether ranges are whole tokens (index lists: all tokens have the same number
 // of blocks).  Splitting tokens evens the ranges out but costs the parts' way
-// through the workspace and the joining kernel, together about as long as 16
-// blocks take (128 tokens of 32 blocks, 76 ranges: 64 blocks at most per range
-// whole, 54 split).
+// through the workspace and the joining kernel, together about as long as eight
+// blocks take (128 tokens of 16 blocks, 76 ranges: 32 blocks at most per range
+// whole, 27 split).
 bool whole_tokens(const smqa_paged_shape& s) {
   if (s.topk == 0) return blocks_per_token(s) <= 1;
   const int groups = (s.H + kHeads - 1) / kHeads;
   const int64_t parts = 152 / groups, nb = blocks_per_token(s);
-  return (s.T + parts - 1) / parts * nb <= s.T * nb / parts + 16;
+  return (s.T + parts - 1) / parts * nb <= s.T * nb / parts + 8;
 }
 // CTAs of a call: per head group, as many ranges as SMs (or as the tokens can
 // have blocks).
