@@ -212,35 +212,22 @@ __device__ __forceinline__ int scale_exponent(float amax) {
   return max(k, -60);
 }
 
-constexpr int kAppendThreads = 256;
+// 16 rows per CTA, a warp each.  The warp of a run's first row (a run:
+// consecutive rows with ascending slots in one page) does the whole run if it is
+// short; a longer one, and the earlier rows of a page whose scale has grown, are
+// left to the whole CTA.  A run's rows are one flat range in kv_new and in the
+// cache, read twice, the second time from L1.  Bound by latency: 8192 rows
+// (D=512, pages of 64: 130 runs) took 11.9 us with a CTA per row, most of which
+// left at once, and take 7.5 us so; 128 single rows 2.6 us against 2.5.
+constexpr int kAppendWarps = 16, kAppendThreads = 32 * kAppendWarps;
+constexpr int kShortRun = 4;                             // rows
 
-// One CTA per row; the CTA of a run's first row (a run: consecutive rows with
-// ascending slots in one page) does the whole run, the others leave at once.
-// A run's rows are one flat range in kv_new and in the cache.
-__global__ void __launch_bounds__(kAppendThreads)
-    smqa_paged_append_kernel(const __nv_bfloat16* kv_new, const int32_t* slots, int T, int D,
-                             int page_shift, int n_slots, uint8_t* cache, float* scales) {
-  const int t = blockIdx.x, tid = threadIdx.x;
-  const int page = 1 << page_shift;
-  const int s0 = slots[t];
-  if (static_cast<unsigned>(s0) >= static_cast<unsigned>(n_slots)) return;
-  const int off = s0 & (page - 1);
-  if (off != 0 && t > 0 && slots[t - 1] == s0 - 1) return;
-  const int64_t pg = s0 >> page_shift;
-  // Read here, before the barriers: one thread writes the new scale at the end.
-  const float had = off ? scales[pg] : 0.f;
-  // Rows of the run: the first row that does not continue it ends it.
-  __shared__ int run;
-  if (tid == 0) run = page - off;
-  __syncthreads();
-  for (int i = tid; i < page - off; i += kAppendThreads)
-    if (t + i >= T || slots[t + i] != s0 + i) atomicMin(&run, i);
-  __syncthreads();
-  const int64_t n = static_cast<int64_t>(run) * D;  // elements, a multiple of 64
-  const uint4* src = reinterpret_cast<const uint4*>(kv_new + static_cast<int64_t>(t) * D);
-  // The run's largest finite magnitude (bf16 bit patterns order like values).
+// The largest finite magnitude of uint4 i, i + step, ... below n, as bf16 bits
+// (which order like values).
+__device__ __forceinline__ uint32_t largest(const uint4* src, int i, int step, int n) {
   uint32_t top = 0;
-  for (int64_t i = tid; i < n / 8; i += kAppendThreads) {
+#pragma unroll 8
+  for (; i < n; i += step) {
     const uint4 v = __ldg(src + i);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -250,43 +237,110 @@ __global__ void __launch_bounds__(kAppendThreads)
       top = max(top, hi < 0x7f80u ? hi : 0u);
     }
   }
-  __shared__ uint32_t warp_top[kAppendThreads / 32];
-  top = __reduce_max_sync(0xffffffffu, top);
-  if ((tid & 31) == 0) warp_top[tid >> 5] = top;
-  __syncthreads();
-  for (int w = 0; w < kAppendThreads / 32; ++w) top = max(top, warp_top[w]);
-  const float want = pow2f(scale_exponent(__uint_as_float(top << 16)));
-  const float s = off ? fmaxf(want, had) : want;
-  uint8_t* base = cache + (pg << page_shift) * D;
-  // Earlier rows under a grown scale.
-  if (off && s > had) {
-    const float f = had / s;
-    uint4* row = reinterpret_cast<uint4*>(base);
-    for (int64_t i = tid; i < static_cast<int64_t>(off) * D / 16; i += kAppendThreads) {
-      uint4 v = row[i];
-      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 a = e4m3x2_value(static_cast<uint16_t>(w[k])), b = e4m3x2_value(static_cast<uint16_t>(w[k] >> 16));
-        w[k] = e4m3x2(a.x * f, a.y * f) | (static_cast<uint32_t>(e4m3x2(b.x * f, b.y * f)) << 16);
-      }
-      row[i] = v;
-    }
-  }
-  // The new rows.
-  const float inv = 1.f / s;
+  return top;
+}
+// Their codes under a scale of 1 / inv.
+__device__ __forceinline__ void encode(const uint4* src, uint2* dst, int i, int step, int n, float inv) {
   auto code = [&](uint32_t w) {  // two bf16 -> two codes; an infinity becomes NaN
     float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
     lo = (w & 0x7fffu) >= 0x7f80u ? __uint_as_float(0x7fffffffu) : lo * inv;
     hi = ((w >> 16) & 0x7fffu) >= 0x7f80u ? __uint_as_float(0x7fffffffu) : hi * inv;
     return static_cast<uint32_t>(e4m3x2(lo, hi));
   };
-  uint2* dst = reinterpret_cast<uint2*>(base + static_cast<int64_t>(off) * D);
-  for (int64_t i = tid; i < n / 8; i += kAppendThreads) {
+#pragma unroll 8
+  for (; i < n; i += step) {
     const uint4 v = __ldg(src + i);
     dst[i] = make_uint2(code(v.x) | (code(v.y) << 16), code(v.z) | (code(v.w) << 16));
   }
-  if (tid == 0) scales[pg] = s;
+}
+// Codes times f = 2^-k.
+__device__ __forceinline__ void rescale(uint4* row, int i, int step, int n, float f) {
+#pragma unroll 8
+  for (; i < n; i += step) {
+    uint4 v = row[i];
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 a = e4m3x2_value(static_cast<uint16_t>(w[k])), b = e4m3x2_value(static_cast<uint16_t>(w[k] >> 16));
+      w[k] = e4m3x2(a.x * f, a.y * f) | (static_cast<uint32_t>(e4m3x2(b.x * f, b.y * f)) << 16);
+    }
+    row[i] = v;
+  }
+}
+
+__global__ void __launch_bounds__(kAppendThreads, 2)
+    smqa_paged_append_kernel(const __nv_bfloat16* kv_new, const int32_t* slots, int T, int D,
+                             int page_shift, int n_slots, uint8_t* cache, float* scales) {
+  __shared__ int runs, grown;                            // long runs: their first rows;
+  __shared__ int run_at[kAppendWarps], grown_to[kAppendWarps];  // pages whose scale has grown: up to
+  __shared__ float grown_by[kAppendWarps];               // this slot, by 1 / f
+  __shared__ unsigned part[4];
+  __shared__ uint32_t warp_top[kAppendWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int page = 1 << page_shift;
+  if (tid == 0) runs = grown = 0;
+  __syncthreads();
+  {
+    // The slots of the row before, of the warp's row and of those behind it.
+    const int t = blockIdx.x * kAppendWarps + warp;
+    const int64_t at = static_cast<int64_t>(t) - 1 + lane;
+    const int x = at >= 0 && at < T ? __ldg(slots + at) : -2;
+    const int s0 = __shfl_sync(0xffffffffu, x, 1), before = __shfl_sync(0xffffffffu, x, 0);
+    const int off = s0 & (page - 1);
+    if (static_cast<unsigned>(s0) < static_cast<unsigned>(n_slots) && (off == 0 || before != s0 - 1)) {
+      const unsigned same = __ballot_sync(0xffffffffu, lane > 0 && lane <= page - off && x == s0 + lane - 1);
+      const int rows = __ffs(~(same >> 1)) - 1;          // (31: or more)
+      if (rows <= kShortRun) {
+        const int64_t pg = s0 >> page_shift;
+        const float had = __shfl_sync(0xffffffffu, off && lane == 0 ? scales[pg] : 0.f, 0);  // (which lane 0 writes)
+        const int n = rows * D / 8;
+        const uint4* src = reinterpret_cast<const uint4*>(kv_new + static_cast<int64_t>(t) * D);
+        const uint32_t top = __reduce_max_sync(0xffffffffu, largest(src, lane, 32, n));
+        const float s = fmaxf(pow2f(scale_exponent(__uint_as_float(top << 16))), had);
+        encode(src, reinterpret_cast<uint2*>(cache + static_cast<int64_t>(s0) * D), lane, 32, n, 1.f / s);
+        if (lane == 0) {
+          scales[pg] = s;
+          if (off && s > had) {
+            const int i = atomicAdd(&grown, 1);
+            grown_to[i] = s0;
+            grown_by[i] = had / s;
+          }
+        }
+      } else if (lane == 0) {
+        run_at[atomicAdd(&runs, 1)] = t;
+      }
+    }
+  }
+  __syncthreads();
+  const int n_grown = grown, n_runs = runs;
+  for (int i = 0; i < n_grown; ++i) {
+    const int off = grown_to[i] & (page - 1);
+    rescale(reinterpret_cast<uint4*>(cache + static_cast<int64_t>(grown_to[i] - off) * D), tid, kAppendThreads, off * D / 16,
+            grown_by[i]);
+  }
+  for (int i = 0; i < n_runs; ++i) {
+    const int t = run_at[i], s0 = __ldg(slots + t), off = s0 & (page - 1);
+    const int64_t pg = s0 >> page_shift;
+    const float had = off ? scales[pg] : 0.f;            // (written behind a barrier)
+    if (warp < 4) {                                      // (a page has 128 rows at most)
+      const bool in = tid < page - off && tid < T - t && __ldg(slots + t + tid) == s0 + tid;
+      const unsigned same = __ballot_sync(0xffffffffu, in);
+      if (lane == 0) part[warp] = same;
+    }
+    __syncthreads();
+    int rows = 0;                                        // the first that does not go on ends the run
+    for (int w = 0; w < 4 && rows == 32 * w; ++w) rows += part[w] == 0xffffffffu ? 32 : __ffs(~part[w]) - 1;
+    const int n = rows * D / 8;
+    const uint4* src = reinterpret_cast<const uint4*>(kv_new + static_cast<int64_t>(t) * D);
+    uint32_t top = __reduce_max_sync(0xffffffffu, largest(src, tid, kAppendThreads, n));
+    if (lane == 0) warp_top[warp] = top;
+    __syncthreads();
+    for (int w = 0; w < kAppendWarps; ++w) top = max(top, warp_top[w]);
+    const float s = fmaxf(pow2f(scale_exponent(__uint_as_float(top << 16))), had);
+    if (off && s > had) rescale(reinterpret_cast<uint4*>(cache + (pg << page_shift) * D), tid, kAppendThreads, off * D / 16, had / s);
+    encode(src, reinterpret_cast<uint2*>(cache + static_cast<int64_t>(s0) * D), tid, kAppendThreads, n, 1.f / s);
+    if (tid == 0) scales[pg] = s;
+  }
 }
 
 int page_shift_of(int page_size) {
@@ -418,7 +472,7 @@ smqa_status smqa_paged_append(const void* kv_new, const int32_t* slot_mapping, i
   if (!kv_new || !slot_mapping || !kv_cache || !kv_scales || !is_aligned(kv_new, 16) ||
       !is_aligned(kv_cache, 16) || !is_aligned(slot_mapping, 4) || !is_aligned(kv_scales, 4))
     return refuse(SMQA_ERR_INVALID_ARG, "null or misaligned pointer");
-  smqa_paged_append_kernel<<<T, kAppendThreads, 0, stream>>>(
+  smqa_paged_append_kernel<<<(T - 1) / kAppendWarps + 1, kAppendThreads, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(kv_new), slot_mapping, T, D, shift, n_pages * page_size,
       static_cast<uint8_t*>(kv_cache), kv_scales);
   const cudaError_t e = cudaGetLastError();

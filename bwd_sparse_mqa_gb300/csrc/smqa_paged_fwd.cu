@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       }
       if (!end_tok[1] && end_tok[2]) l.tail_tok = end_tok[0];
     }
-    reinterpret_cast<Leftover*>(p.ws)[blockIdx.x] = l;
+    if (!p.whole_tokens) reinterpret_cast<Leftover*>(p.ws)[blockIdx.x] = l;
   }
 
   // Padding tokens belong to no range; warps without another role see to them.
@@ -1122,7 +1122,7 @@ cudaError_t launch(const PagedFwdParams& p, int ctas, cudaStream_t stream) {
 size_t paged_fwd_workspace(const smqa_paged_shape& s) {
   const int groups = (s.H + kHeads - 1) / kHeads;
   static_assert(152 <= kMaxCtas, "a leftover per CTA");
-  if (whole_tokens(s)) return kLeftoverBytes;
+  if (whole_tokens(s)) return 0;
   return kLeftoverBytes + static_cast<size_t>(ranges_of(s)) * groups * 2 * part_floats(s.D) * sizeof(float);
 }
 

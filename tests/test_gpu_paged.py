@@ -126,6 +126,23 @@ def test_append_prompts_and_tokens(D, page):
     _check_append(new, slot, cache, scale)
 
 
+@pytest.mark.parametrize("D", [64, 512])
+@pytest.mark.parametrize("page", [32, 128])
+def test_append_runs_of_all_lengths_under_growing_scales(D, page):
+    """Runs of every length up to a page, in an order that mixes short and long ones, each in a
+    page of its own behind earlier rows whose codes have to be rescaled (or not)."""
+    g = torch.Generator().manual_seed(D + page)
+    lens = torch.randperm(page, generator=g)[:40].add(1).tolist() + [1] * 20 + [4, 5, 30, 31, 32, page]
+    cache, scale = ref.fill_cache(len(lens), page, D, 11, spread=2)
+    slot, mag = [], []
+    for i, n in enumerate(lens):
+        off = int(torch.randint(0, page - n + 1, (1,), generator=g))
+        slot += [i * page + off + j for j in range(n)]
+        mag += [2.0 ** (3 * (i % 4))] * n
+    new = (torch.randn(len(slot), D, generator=g) * torch.tensor(mag)[:, None]).bfloat16()
+    _check_append(new, slot, cache, scale)
+
+
 def test_append_magnitudes():
     """Scales at the border 448 * 2^k, zero pages, the smallest and largest values, rescaling far
     enough to reach e4m3's subnormals, NaN and infinities, and values behind the run."""
