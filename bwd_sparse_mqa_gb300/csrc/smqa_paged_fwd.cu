@@ -50,6 +50,13 @@
 //                        memory, Q's pieces into TMEM at the start of a token
 //                        and O^T out of it at the end.
 // TMEM: S 128 columns, O^T D/2, Q D/4.
+//
+// Bound by shared memory: a block writes 64 KB of rows into it and reads them
+// for S, again for O (once, by the collector) and P four times (once per 128 of
+// D), 2050 cycles at 128 bytes a clock; the tensor core takes 2500 for it (N of
+// 64 and 128 fill it by two thirds) and a block 3500 in all.  Tried and slower
+// (128 tokens H=128 topk=2048, 83 us so): O's pieces without the collector, S and
+// O issued by two warps, 93; blocks of 64 slots, 84.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -119,8 +126,11 @@ struct PagedLayout {
   static constexpr int kBarSFull = kBarEmpty + 4 * kStages;
   static constexpr int kBarSFree = kBarSFull + 1;
   static constexpr int kBarPFull = kBarSFree + 1;
-  static constexpr int kBarPDone = kBarPFull + 1;            // P and its tile used, O up to date
-  static constexpr int kBarNote = kBarPDone + 1;             // [2] a warpgroup's note is written
+  // P and its tile used, O up to date.  [2], of even and odd entries: a
+  // warpgroup waits for every other one, which in one barrier's two parities
+  // could not be told from the one before.
+  static constexpr int kBarPDone = kBarPFull + 1;
+  static constexpr int kBarNote = kBarPDone + 2;             // [2] a warpgroup's note is written
   static constexpr int kBarQFull = kBarNote + 2;
   static constexpr int kBarDrain = kBarQFull + 1;
   static constexpr int kNumBars = kBarDrain + 1;
@@ -312,7 +322,10 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
   const uint32_t pad = (1024u - (base & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
   base += pad;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (The warp's number as a value the compiler knows to be the same in all
+  // lanes: without it the instructions that feed the tensor core take 15 %
+  // longer to issue.)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int groups = (p.H + kHeads - 1) / kHeads;
   const int part = blockIdx.x / groups, parts = gridDim.x / groups;
   const int h0 = (blockIdx.x % groups) * kHeads;
@@ -331,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
     mbar_init(bar(L::kBarSFull), 1);
     mbar_init(bar(L::kBarSFree), kSoftmaxThreads / 64);  // (one arrival per warp)
     mbar_init(bar(L::kBarPFull), kSoftmaxThreads / 64);
-    mbar_init(bar(L::kBarPDone), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(L::kBarPDone + i), 1);
     mbar_init(bar(L::kBarNote), kSoftmaxThreads / 64);
     mbar_init(bar(L::kBarNote + 1), kSoftmaxThreads / 64);
     mbar_init(bar(L::kBarQFull), kSoftmaxThreads / 32);
@@ -544,13 +557,11 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       if (now & kFinal) break;
     }
     cp_async_wait_all();
-  } else if (rg.count > 0 && warp > kMmaWarp) {
-    reg_dealloc<kOtherRegs>();                           // (the MMA warp's group)
-  } else if (rg.count > 0 && warp == kMmaWarp) {
-    reg_dealloc<kOtherRegs>();
+  } else if (rg.count > 0 && warp >= kMmaWarp) {
+    reg_dealloc<kOtherRegs>();                           // (the warpgroup's other warps have no role)
     // ------------------------------------------------------------ MMA issuer
     // The whole warp runs this, one lane of it issues.
-    {
+    if (warp == kMmaWarp) {
       constexpr uint32_t idesc_s = idesc_e4m3_f32(128, kBlk, false);
       constexpr uint32_t idesc_o = idesc_e4m3_f32(128, kHeads, true);
       const uint64_t d_k = smem_desc(base, 16u, 1024u, kSwizzle128B);
@@ -565,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
                   k + (((c / 4) * L::kChunkBytes + (c % 4) * 32u) >> 4), idesc_s, c != 0 ? 1u : 0u);
         mma_commit_elect(bar(L::kBarSFull));
       };
-      auto issue_o = [&](int st, bool first) {
+      auto issue_o = [&](int e, int st, bool first) {
         const uint64_t v = d_v + ((static_cast<uint32_t>(st) * L::kStageBytes) >> 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -578,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
           }
           mma_commit_elect(bar(L::kBarEmpty + 4 * st + k));
         }
-        mma_commit_elect(bar(L::kBarPDone));
+        mma_commit_elect(bar(L::kBarPDone + (e & 1)));
       };
       // Whichever is ready, the older work first: O of entry no, once its P is
       // written; S of entry ns, once its rows are there, S's columns have been
@@ -592,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
           const int st = no % L::kStages;
           const bool first = (flags_of[st] & kFirst) != 0;
           tc_fence_after();
-          issue_o(st, first);
+          issue_o(no, st, first);
           ++no;
         } else if (more && ns - no < L::kStages && ready(L::kBarFull + ns % L::kStages, ns / L::kStages) &&
                    (ns == 0 || ready(L::kBarSFree, ns - 1))) {
@@ -645,6 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
     float* head_end = reinterpret_cast<float*>(smem + L::kOffEnd);  // warpgroup, and m
     Note* notes = reinterpret_cast<Note*>(smem + L::kOffNotes);
     const volatile int* flags_of = reinterpret_cast<const volatile int*>(smem + L::kOffFlags);
+    auto done_with = [&](int e) { return mbar_wait(bar(L::kBarPDone + (e & 1)), (e >> 1) & 1, ctl); };
     int64_t left = rg.count;
     int e = 0;
     bool run = true;
@@ -785,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
         const unsigned raised[2] = {*reinterpret_cast<volatile unsigned*>(&note->heads[0]),
                                     *reinterpret_cast<volatile unsigned*>(&note->heads[1])};
         // P and O are this thread's once the previous block's products are done.
-        if (e > 0 && !mbar_wait(bar(L::kBarPDone), (e - 1) & 1, ctl)) bad = true;
+        if (e > 0 && !done_with(e - 1)) bad = true;
         __syncwarp();
         if (raised[0] | raised[1]) {                     // O of these heads, rescaled
           tc_fence_after();
@@ -851,7 +863,8 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
           if (half == 0) head_end[hq + 8 * g] = m[g];
         }
       }
-      if (!mbar_wait(bar(L::kBarPDone), (e - 1) & 1, ctl)) bad = true;
+      if (!done_with(e - 1)) bad = true;
+      __syncwarp();
       bar_sync(1, kSoftmaxThreads);
       tc_fence_after();
       if (left > 0) {

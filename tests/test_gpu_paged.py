@@ -370,6 +370,24 @@ def test_attn_equals_the_bf16_forward_on_the_same_rows():
     assert float((lse - lse2[0]).abs().max()) <= 1e-4 * float(lse2.abs().max())
 
 
+@pytest.mark.parametrize("H,D,T,ctx,topk", [(128, 512, 128, 1200, 1024), (128, 512, 9, 6000, 0), (48, 64, 100, 900, 0)])
+def test_attn_many_calls_in_a_row(H, D, T, ctx, topk):
+    """Back to back, the same call gives the same bits and no wait runs out: every phase of the
+    kernel's barriers is told from the one before, however far a group of warps falls behind."""
+    x = _attn_case([ctx] * 3, [(t % 3, ctx - 1 - t // 3) for t in range(T)], H, D, topk, 64, 5)
+    d = {k: (None if v is None else v.cuda()) for k, v in x.items()}
+
+    def call():
+        return sparse_mqa_paged_fwd(d["q"], d["kv_cache"], d["kv_scales"], d["attn_sink"], d["block_table"],
+                                    d["seq_lens"], d["token_req"], d["positions"], d["topk_idxs"])
+    o, lse = call()
+    for _ in range(20):
+        for _ in range(200):
+            o2, lse2 = call()
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        assert device_status() == 0
+
+
 def test_attn_out_keeps_padding_and_workspace_is_reused():
     x = _attn_case([300, 200], [(0, 299), (1, 199)], 24, 512, 130, 64, 17, pad=3)
     o = torch.full((5, 24, 512), 7.0, dtype=torch.bfloat16, device="cuda")
