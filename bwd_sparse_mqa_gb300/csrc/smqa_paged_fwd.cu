@@ -591,43 +591,52 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
         }
         mma_commit_elect(bar(L::kBarPDone + (e & 1)));
       };
-      // Whichever is ready, the older work first: O of entry no, once its P is
-      // written; S of entry ns, once its rows are there, S's columns have been
-      // read and, at a token's start, its Q is in place.
-      bool ok = *abort_flag == 0, more = true;           // (more S to come)
-      int ns = 0, no = 0, seg = 0;
-      PollState ps = poll_start();
+      // S of an entry before O of the one before, so that the softmax works on the
+      // former's while the latter is formed; but O first if the rows come late.
+      // A test of a barrier takes some 280 cycles beside the other warps' copies
+      // and stores: what has been seen done is not asked again.
+      auto wait = [&](int i, int phase) { return __all_sync(0xffffffffu, mbar_wait(bar(i), phase & 1, ctl)); };
       auto ready = [&](int i, int phase) { return __all_sync(0xffffffffu, mbar_probe(bar(i), phase & 1)); };
+      bool ok = *abort_flag == 0, more = true, rows = false;  // (more S to come; the next one's rows are there)
+      int ns = 0, no = 0, seg = 0, st_s = 0, turn = 0, st_o = 0, flags = 0;
+      unsigned begins = 0;                               // bit i: entry no + i is its token's first
+      PollState ps = poll_start();
       for (uint32_t spins = 0; ok && (more || no < ns);) {
-        if (no < ns && ready(L::kBarPFull, no)) {
-          const int st = no % L::kStages;
-          const bool first = (flags_of[st] & kFirst) != 0;
-          tc_fence_after();
-          issue_o(no, st, first);
-          ++no;
-        } else if (more && ns - no < L::kStages && ready(L::kBarFull + ns % L::kStages, ns / L::kStages) &&
-                   (ns == 0 || ready(L::kBarSFree, ns - 1))) {
-          const int st = ns % L::kStages;
-          const int flags = flags_of[st];
+        const bool only_o = !more || ns - no >= 2;       // (S after next: its softmax waits for O)
+        bool s_next = false;
+        if (!only_o) {
+          if (!rows && (rows = ready(L::kBarFull + st_s, turn))) flags = flags_of[st_s];
+          s_next = rows && (ns == 0 || ready(L::kBarSFree, ns - 1));
+          // A token's first S needs its Q, brought once the token before is finished.
+          if (s_next && (flags & kFirst)) s_next = no == ns && ready(L::kBarQFull, seg);
+        }
+        if (s_next) {
           if (flags & kFirst) {
-            // The softmax warps bring Q once the token before is finished.
-            if (!ready(L::kBarQFull, seg)) {
-              if ((++spins & 63u) == 0u) ok = __all_sync(0xffffffffu, poll_check(ctl, ps));
-              continue;
-            }
             ++seg;
+            begins |= 1u << (ns - no);
           }
           fence_proxy_async_smem();                      // rows written by cp.async -> tensor core
           tc_fence_after();
-          issue_s(st);
+          issue_s(st_s);
           more = (flags & kFinal) == 0;
           if (ns == 0 && static_cast<int>(blockIdx.x) == p.stall_cta) {  // test hook only
             ok = __any_sync(0xffffffffu, stall_until_limit(ctl));
             break;
           }
+          rows = false;
           ++ns;
+          if (++st_s == L::kStages) {
+            st_s = 0;
+            ++turn;
+          }
+        } else if (only_o ? (ok = wait(L::kBarPFull, no)) : no < ns && ready(L::kBarPFull, no)) {
+          tc_fence_after();
+          issue_o(no, st_o, begins & 1u);
+          begins >>= 1;
+          ++no;
+          if (++st_o == L::kStages) st_o = 0;
         } else {
-          if ((++spins & 63u) == 0u) ok = __all_sync(0xffffffffu, poll_check(ctl, ps));
+          if ((++spins & 63u) == 0u) ok = ok && __all_sync(0xffffffffu, poll_check(ctl, ps));
           continue;
         }
         ps.t0 = globaltimer_ns();                        // progress: the limit counts from here
