@@ -19,8 +19,8 @@
 //        the token's first block, so that the largest weight's code is 2^4 at
 //        least, and may fall 2.75 behind the running maximum (2^8.75 < 448,
 //        e4m3's largest) before O is rescaled, which holds the pipeline up
-//        (128 tokens H=128 topk=2048, page scales up to 2^3 apart: 84.4 us
-//        with m at the maximum, 82.4 us so).  l adds w / s_j in fp32.
+//        (128 tokens H=128 topk=2048, page scales up to 2^3 apart: 2 us more
+//        with m at the maximum).  l adds w / s_j in fp32.
 //        An fp16 number below 2 holds an e4m3 code of its 2^8-fold in bits
 //        7-13 (and the sign), subnormals included, so both pieces come from
 //        integer operations on pairs of fp16: the conversion instructions
@@ -55,8 +55,9 @@
 // for S, again for O (once, by the collector) and P four times (once per 128 of
 // D), 2050 cycles at 128 bytes a clock; the tensor core takes 2500 for it (N of
 // 64 and 128 fill it by two thirds) and a block 3500 in all.  Tried and slower
-// (128 tokens H=128 topk=2048, 83 us so): O's pieces without the collector, S and
-// O issued by two warps, 93; blocks of 64 slots, 84.
+// (128 tokens H=128 topk=2048, 80 us so): O's pieces without the collector, S and
+// O issued by two warps, 93; P in a ring of three halves, written and multiplied
+// by halves, 90; blocks of 64 slots, 84.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -308,7 +309,6 @@ struct QLoader {
       }
     }
     const uint32_t t0 = top_of(16 * quarter + (lane >> 2)), t1 = top_of(16 * quarter + 8 + (lane >> 2));
-    bar_sync(4 + quarter, 64);                           // head_top's place is head_max's next
     auto scale = [&](uint32_t m) { return m >= 0x7f80u ? __uint_as_float(0x7fffffffu) : pow2f(exponent(m) - 7); };
     return make_float2(scale(t0), scale(t1));
   }
@@ -971,8 +971,9 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
 // every 128 for the four heads, lane i of every warp also m and l of part i,
 // which weighs 2^(m_i - top).  Bound by latency: whose token and how many parts
 // is one trip to L2, m, l and the first kAhead parts of O together the second.
-// Small blocks with many loads each: four times larger ones, each warp with all
-// the reductions for a quarter of the columns, took 25 us where these take 6.
+// Small blocks with many loads each: with four times larger ones, each warp with
+// all the reductions for a quarter of the columns, a call whose 152 CTAs all leave
+// parts took 16 us longer.  It adds 6 us to a lone token's 14.
 constexpr int kJoinHeads = 4;
 
 template <int D, int kAhead>

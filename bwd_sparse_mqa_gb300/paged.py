@@ -42,6 +42,7 @@ class PagedPlan(NamedTuple):
 # it fails, and the stream and device are read without building objects.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_LIM = 2 ** 31                                           # (the C ABI takes sizes as int32)
 _I32, _BF16, _F32, _E4M3 = torch.int32, torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
 
@@ -92,12 +93,13 @@ def paged_plan(context_lens: torch.Tensor, query_lens: torch.Tensor, block_table
               and context_lens.shape == query_lens.shape == (R,) and free_count.shape == (1,)
               and free_pages.ndim == 1 and context_lens.is_contiguous()
               and query_lens.is_contiguous() and block_table.is_contiguous()
-              and free_pages.is_contiguous() and max_tokens >= 0)
+              and free_pages.is_contiguous() and 0 <= max_tokens < _LIM and 0 <= page_size < _LIM
+              and 0 <= n_pages < _LIM)
     except (AttributeError, ValueError):
         ok = False
     if not ok:
         _explain("context_lens, query_lens and block_table must have the same number of requests, "
-                 "free_count one element, and max_tokens must not be negative",
+                 "free_count one element, and page_size, max_tokens and n_pages lie in [0, 2^31)",
                  (context_lens, "context_lens", _I32, 1), (query_lens, "query_lens", _I32, 1),
                  (block_table, "block_table", _I32, 2), (free_pages, "free_pages", _I32, 1),
                  (free_count, "free_count", _I32, 1))
@@ -138,8 +140,9 @@ def paged_release(block_table: torch.Tensor, release: torch.Tensor, free_pages: 
     R, W = block_table.shape
     if release.shape[0] != R or free_count.shape[0] != 1 or \
             (seq_lens is not None and seq_lens.shape[0] != R) or \
-            len({t.device for t, *_ in tensors}) != 1:
-        _explain(f"release and seq_lens must have R={R} entries, free_count one element", *tensors)
+            len({t.device for t, *_ in tensors}) != 1 or not 0 <= n_pages < _LIM:
+        _explain(f"release and seq_lens must have R={R} entries, free_count one element, and n_pages "
+                 "lie in [0, 2^31)", *tensors)
     _call("smqa_paged_release", block_table.get_device(), _lib.load().smqa_paged_release,
           block_table.data_ptr(), None if seq_lens is None else seq_lens.data_ptr(),
           release.data_ptr(), R, W, int(n_pages), free_pages.data_ptr(), free_count.data_ptr(),

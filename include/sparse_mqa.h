@@ -472,12 +472,16 @@ smqa_status smqa_paged_append(const void* kv_new, const int32_t* slot_mapping, i
  * j < seq_lens[req].  A position whose block-table entry is outside
  * [0, n_pages) is masked.  A token with nothing to attend to gets O = 0 and
  * lse = sink / ln 2.  A head whose q row holds a NaN or an infinity gets NaN.
- * kv_scales lie in [2^-60, 2^120]. 
+ * kv_scales lie in [2^-60, 2^120].
  *   workspace    at least smqa_paged_fwd_workspace_bytes(shape) bytes, 256-byte
  *                aligned (NULL allowed when that is 0); needs no
  *                initialisation; calls whose kernels may overlap must not
  *                share it
  *   flags        0 or SMQA_FLAG_ZERO_PADDING
+ * The codes enter the tensor core as they are.  A q row is exact down to 2^-22
+ * of its largest value; a weight has a relative error of 2^-8 + 2^-11 at most,
+ * down to 2^-14 of its token's and head's largest p_j s_j; S, O, the maxima and
+ * l are held in fp32, O is rounded to bf16 once.
  * 1 <= H <= 128, D in {64, 512}, n_pages * page_size < 2^31,
  * T * max(H, topk) < 2^31.
  */

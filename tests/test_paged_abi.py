@@ -173,3 +173,16 @@ def test_plain_attn_matches_softmax():
         z = torch.cat([q[t].double() @ rows[:n].T / 8.0, sink.double()[:, None]], 1)
         assert torch.allclose(o[t], torch.softmax(z, 1)[:, :-1] @ rows[:n], rtol=1e-12, atol=1e-12)
         assert torch.allclose(lse[t], torch.logsumexp(z, 1) / math.log(2.0), rtol=1e-12)
+
+
+@pytest.mark.gpu
+def test_python_refuses_sizes_beyond_int32():
+    """The C ABI's sizes are int32: a larger one is refused, not cut to its low bits."""
+    i = torch.zeros(2, dtype=torch.int32, device="cuda")
+    table = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    for page, tokens, pages in ((16 + 2 ** 32, 4, 3), (16, 4 + 2 ** 32, 3), (16, 4, 3 + 2 ** 32), (16, -1, 3)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            paged_plan(i, i, table, i, i[:1].clone(), page, tokens, pages)
+    with pytest.raises(ValueError, match="2\\^31"):
+        paged_release(table, i.bool(), i, i[:1].clone(), 3 + 2 ** 32)
+    assert table.eq(0).all()
