@@ -2,6 +2,9 @@
 element within derived bounds (tests/_paged.py), at the sizes, masks and lengths
 where they can go wrong, alone and together."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -505,6 +508,66 @@ STEPS = [([bool(v) for v in gone], adds) for gone, adds in STEPS]
 @pytest.mark.parametrize("D,H,topk", [(512, 64, 40), (64, 16, 0), (512, 128, 0)])
 def test_serving_steps(D, H, topk, capture):
     _serve(STEPS, D, H, topk, capture)
+
+
+def test_no_tokens():
+    """Calls without tokens do nothing and return empty rows."""
+    cache, scale = ref.fill_cache(3, 16, 64, 1)
+    c, sc, z = cache.cuda(), scale.cuda(), _i32([0, 0])
+    table, count = _i32([[0, -1], [-1, -1]]), _i32([2])
+    plan = paged_plan(_i32([5, 0]), z, table, _i32([1, 2]), count, 16, 0, 3)
+    assert plan.block_table.tolist() == table.tolist() and int(plan.free_count) == 2
+    assert plan.seq_lens.tolist() == [5, 0] and plan.cu_query.tolist() == [0, 0, 0] and plan.token_req.numel() == 0
+    paged_kv_append(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), plan.slot_mapping, c, sc)
+    assert torch.equal(c.cpu().view(torch.uint8), cache.view(torch.uint8)) and torch.equal(sc.cpu(), scale)
+    for idx in (None, torch.empty(0, 7, dtype=torch.int32, device="cuda")):
+        o, lse = sparse_mqa_paged_fwd(torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda"), c, sc,
+                                      torch.zeros(4, device="cuda"), table, plan.seq_lens, plan.token_req,
+                                      plan.positions, idx)
+        assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
+FIRST_CALLS = """
+import torch
+from bwd_sparse_mqa_gb300 import paged_kv_append, paged_plan, paged_release, sparse_mqa_paged_fwd
+torch.manual_seed(0)
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+ctx, qry, free, count = i32([0, 0]), i32([40, 7]), i32([3, 1, 0, 2, 4]), i32([5])
+table = torch.full((2, 3), -1, dtype=torch.int32, device="cuda")
+cache = torch.zeros(5, 16, 512, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+scales, sink = torch.zeros(5, device="cuda"), torch.randn(128, device="cuda")
+q = torch.randn(47, 128, 512, device="cuda").bfloat16()
+new = torch.randn(47, 512, device="cuda").bfloat16()
+stop = torch.tensor([False, True], device="cuda")
+
+def step():
+    p = paged_plan(ctx, qry, table, free, count, 16, 47, 5)
+    paged_kv_append(new, p.slot_mapping, cache, scales)
+    out = sparse_mqa_paged_fwd(q, cache, scales, sink, p.block_table, p.seq_lens, p.token_req, p.positions)
+    paged_release(p.block_table, stop, free, p.free_count, 5)
+    return *out, p.block_table, p.free_count
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    held = step()
+graph.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in held]
+free.copy_(i32([3, 1, 0, 2, 4]))
+want = step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+assert got[0].float().abs().max() > 0 and got[2].tolist() == [[4, 2, 0], [-1, -1, -1]] and int(got[3]) == 2
+print("OK")
+"""
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first call of every operator is captured: nothing is set up outside the graph."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("OK"), r.stderr[-3000:]
 
 
 def test_two_streams_at_once():
