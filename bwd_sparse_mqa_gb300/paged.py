@@ -105,23 +105,25 @@ def paged_plan(context_lens: torch.Tensor, query_lens: torch.Tensor, block_table
                  (free_count, "free_count", _I32, 1))
     N = int(max_tokens)
     # One allocation: seq_lens, cu_query, token_req, positions, slot_mapping,
-    # and the table and count unless they are updated in place.
-    if inplace:
-        sizes, table, count = [R, R + 1, N, N, N], block_table, free_count
-        seq, cu, req, pos, slot = torch.empty(2 * R + 1 + 3 * N, dtype=_I32,
-                                              device=dev).split_with_sizes(sizes)
-    else:
-        sizes = [R, R + 1, N, N, N, 1, R * W]
-        seq, cu, req, pos, slot, count, table = torch.empty(
-            2 * R + 2 + 3 * N + R * W, dtype=_I32, device=dev).split_with_sizes(sizes)
-        table = table.view(R, W)
-    # (The outputs lie one behind another.)
-    at = seq.data_ptr()
+    # and the count and table unless they are updated in place.  The kernel is
+    # launched before the tensors over its parts are made ("unsafe": not as
+    # views that autograd would follow, which these integers need not be).
+    sizes = [R, R + 1, N, N, N] if inplace else [R, R + 1, N, N, N, 1, R * W]
+    base = torch.empty(sum(sizes), dtype=_I32, device=dev)
+    at = base.data_ptr()
+    tok = at + 8 * R + 4
+    end = tok + 12 * N
     _call("smqa_paged_plan", dev, _lib.load().smqa_paged_plan, context_lens.data_ptr(),
           query_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
           free_count.data_ptr(), R, W, int(page_size), int(n_pages), free_pages.shape[0], N,
-          table.data_ptr(), count.data_ptr(), at, at + 4 * R, at + 8 * R + 4,
-          at + 8 * R + 4 + 4 * N, at + 8 * R + 4 + 8 * N)
+          block_table.data_ptr() if inplace else end + 4,
+          free_count.data_ptr() if inplace else end, at, at + 4 * R, tok, tok + 4 * N, tok + 8 * N)
+    if inplace:
+        table, count = block_table, free_count
+        seq, cu, req, pos, slot = torch.unsafe_split_with_sizes(base, sizes)
+    else:
+        seq, cu, req, pos, slot, count, table = torch.unsafe_split_with_sizes(base, sizes)
+        table = table.view(R, W)
     return PagedPlan(table, count, seq, cu, req, pos, slot)
 
 
