@@ -218,9 +218,9 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 // left to the whole CTA.  A run's rows are one flat range in kv_new and in the
 // cache, read twice, the second time from L1.  Bound by latency: 8192 rows
 // (D=512, pages of 64: 130 runs) took 11.9 us with a CTA per row, most of which
-// left at once, and take 7.5 us so; 128 single rows 2.6 us against 2.5.
+// left at once, and take 7.3 us so; 128 single rows 2.8 us against 2.5.
 constexpr int kAppendWarps = 16, kAppendThreads = 32 * kAppendWarps;
-constexpr int kShortRun = 4;                             // rows
+constexpr int kShortRun = 8;                             // rows (512 runs of 6: 4.6 us by warps, 6.1 by CTAs)
 
 // The largest finite magnitude of uint4 i, i + step, ... below n, as bf16 bits
 // (which order like values).
@@ -271,25 +271,36 @@ __device__ __forceinline__ void rescale(uint4* row, int i, int step, int n, floa
 __global__ void __launch_bounds__(kAppendThreads, 2)
     smqa_paged_append_kernel(const __nv_bfloat16* kv_new, const int32_t* slots, int T, int D,
                              int page_shift, int n_slots, uint8_t* cache, float* scales) {
-  __shared__ int runs, grown;                            // long runs: their first rows;
-  __shared__ int run_at[kAppendWarps], grown_to[kAppendWarps];  // pages whose scale has grown: up to
-  __shared__ float grown_by[kAppendWarps];               // this slot, by 1 / f
-  __shared__ unsigned part[4];
-  __shared__ uint32_t warp_top[kAppendWarps];
+  __shared__ int runs, grown;                            // long runs: first row, number of rows;
+  __shared__ int run_at[kAppendWarps], run_rows[kAppendWarps];
+  __shared__ int grown_to[kAppendWarps];                 // pages whose scale has grown: up to this
+  __shared__ float grown_by[kAppendWarps];               // slot, by 1 / f
+  __shared__ uint32_t warp_top[2][kAppendWarps];         // (of even and odd runs)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int page = 1 << page_shift;
   if (tid == 0) runs = grown = 0;
   __syncthreads();
   {
-    // The slots of the row before, of the warp's row and of those behind it.
+    // The slots of the row before, of the warp's row and of those behind it that
+    // can be in its page.
     const int t = blockIdx.x * kAppendWarps + warp;
-    const int64_t at = static_cast<int64_t>(t) - 1 + lane;
-    const int x = at >= 0 && at < T ? __ldg(slots + at) : -2;
-    const int s0 = __shfl_sync(0xffffffffu, x, 1), before = __shfl_sync(0xffffffffu, x, 0);
+    const int before = t > 0 && t <= T ? __ldg(slots + t - 1) : -2;
+    int x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = 32 * k + lane;
+      x[k] = i < page && i < T - t ? __ldg(slots + t + i) : -2;
+    }
+    const int s0 = __shfl_sync(0xffffffffu, x[0], 0);
     const int off = s0 & (page - 1);
     if (static_cast<unsigned>(s0) < static_cast<unsigned>(n_slots) && (off == 0 || before != s0 - 1)) {
-      const unsigned same = __ballot_sync(0xffffffffu, lane > 0 && lane <= page - off && x == s0 + lane - 1);
-      const int rows = __ffs(~(same >> 1)) - 1;          // (31: or more)
+      int rows = 0;                                      // the first that does not go on ends the run
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = 32 * k + lane;
+        const unsigned same = __ballot_sync(0xffffffffu, i < page - off && x[k] == s0 + i);
+        if (rows == 32 * k) rows += same == 0xffffffffu ? 32 : __ffs(~same) - 1;
+      }
       if (rows <= kShortRun) {
         const int64_t pg = s0 >> page_shift;
         const float had = __shfl_sync(0xffffffffu, off && lane == 0 ? scales[pg] : 0.f, 0);  // (which lane 0 writes)
@@ -307,7 +318,9 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
           }
         }
       } else if (lane == 0) {
-        run_at[atomicAdd(&runs, 1)] = t;
+        const int i = atomicAdd(&runs, 1);
+        run_at[i] = t;
+        run_rows[i] = rows;
       }
     }
   }
@@ -322,20 +335,12 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
     const int t = run_at[i], s0 = __ldg(slots + t), off = s0 & (page - 1);
     const int64_t pg = s0 >> page_shift;
     const float had = off ? scales[pg] : 0.f;            // (written behind a barrier)
-    if (warp < 4) {                                      // (a page has 128 rows at most)
-      const bool in = tid < page - off && tid < T - t && __ldg(slots + t + tid) == s0 + tid;
-      const unsigned same = __ballot_sync(0xffffffffu, in);
-      if (lane == 0) part[warp] = same;
-    }
-    __syncthreads();
-    int rows = 0;                                        // the first that does not go on ends the run
-    for (int w = 0; w < 4 && rows == 32 * w; ++w) rows += part[w] == 0xffffffffu ? 32 : __ffs(~part[w]) - 1;
-    const int n = rows * D / 8;
+    const int n = run_rows[i] * D / 8;
     const uint4* src = reinterpret_cast<const uint4*>(kv_new + static_cast<int64_t>(t) * D);
     uint32_t top = __reduce_max_sync(0xffffffffu, largest(src, tid, kAppendThreads, n));
-    if (lane == 0) warp_top[warp] = top;
+    if (lane == 0) warp_top[i & 1][warp] = top;
     __syncthreads();
-    for (int w = 0; w < kAppendWarps; ++w) top = max(top, warp_top[w]);
+    for (int w = 0; w < kAppendWarps; ++w) top = max(top, warp_top[i & 1][w]);
     const float s = fmaxf(pow2f(scale_exponent(__uint_as_float(top << 16))), had);
     if (off && s > had) rescale(reinterpret_cast<uint4*>(cache + (pg << page_shift) * D), tid, kAppendThreads, off * D / 16, had / s);
     encode(src, reinterpret_cast<uint2*>(cache + static_cast<int64_t>(s0) * D), tid, kAppendThreads, n, 1.f / s);

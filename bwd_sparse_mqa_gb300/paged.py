@@ -161,7 +161,8 @@ def paged_kv_append(kv_new: torch.Tensor, slot_mapping: torch.Tensor, kv_cache: 
     e4m3's 448; it grows while the page fills (the page's older rows are
     rescaled) and starts afresh when the page's first row is written.  The rows
     of one page must be consecutive, with slots ascending by one, as
-    paged_plan lists them."""
+    paged_plan lists them; a page listed otherwise (a slot twice, its rows apart)
+    gets undefined codes and scale, the other pages theirs."""
     try:
         dev = kv_cache.get_device()
         n_pages, page_size, D = kv_cache.shape
