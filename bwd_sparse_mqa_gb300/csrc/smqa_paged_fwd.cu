@@ -1091,15 +1091,16 @@ int64_t blocks_per_token(const smqa_paged_shape& s) {
   return (slots + kBlk - 1) / kBlk;
 }
 // Whether ranges are whole tokens (index lists: all tokens have the same number
-// of blocks).  Splitting tokens evens the ranges out but costs the parts' way
-// through the workspace and the joining kernel, together about as long as eight
-// blocks take (128 tokens of 16 blocks, 76 ranges: 32 blocks at most per range
-// whole, 27 split).
+// of blocks).  Splitting tokens evens the ranges out but costs a read-out and a Q
+// more per range, the parts' way through the workspace and the joining kernel,
+// together about as long as twelve blocks take (topk=2048, 16 blocks: 100 tokens
+// of 128 heads on 76 ranges 80 us whole (32 blocks at most per range), 87 split
+// (22); 160 tokens of 64 heads on 152 ranges 80 us whole (32), 76 split (17)).
 bool whole_tokens(const smqa_paged_shape& s) {
   if (s.topk == 0) return blocks_per_token(s) <= 1;
   const int groups = (s.H + kHeads - 1) / kHeads;
   const int64_t parts = 152 / groups, nb = blocks_per_token(s);
-  return (s.T + parts - 1) / parts * nb <= s.T * nb / parts + 8;
+  return (s.T + parts - 1) / parts * nb <= s.T * nb / parts + 12;
 }
 // CTAs of a call: per head group, as many ranges as SMs (or as the tokens can
 // have blocks).
