@@ -179,12 +179,13 @@ __device__ __forceinline__ int slots_of(const PagedFwdParams& p, int t, int req,
   return n > 0 ? static_cast<int>(n) : 0;
 }
 // Blocks of token t: at least one (it writes O = 0), none for padding.
-__device__ __forceinline__ int blocks_of(const PagedFwdParams& p, int t) {
-  const int req = __ldg(p.token_req + t);
+__device__ __forceinline__ int blocks_of(const PagedFwdParams& p, int t, int req) {
   if (!live_token(p, req)) return 0;
   if (p.idx) return (p.topk + kBlk - 1) / kBlk;
   return max(1, (slots_of(p, t, req, __ldg(p.seq_lens + req)) + kBlk - 1) / kBlk);
 }
+
+__device__ __forceinline__ int blocks_of(const PagedFwdParams& p, int t) { return blocks_of(p, t, __ldg(p.token_req + t)); }
 
 // The two e4m3 pieces of 2^8 w for four weights 0 <= w <= 1.6875: hi the
 // nearest code (halves up), lo that of the rest.
@@ -686,6 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       const bool whole = b == 0 && stop == nb;
       const int slot = b == 0 ? 1 : 0;                   // of the CTA's two workspace parts
       left -= stop - b;
+      // (Asked for here: its answer takes 1600 cycles at the token's end.)
+      int next_req = left > 0 ? __ldg(p.token_req + t + 1) : -1;
 
       float m[2] = {-INFINITY, -INFINITY};
       float2 l[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // (even and odd slots apart)
@@ -857,8 +860,8 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       // before that the next token's Q, whose S then runs beside it.
       const int done = t;
       if (left > 0) {
-        do nb = blocks_of(p, ++t);
-        while (nb == 0);
+        for (++t; !live_token(p, next_req); next_req = __ldg(p.token_req + t)) ++t;
+        nb = blocks_of(p, t, next_req);
         b = 0;
         q.fetch(p, t, h0, heads, quarter, half, lane);
       }
