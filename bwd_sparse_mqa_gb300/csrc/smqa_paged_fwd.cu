@@ -350,13 +350,16 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
     mbar_init(bar(L::kBarNote + 1), kSoftmaxThreads / 64);
     mbar_init(bar(L::kBarQFull), kSoftmaxThreads / 32);
     mbar_init(bar(L::kBarDrain), 1);
-    *abort_flag = *reinterpret_cast<volatile int*>(p.status) != 0 ? 1 : 0;
     range->count = 0;
     end_tok[0] = -1;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc(base + L::kOffCtl, L::kTmemCols);
+  // So far beside the kernel before, whose results are read (or whose workspace
+  // is written) from here on.
+  grid_dependency_wait();
   grid_dependents_launch();
+  if (tid == 0) *abort_flag = *reinterpret_cast<volatile int*>(p.status) != 0 ? 1 : 0;
   // The CTA's range: the total number of blocks, and the tokens in which the
   // range begins and ends (each thread sums a run of tokens).
   {
@@ -1128,19 +1131,22 @@ cudaError_t launch(const PagedFwdParams& p, int ctas, cudaStream_t stream) {
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(smqa_paged_fwd_kernel<D>), L::kSmem, allowed);
   if (e != cudaSuccess) return e;
-  smqa_paged_fwd_kernel<D><<<ctas, kThreads, L::kSmem, stream>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || p.whole_tokens) return e;  // nothing to join
-  const bool few = ctas <= 64;                           // then with many parts each
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas) * (kHeads / kJoinHeads));
-  cfg.blockDim = dim3(D < 128 ? D : 128);
-  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::kSmem;
+  cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, smqa_paged_fwd_kernel<D>, p);
+  if (e != cudaSuccess || p.whole_tokens) return e;  // nothing to join
+  const bool few = ctas <= 64;                           // then with many parts each
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas) * (kHeads / kJoinHeads));
+  cfg.blockDim = dim3(D < 128 ? D : 128);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, few ? smqa_paged_join_kernel<D, 8> : smqa_paged_join_kernel<D, 2>, p, ctas);
 }
 
