@@ -45,6 +45,10 @@ __global__ void __launch_bounds__(kPlanThreads) smqa_paged_plan_kernel(const Pla
   const int page = 1 << p.page_shift;
   if (tid == 0) carry[0] = carry[1] = 0;
   __syncthreads();
+  // (Launched beside the kernel before, whose results are read from here on; the
+  // next one may be launched beside this.)
+  grid_dependency_wait();
+  grid_dependents_launch();
   for (int r0 = 0; r0 < p.R; r0 += kPlanThreads) {
     const int r = r0 + tid;
     int64_t tok = 0, pg = 0;
@@ -218,9 +222,9 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 // left to the whole CTA.  A run's rows are one flat range in kv_new and in the
 // cache, read twice, the second time from L1.  Bound by latency: 8192 rows
 // (D=512, pages of 64: 130 runs) took 11.9 us with a CTA per row, most of which
-// left at once, and take 7.3 us so; 128 single rows 2.8 us against 2.5.
+// left at once, and take 7.0 us so; 128 single rows 2.5 us.
 constexpr int kAppendWarps = 16, kAppendThreads = 32 * kAppendWarps;
-constexpr int kShortRun = 8;                             // rows (512 runs of 6: 4.6 us by warps, 6.1 by CTAs)
+constexpr int kShortRun = 8;                             // rows (512 runs of 6: 4.4 us by warps, 6.1 by CTAs)
 
 // The largest finite magnitude of uint4 i, i + step, ... below n, as bf16 bits
 // (which order like values).
@@ -280,6 +284,8 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
   const int page = 1 << page_shift;
   if (tid == 0) runs = grown = 0;
   __syncthreads();
+  grid_dependency_wait();                                // (launched beside the kernel before,
+  grid_dependents_launch();                              // the next one beside this)
   {
     // The slots of the row before, of the warp's row and of those behind it that
     // can be in its page.
@@ -429,14 +435,17 @@ smqa_status smqa_paged_plan(const int32_t* context_lens, const int32_t* query_le
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   if (in_place) {
     cfg.gridDim = dim3(8);
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 8;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 8;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
   } else {
     const int64_t work = std::max<int64_t>(static_cast<int64_t>(R) * max_pages, max_tokens);
     cfg.gridDim = dim3(static_cast<unsigned>(
@@ -477,10 +486,18 @@ smqa_status smqa_paged_append(const void* kv_new, const int32_t* slot_mapping, i
   if (!kv_new || !slot_mapping || !kv_cache || !kv_scales || !is_aligned(kv_new, 16) ||
       !is_aligned(kv_cache, 16) || !is_aligned(slot_mapping, 4) || !is_aligned(kv_scales, 4))
     return refuse(SMQA_ERR_INVALID_ARG, "null or misaligned pointer");
-  smqa_paged_append_kernel<<<(T - 1) / kAppendWarps + 1, kAppendThreads, 0, stream>>>(
-      static_cast<const __nv_bfloat16*>(kv_new), slot_mapping, T, D, shift, n_pages * page_size,
-      static_cast<uint8_t*>(kv_cache), kv_scales);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((T - 1) / kAppendWarps + 1));
+  cfg.blockDim = dim3(kAppendThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(
+      &cfg, smqa_paged_append_kernel, static_cast<const __nv_bfloat16*>(kv_new), slot_mapping, T, D,
+      shift, n_pages * page_size, static_cast<uint8_t*>(kv_cache), kv_scales);
   if (e != cudaSuccess) return cuda_failure(e, "paged append launch");
   return SMQA_OK;
 }
