@@ -684,14 +684,99 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
     int t = rg.tok, b = rg.off, nb = blocks_of(p, t);
     QLoader<D> q;
     q.fetch(p, t, h0, heads, quarter, half, lane);
-    float2 rs = q.place(base, smem, tmem, quarter, half, lane);
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(L::kBarQFull));
+    float2 rs = make_float2(0.f, 0.f);
+    int done = -1, slot = 0;                             // the token before (-1: none yet), its part
+    bool whole = false;
+    // (One copy of the code that places Q and of the one that reads O out: the
+    // first time through a piece of code is slow.)
     while (true) {
+      // The next token's Q, whose S then runs beside what is left of the one before.
+      const bool more = done < 0 || left > 0;
+      if (more) {
+        rs = q.place(base, smem, tmem, quarter, half, lane);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kBarQFull));
+      }
+      // The token's (or its part's) result.
+      if (done >= 0) {
+        float* ws = reinterpret_cast<float*>(p.ws + kLeftoverBytes) +
+                    (static_cast<int64_t>(blockIdx.x) * 2 + slot) * part_floats(D);
+        if (tid < kHeads) {                                // thread = head
+          const int hl = tid;
+          const float m_end = head_end[hl], l_end = head_sum[hl] + head_sum[kHeads + hl];
+          if (whole) {
+            const float top = fmaxf(m_end, sink);
+            float inv, lse;
+            if (top == -INFINITY) {                        // nothing at all (or only NaN)
+              inv = l_end * 0.f;
+              lse = l_end != l_end ? l_end : -INFINITY;
+            } else {
+              const float f = exp2f(m_end - top);
+              const float total = fmaf(l_end, 4.f * f, exp2f(sink - top));
+              inv = 4.f * kCodeUnit * f / total;           // 4 = 2^kShift
+              lse = log2f(total) + top;
+            }
+            head_f[hl] = inv;
+            if (hl < heads) p.lse[static_cast<int64_t>(done) * p.H + h0 + hl] = lse;
+          } else {
+            ws[part_o(D) + hl] = m_end;
+            ws[part_o(D) + kHeads + hl] = l_end;
+          }
+        }
+        if (whole) {
+          bar_sync(1, kSoftmaxThreads);
+          // 32 heads x 32 columns a time through the warp's part of P's place
+          // (free now) to 64-byte rows: [head][4 pieces of 8 columns].
+          uint8_t* tile = smem + L::kOffP + warp * 2048;
+          const uint32_t tile_at = base + L::kOffP + warp * 2048;
+          float2 f[4];                                     // of heads 8 j + 2 quad, + 1
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[j] = *reinterpret_cast<const float2*>(head_f + half * 32 + 8 * j + 2 * quad);
+          if (D >= 128 || quarter < D / 32) {
+#pragma unroll 1
+            for (int c = 0; c < L::kChunks; ++c) {
+              float v[2][16];                              // columns 0-15, 16-31 of the quarter's 32
+              tmem_ld16x32x2(tmem + lanes + L::kTmemO + c * kHeads + half * 32, v[0], v[1]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {                // 8 heads: four 8-column matrices
+                uint32_t w[4];
+#pragma unroll
+                for (int o = 0; o < 4; ++o)
+                  w[o] = pack_bf16x2(v[o >> 1][4 * j + 2 * (o & 1)] * f[j].x, v[o >> 1][4 * j + 2 * (o & 1) + 1] * f[j].y);
+                const uint32_t h = static_cast<uint32_t>(8 * j + (lane & 7));
+                stmatrix_trans_x4(tile_at + h * 64u + ((static_cast<uint32_t>(lane >> 3) ^ ((h >> 1) & 3u)) << 4), w[0], w[1], w[2], w[3]);
+              }
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int h = 8 * i + (lane >> 2);
+                const uint4 x = *reinterpret_cast<const uint4*>(tile + h * 64 + ((quad ^ ((h >> 1) & 3)) << 4));
+                if (half * 32 + h < heads)
+                  *reinterpret_cast<uint4*>(p.o + (static_cast<int64_t>(done) * p.H + h0 + half * 32 + h) * D + c * 128 + 32 * quarter + quad * 8) = x;
+              }
+              __syncwarp();
+            }
+          }
+        } else if (D >= 128 || quarter < D / 32) {
+          float4* part = reinterpret_cast<float4*>(ws) + half * 8 * 128 + 32 * quarter + lane;
+#pragma unroll 1
+          for (int c = 0; c < L::kChunks; ++c) {           // 128 of D, 32 heads per warpgroup
+            float o[32];
+            tmem_ld32(tmem + lanes + L::kTmemO + c * kHeads + half * 32, o);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              __stcg(part + (c * (kHeads / 4) + i / 4) * 128, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+          }
+        }
+        tc_fence_before();
+        if (!more) break;
+        // Both have read O and P's place before either brings the next token's.
+        bar_sync(1, kSoftmaxThreads);
+      }
       const int stop = static_cast<int>(min(static_cast<int64_t>(nb), b + left));
-      const bool whole = b == 0 && stop == nb;
-      const int slot = b == 0 ? 1 : 0;                   // of the CTA's two workspace parts
+      whole = b == 0 && stop == nb;
+      slot = b == 0 ? 1 : 0;                             // of the CTA's two workspace parts
       left -= stop - b;
       // (Asked for here: its answer takes 1600 cycles at the token's end.)
       int next_req = left > 0 ? __ldg(p.token_req + t + 1) : -1;
@@ -862,9 +947,8 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       }
       if (!run) break;
 
-      // The token's (or its part's) result, once its last products are done;
-      // before that the next token's Q, whose S then runs beside it.
-      const int done = t;
+      // On to the next token, once the last products are done.
+      done = t;
       if (left > 0) {
         for (++t; !live_token(p, next_req); next_req = __ldg(p.token_req + t)) ++t;
         nb = blocks_of(p, t, next_req);
@@ -885,85 +969,6 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       __syncwarp();
       bar_sync(1, kSoftmaxThreads);
       tc_fence_after();
-      if (left > 0) {
-        rs = q.place(base, smem, tmem, quarter, half, lane);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kBarQFull));
-      }
-      float* ws = reinterpret_cast<float*>(p.ws + kLeftoverBytes) +
-                  (static_cast<int64_t>(blockIdx.x) * 2 + slot) * part_floats(D);
-      if (tid < kHeads) {                                // thread = head
-        const int hl = tid;
-        const float m_end = head_end[hl], l_end = head_sum[hl] + head_sum[kHeads + hl];
-        if (whole) {
-          const float top = fmaxf(m_end, sink);
-          float inv, lse;
-          if (top == -INFINITY) {                        // nothing at all (or only NaN)
-            inv = l_end * 0.f;
-            lse = l_end != l_end ? l_end : -INFINITY;
-          } else {
-            const float f = exp2f(m_end - top);
-            const float total = fmaf(l_end, 4.f * f, exp2f(sink - top));
-            inv = 4.f * kCodeUnit * f / total;           // 4 = 2^kShift
-            lse = log2f(total) + top;
-          }
-          head_f[hl] = inv;
-          if (hl < heads) p.lse[static_cast<int64_t>(done) * p.H + h0 + hl] = lse;
-        } else {
-          ws[part_o(D) + hl] = m_end;
-          ws[part_o(D) + kHeads + hl] = l_end;
-        }
-      }
-      if (whole) {
-        bar_sync(1, kSoftmaxThreads);
-        // 32 heads x 32 columns a time through the warp's part of P's place
-        // (free now) to 64-byte rows: [head][4 pieces of 8 columns].
-        uint8_t* tile = smem + L::kOffP + warp * 2048;
-        const uint32_t tile_at = base + L::kOffP + warp * 2048;
-        float2 f[4];                                     // of heads 8 j + 2 quad, + 1
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = *reinterpret_cast<const float2*>(head_f + half * 32 + 8 * j + 2 * quad);
-        if (D >= 128 || quarter < D / 32) {
-#pragma unroll 1
-          for (int c = 0; c < L::kChunks; ++c) {
-            float v[2][16];                              // columns 0-15, 16-31 of the quarter's 32
-            tmem_ld16x32x2(tmem + lanes + L::kTmemO + c * kHeads + half * 32, v[0], v[1]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {                // 8 heads: four 8-column matrices
-              uint32_t w[4];
-#pragma unroll
-              for (int o = 0; o < 4; ++o)
-                w[o] = pack_bf16x2(v[o >> 1][4 * j + 2 * (o & 1)] * f[j].x, v[o >> 1][4 * j + 2 * (o & 1) + 1] * f[j].y);
-              const uint32_t h = static_cast<uint32_t>(8 * j + (lane & 7));
-              stmatrix_trans_x4(tile_at + h * 64u + ((static_cast<uint32_t>(lane >> 3) ^ ((h >> 1) & 3u)) << 4), w[0], w[1], w[2], w[3]);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int h = 8 * i + (lane >> 2);
-              const uint4 x = *reinterpret_cast<const uint4*>(tile + h * 64 + ((quad ^ ((h >> 1) & 3)) << 4));
-              if (half * 32 + h < heads)
-                *reinterpret_cast<uint4*>(p.o + (static_cast<int64_t>(done) * p.H + h0 + half * 32 + h) * D + c * 128 + 32 * quarter + quad * 8) = x;
-            }
-            __syncwarp();
-          }
-        }
-      } else if (D >= 128 || quarter < D / 32) {
-        float4* part = reinterpret_cast<float4*>(ws) + half * 8 * 128 + 32 * quarter + lane;
-#pragma unroll 1
-        for (int c = 0; c < L::kChunks; ++c) {           // 128 of D, 32 heads per warpgroup
-          float o[32];
-          tmem_ld32(tmem + lanes + L::kTmemO + c * kHeads + half * 32, o);
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            __stcg(part + (c * (kHeads / 4) + i / 4) * 128, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
-        }
-      }
-      tc_fence_before();
-      if (left == 0) break;
-      // Both have read O and P's place before either brings the next token's.
-      bar_sync(1, kSoftmaxThreads);
     }
   }
 
