@@ -12,11 +12,6 @@ __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
   return d;
 }
-__device__ __forceinline__ uint16_t e4m3x2(__half2 v) {
-  uint16_t d;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(*reinterpret_cast<uint32_t*>(&v)));
-  return d;
-}
 // The values of two codes (exact).
 __device__ __forceinline__ __half2 e4m3x2_half2(uint16_t v) {
   uint32_t h;
@@ -176,19 +171,6 @@ __device__ __forceinline__ void reg_dealloc() {
 // Barrier `id` over `threads` threads (whole warps).
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-// The same barrier, returning whether any thread passed true.
-__device__ __forceinline__ bool bar_any(int id, int threads, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %3, 0;\n\t"
-      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(v))
-      : "memory");
-  return r != 0;
 }
 
 // cp.async of 16 bytes, or of 16 zero bytes (nothing is read then).
