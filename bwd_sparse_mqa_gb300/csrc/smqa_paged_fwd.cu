@@ -904,29 +904,19 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
         if (raised[0] | raised[1]) {                     // O of these heads, rescaled
           tc_fence_after();
           const uint32_t o = tmem + lanes + L::kTmemO;
-          if (__popc(raised[0]) + __popc(raised[1]) <= 16) {  // column by column
+          // A column at a time, few as they mostly are: a second form for many heads at
+          // once cost every call 1 to 2 % by its size alone.
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-              for (unsigned some = raised[u]; some != 0; some &= some - 1) {
-                const int h = 32 * u + __ffs(some) - 1;
-                const float f = note->f[h];
-                float v[L::kChunks];
-                tmem_ld1xn<L::kChunks, kHeads>(o + h, v);
+          for (int u = 0; u < 2; ++u)
+            for (unsigned some = raised[u]; some != 0; some &= some - 1) {
+              const int h = 32 * u + __ffs(some) - 1;
+              const float f = note->f[h];
+              float v[L::kChunks];
+              tmem_ld1xn<L::kChunks, kHeads>(o + h, v);
 #pragma unroll
-                for (int c = 0; c < L::kChunks; ++c) tmem_st1(o + c * kHeads + h, v[c] * f);
-              }
-            tmem_wait_st();
-          } else {                                       // all of it
-#pragma unroll 1
-            for (int c = 0; c < 2 * L::kChunks; ++c) {
-              float v[32];
-              tmem_ld32(o + c * 32, v);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if ((raised[c & 1] >> i) & 1u) v[i] *= note->f[(c & 1) * 32 + i];
-              tmem_st32(o + c * 32, v);
+              for (int c = 0; c < L::kChunks; ++c) tmem_st1(o + c * kHeads + h, v[c] * f);
             }
-          }
+          tmem_wait_st();
         }
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
