@@ -57,9 +57,9 @@
 // 64 and 128 fill it by two thirds) and a block 3500 in all.  A token's end and
 // the next one's start take some 20000 more (the next Q's loads 4000, placing it
 // 4000 to 10000, the read-out of O 6000).  Tried and slower (128 tokens H=128
-// topk=2048, 75 us so): O's pieces without the collector, S and O issued by two
+// topk=2048, 74 us so): O's pieces without the collector, S and O issued by two
 // warps, 93; P in a ring of three halves, written and multiplied by halves, 90;
-// blocks of 64 slots, 84.  128 tokens take 75 us, 1024 tokens 483 (H=128,
+// blocks of 64 slots, 84.  128 tokens take 74 us, 1024 tokens 480 (H=128,
 // topk=2048), a lone one 17, its join included.
 #include <cuda_runtime.h>
 
