@@ -1,5 +1,6 @@
 // smqa_paged.cuh -- building blocks of the 8-bit paged cache's kernels: e4m3
-// conversions, tcgen05 MMAs on e4m3 operands and a vote over some warps.
+// conversions, tcgen05 MMAs on e4m3 operands (plain and block-scaled), TMEM
+// accesses, and the start-up beside the kernel before.
 #pragma once
 
 #include "smqa_ptx.cuh"
@@ -41,26 +42,49 @@ __device__ __forceinline__ void mma8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
+__device__ __forceinline__ void mma8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+// Instruction descriptor for kind::mxf8f6f4: e4m3 A/B, an fp32 accumulator and
+// ue8m0 scale factors (a power of two by its exponent's bits), one per row of A
+// and of B and 32 elements of K: B's is byte `b_byte` of its row's word in TMEM,
+// A's byte 0.  Rows of a factor go by lane (row mod 32, the same in all four
+// lane quarters) and column (row / 32).
+__host__ __device__ constexpr uint32_t idesc_mx_e4m3_f32(int M, int N, bool a_mn_major, int b_byte) {
+  return (static_cast<uint32_t>(b_byte) << 4) | (static_cast<uint32_t>(a_mn_major) << 15) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(M >> 7) << 27);
+}
 // A kept in the tensor core's collector, and the A that the instruction before
 // left there (the same descriptor): its bytes are read from shared memory once
 // for both.
-__device__ __forceinline__ void mma8_ss_keep(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                        uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_mx_ss_keep(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t a_scale, uint32_t b_scale,
+                                        uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "elect.sync _|q, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::fill [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X.collector::a::fill "
+      "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate));
 }
-__device__ __forceinline__ void mma8_ss_again(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                        uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_mx_ss_again(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t a_scale, uint32_t b_scale,
+                                        uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "elect.sync _|q, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::lastuse [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X.collector::a::lastuse "
+      "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate));
 }
 __device__ __forceinline__ void mma_commit_elect(uint32_t bar) {
   asm volatile(
@@ -151,9 +175,19 @@ __device__ __forceinline__ void tmem_ld1xn(uint32_t t, float (&v)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
 }
-// (A store: tmem_wait_st waits for it.)
+// (Stores: tmem_wait_st waits for them.)
 __device__ __forceinline__ void tmem_st1(uint32_t t, float v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(t), "r"(__float_as_uint(v)) : "memory");
+}
+// Four and eight consecutive columns from this thread's lane.
+__device__ __forceinline__ void tmem_st4u(uint32_t t, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(t), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8u(uint32_t t, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 

@@ -13,14 +13,18 @@
 //   q  = 2^-k (hi + lo / 32), k per row so that the largest value of 2^k q
 //        lies in [128, 256): bf16's 8 bits fit the two pieces exactly down to
 //        2^-22 of the row's largest value;
-//   w  = 2^(y_j - m - 2), y_j = x_j + log2 s_j: the weight that multiplies the
-//        codes, 2^8 w = hi + lo: a relative error of 2^-8 + 2^-11 at most, down
-//        to 2^-14 of the largest weight.  m is set 2 above the maximum of y of
-//        the token's first block, so that the largest weight's code is 2^4 at
-//        least, and may fall 2.75 behind the running maximum (2^8.75 < 448,
-//        e4m3's largest) before O is rescaled, which holds the pipeline up
-//        (128 tokens H=128 topk=2048, page scales up to 2^3 apart: 2 us more
-//        with m at the maximum).  l adds w / s_j in fp32.
+//   w  = 2^(y_j - u), y_j = x_j + log2 s_j: the weight that multiplies the
+//        codes, 2^8 w = hi + lo / 32.  u is an integer for each head and group of
+//        32 slots, the least at or above the group's largest y, so that its
+//        largest w lies in (1/2, 1]: a weight has a relative error of 2^-8 + 2^-11
+//        at most down to 2^-14 of its group's largest, and one of 2^-22 of that
+//        below.  The sums' unit is 2^m; the block-scaled MMA (kind::mxf8f6f4)
+//        multiplies each group's products by 2^(u - m), and hi's and lo's by their
+//        own factor.  One unit for all of a token's slots, as two e4m3 pieces
+//        could hold it, ends 2^14 below the largest weight: a long flat rest
+//        beside one heavy position would be lost from O, whatever its sum.
+//        m is set by the token's first block and raised, O being rescaled, where
+//        later ones exceed it by more than 2^32.  l adds w / s_j in fp32.
 //        An fp16 number below 2 holds an e4m3 code of its 2^8-fold in bits
 //        7-13 (and the sign), subnormals included, so both pieces come from
 //        integer operations on pairs of fp16: the conversion instructions
@@ -39,8 +43,8 @@
 //                        into a 128-byte-swizzled tile [D/128][128 slots][128],
 //                        three tiles in a ring, a warp's 32 rows freed and
 //                        refilled on their own; the slots' scale factors;
-//   MMA (warp 8)         S = Q.K^T: M = 128 (64 heads x 2 pieces, A in TMEM),
-//                        N = 128 slots; O^T += V^T.P^T: M = 128 of D (A: the
+//   MMA (warp 8)         S = Q.K^T: M = 128 (64 heads x 2 pieces, A in TMEM,
+//                        its last 32 of D in shared memory), N = 128 slots; O^T += V^T.P^T: M = 128 of D (A: the
 //                        same tile read MN-major, kept in the collector for
 //                        the second piece), N = 64 heads, K = 128 slots, for
 //                        both pieces of P;
@@ -49,18 +53,20 @@
 //                        in one lane; weights, their two pieces to shared
 //                        memory, Q's pieces into TMEM at the start of a token
 //                        and O^T out of it at the end.
-// TMEM: S 128 columns, O^T D/2, Q D/4.
+// TMEM: S 128 columns, O^T D/2, Q D/4 (D = 512: 8 less), factors 8.
 //
 // Bound by shared memory: a block writes 64 KB of rows into it and reads them
 // for S, again for O (once, by the collector) and P four times (once per 128 of
-// D), 2050 cycles at 128 bytes a clock; the tensor core takes 2500 for it (N of
-// 64 and 128 fill it by two thirds) and a block 3500 in all.  A token's end and
-// the next one's start take some 20000 more (the next Q's loads 4000, placing it
-// 4000 to 10000, the read-out of O 6000).  Tried and slower (128 tokens H=128
-// topk=2048, 74 us so): O's pieces without the collector, S and O issued by two
-// warps, 93; P in a ring of three halves, written and multiplied by halves, 90;
-// blocks of 64 slots, 84.  128 tokens take 74 us, 1024 tokens 480 (H=128,
-// topk=2048), a lone one 17, its join included.
+// D), 2050 cycles at 128 bytes a clock; the tensor core takes 2700 for it (N of
+// 64 and 128 fill it by two thirds; the factors make an instruction of O 7 cycles
+// longer, eight in a row 704 instead of 645) and a block 3700 in all.  A token's
+// end and the next one's start take some 20000 more (the next Q's loads 4000,
+// placing it 4000 to 10000, the read-out of O 6000).  Tried and slower, before the
+// factors (128 tokens H=128 topk=2048, 80 us then): O's pieces without the
+// collector, S and O issued by two warps, 93; P in a ring of three halves, written
+// and multiplied by halves, 90; blocks of 64 slots, 84.  128 tokens take 78 us,
+// 1024 tokens 501 (H=128, topk=2048), a lone one 17.3, its join included; with one
+// unit per token instead of the groups' (which loses flat rests) 74, 480 and 17.2.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -85,18 +91,24 @@ static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs <= 512, "registers of the launch
 // Warps 0-7 take more registers, 8-15 give some back: a warpgroup does one of
 // the two as a whole, or none of its warps would go on.
 static_assert(kSoftmaxThreads == 256 && kMmaWarp == 8 && kGatherWarp0 == 12 && kThreads == 512, "roles by warpgroup");
-constexpr float kShift = 2.f;             // weights are 2^-2 at m
-constexpr float kAbove = 2.f;             // how far m is set above the maximum
-constexpr float kLag = 2.75f;             // and how far it may fall behind
+// How far the running maximum may exceed m (in log2), and how far below m a group's
+// unit may lie: with 448 2^8 per slot both leave fp32's range alone, and what lies
+// further below is lost beside the slot that set m.
+constexpr float kLag = 32.f, kDepth = 120.f;
 constexpr float kCodeUnit = 0x1p-8f;      // what the tensor core's P counts
+constexpr float kFine = 32.f;             // P's lo counts as much less,
+constexpr uint32_t kFineSteps = 0x05050505u;  // in four factors' exponents
 
 // What the warpgroup that takes a block tells the other about it: whether it is
-// its token's last, and the heads whose maximum it has raised, to `to`, O and l
-// being multiplied by f (of a token's first block, `to` has every head's).
+// its token's last, and the heads whose m it has raised, to `to`, O and l being
+// multiplied by f (of a token's first block, `to` has every head's).  `units` is
+// for its own warps: the exponents of 2^(u - m) of each head's four groups of
+// slots, as ue8m0 bytes.
 struct Note {
   unsigned heads[2];
   int last, failed;
   float to[kHeads], f[kHeads];
+  uint32_t units[kHeads];
 };
 static_assert(sizeof(Note) % 8 == 0, "alignment of what follows");
 // A note is cleared four blocks before it is written (by the same warpgroup:
@@ -116,7 +128,11 @@ struct PagedLayout {
   // pairs of one lane together (meta_at, rec_at).
   static constexpr int kMeta = 4 * kBlk / 2 + kBlk;          // floats
   static constexpr uint32_t kOffP = kStages * kStageBytes;
-  static constexpr uint32_t kOffA = kOffP + 2 * kPieceBytes; // [kStages][kMeta]: a, c, r
+  // The last 32 elements of Q's rows, where TMEM has no room for them: as 8 x 16-byte
+  // matrices, [16 groups of 8 rows][2][8][16].
+  static constexpr bool kQTail = D == 512;
+  static constexpr uint32_t kOffQ = kOffP + 2 * kPieceBytes;
+  static constexpr uint32_t kOffA = kOffQ + (kQTail ? 4096 : 0);  // [kStages][kMeta]: a, c, r
   static constexpr uint32_t kOffFlags = kOffA + kStages * kMeta * 4;  // [kStages]
   static constexpr uint32_t kOffHead = (kOffFlags + kStages * 4 + 15) & ~15u;  // float [64]
   static constexpr uint32_t kOffMax = kOffHead + kHeads * 4;   // uint32 [2][64] (QLoader)
@@ -145,7 +161,10 @@ struct PagedLayout {
   static constexpr uint32_t kTmemS = 0, kTmemO = 128;
   static constexpr uint32_t kTmemQ = kTmemO + kChunks * kHeads;
   static constexpr uint32_t kTmemCols = D == 512 ? 512 : 256;
-  static_assert(kTmemQ + D / 4 <= kTmemCols, "TMEM budget");
+  // The block-scaled MMA's factors: of V's 128 rows (all 1) and of the 64 heads, for
+  // P's hi and lo.
+  static constexpr uint32_t kTmemFV = kTmemCols - 8, kTmemFHi = kTmemFV + 4, kTmemFLo = kTmemFHi + 2;
+  static_assert(kTmemQ + (D - (kQTail ? 32 : 0)) / 4 <= kTmemFV, "TMEM budget");
 };
 
 // The range of blocks of a CTA: from block `off` of token `tok`, `count` blocks.
@@ -189,16 +208,17 @@ __device__ __forceinline__ int blocks_of(const PagedFwdParams& p, int t, int req
 
 __device__ __forceinline__ int blocks_of(const PagedFwdParams& p, int t) { return blocks_of(p, t, __ldg(p.token_req + t)); }
 
-// The two e4m3 pieces of 2^8 w for four weights 0 <= w <= 1.6875: hi the
-// nearest code (halves up), lo that of the rest.
+// The two e4m3 pieces of 2^8 w for four weights 0 <= w <= 1: hi the nearest code
+// (halves up), lo that of 32 times the rest (which is 2^-5 at most).
 __device__ __forceinline__ void split_e4m3x4(float2 w01, float2 w23, uint32_t& hi, uint32_t& lo) {
   const __half2 a = __floats2half2_rn(w01.x, w01.y), b = __floats2half2_rn(w23.x, w23.y);
   const uint32_t ra = *reinterpret_cast<const uint32_t*>(&a) + 0x00400040u;
   const uint32_t rb = *reinterpret_cast<const uint32_t*>(&b) + 0x00400040u;
   hi = __byte_perm(ra << 1, rb << 1, 0x7531);
   const uint32_t ka = ra & 0xff80ff80u, kb = rb & 0xff80ff80u;
-  const __half2 da = __hsub2(a, *reinterpret_cast<const __half2*>(&ka));
-  const __half2 db = __hsub2(b, *reinterpret_cast<const __half2*>(&kb));
+  const __half2 fine = __float2half2_rn(kFine);
+  const __half2 da = __hmul2(__hsub2(a, *reinterpret_cast<const __half2*>(&ka)), fine);
+  const __half2 db = __hmul2(__hsub2(b, *reinterpret_cast<const __half2*>(&kb)), fine);
   const uint32_t sa = *reinterpret_cast<const uint32_t*>(&da) + 0x00400040u;
   const uint32_t sb = *reinterpret_cast<const uint32_t*>(&db) + 0x00400040u;
   // The sign next to the code (bit 14 is free: the values are below 2).
@@ -307,7 +327,16 @@ struct QLoader {
           w[4 * k + 2] = x.z;
           w[4 * k + 3] = x.w;
         }
-        tmem_st16u(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + L::kTmemQ + (half * kC + c) * 16, w);
+        const uint32_t to = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + L::kTmemQ + (half * kC + c) * 16;
+        if (L::kQTail && half == 1 && c == kC - 1) {     // 32 of the 64 elements to shared memory
+          tmem_st8u(to, w);
+          uint4* tail = reinterpret_cast<uint4*>(smem + L::kOffQ + quarter * 1024 + (lane >> 3) * 256 + (lane & 7) * 16);
+          tail[0] = make_uint4(w[8], w[9], w[10], w[11]);
+          tail[8] = make_uint4(w[12], w[13], w[14], w[15]);
+          tmem_wait_st();
+        } else {
+          tmem_st16u(to, w);
+        }
         __syncwarp();
       }
     }
@@ -569,17 +598,21 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
     // The whole warp runs this, one lane of it issues.
     if (warp == kMmaWarp) {
       constexpr uint32_t idesc_s = idesc_e4m3_f32(128, kBlk, false);
-      constexpr uint32_t idesc_o = idesc_e4m3_f32(128, kHeads, true);
       const uint64_t d_k = smem_desc(base, 16u, 1024u, kSwizzle128B);
       const uint64_t d_v = smem_desc(base, L::kChunkBytes, 1024u, kSwizzle128B);
       const uint64_t d_p = smem_desc(base + L::kOffP, 16u, 1024u, kSwizzle128B);
+      const uint64_t d_q = smem_desc(base + L::kOffQ, 128u, 256u, 0u);
       const volatile int* flags_of = reinterpret_cast<const volatile int*>(smem + L::kOffFlags);
       auto issue_s = [&](int st) {
         const uint64_t k = d_k + ((static_cast<uint32_t>(st) * L::kStageBytes) >> 4);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-          mma8_ts(tmem + L::kTmemS, tmem + L::kTmemQ + c * 8,
-                  k + (((c / 4) * L::kChunkBytes + (c % 4) * 32u) >> 4), idesc_s, c != 0 ? 1u : 0u);
+        for (int c = 0; c < D / 32; ++c) {
+          const uint64_t kd = k + (((c / 4) * L::kChunkBytes + (c % 4) * 32u) >> 4);
+          if (L::kQTail && c == D / 32 - 1)
+            mma8_ss(tmem + L::kTmemS, d_q, kd, idesc_s, 1u);
+          else
+            mma8_ts(tmem + L::kTmemS, tmem + L::kTmemQ + c * 8, kd, idesc_s, c != 0 ? 1u : 0u);
+        }
         mma_commit_elect(bar(L::kBarSFull));
       };
       auto issue_o = [&](int e, int st, bool first) {
@@ -590,8 +623,11 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
           for (int c = 0; c < L::kChunks; ++c) {
             const uint64_t ad = v + ((c * L::kChunkBytes + k * 4096u) >> 4);
             const uint64_t bd = d_p + ((k * 32u) >> 4);
-            mma8_ss_keep(tmem + L::kTmemO + c * kHeads, ad, bd, idesc_o, (!first || k > 0) ? 1u : 0u);
-            mma8_ss_again(tmem + L::kTmemO + c * kHeads, ad, bd + (L::kPieceBytes >> 4), idesc_o, 1u);
+            const uint32_t idesc_o = idesc_mx_e4m3_f32(128, kHeads, true, k);
+            mma_mx_ss_keep(tmem + L::kTmemO + c * kHeads, ad, bd, idesc_o, tmem + L::kTmemFV, tmem + L::kTmemFHi,
+                           (!first || k > 0) ? 1u : 0u);
+            mma_mx_ss_again(tmem + L::kTmemO + c * kHeads, ad, bd + (L::kPieceBytes >> 4), idesc_o, tmem + L::kTmemFV,
+                            tmem + L::kTmemFLo, 1u);
           }
           mma_commit_elect(bar(L::kBarEmpty + 4 * st + k));
         }
@@ -678,6 +714,10 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
     bool bad = *abort_flag != 0;                         // a wait of this thread has failed
     const float sink = tid < heads ? __ldg(p.sink + h0 + tid) * 1.4426950408889634f : 0.f;  // (thread = head)
     if (tid < kNotes) notes[tid].heads[0] = notes[tid].heads[1] = notes[tid].failed = 0;
+    if (half == 0) {                                     // V's factors (seen by the tensor core as Q is)
+      tmem_st4u(tmem + lanes + L::kTmemFV, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+      tmem_wait_st();
+    }
     bar_sync(1, kSoftmaxThreads);
     // The CTA's tokens, or parts of tokens, one after another.
     int t = rg.tok, b = rg.off, nb = blocks_of(p, t);
@@ -694,6 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
       if (more) {
         rs = q.place(base, smem, tmem, quarter, half, lane);
         tc_fence_before();
+        if (L::kQTail) fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::kBarQFull));
       }
@@ -712,8 +753,8 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
               lse = l_end != l_end ? l_end : -INFINITY;
             } else {
               const float f = exp2f(m_end - top);
-              const float total = fmaf(l_end, 4.f * f, exp2f(sink - top));
-              inv = 4.f * kCodeUnit * f / total;           // 4 = 2^kShift
+              const float total = fmaf(l_end, f, exp2f(sink - top));
+              inv = kCodeUnit * f / total;
               lse = log2f(total) + top;
             }
             head_f[hl] = inv;
@@ -834,30 +875,45 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
             }
           }
         }
-        // The maxima: set by a token's first block, raised where this block's
-        // outran the lag.
+        // The groups' maxima.  m is set by a token's first block, raised where this
+        // block's outran it.
+        float u[2][4];                                   // u of the groups
+        uint32_t unit_of[2];                             // the exponents of 2^(u - m)
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const int h = hq + 8 * g;
-          float top = fmaxf(y[g][0].x, y[g][0].y);
 #pragma unroll
-          for (int j = 1; j < 16; ++j) top = fmax3f(top, y[g][j].x, y[g][j].y);
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const float mx = top + kAbove;
+          for (int k = 0; k < 4; ++k) {
+            float t = fmaxf(y[g][4 * k].x, y[g][4 * k].y);
+#pragma unroll
+            for (int j = 4 * k + 1; j < 4 * k + 4; ++j) t = fmax3f(t, y[g][j].x, y[g][j].y);
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+            u[g][k] = ceilf(fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2)));
+          }
+          const float top = fmaxf(fmaxf(u[g][0], u[g][1]), fmaxf(u[g][2], u[g][3]));
           if (first) {
-            if (lead) note->to[h] = mx;
-            m[g] = mx;
+            if (lead) note->to[h] = top;
+            m[g] = top;
           } else if (top > m[g] + kLag) {
-            const float f = fast_exp2(m[g] - mx);
+            const float f = fast_exp2(m[g] - top);
             l[g] = mul2(l[g], make_float2(f, f));
-            m[g] = mx;
+            m[g] = top;
             if (lead) {
-              note->to[h] = mx;
+              note->to[h] = top;
               note->f[h] = f;
               atomicOr(&note->heads[h >> 5], 1u << (h & 31));
             }
           }
+          // (Nothing yet: any unit will do.  A NaN becomes a factor of 1; its weight is NaN.)
+          const float m0 = m[g] == -INFINITY ? 0.f : m[g];
+          uint32_t units = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            u[g][k] = fmaxf(u[g][k], m0 - kDepth);
+            units |= static_cast<uint32_t>(127 + static_cast<int>(u[g][k] - m0)) << (8 * k);
+          }
+          if (lead) note->units[h] = units;
+          unit_of[g] = units;
         }
         if (bad) note->failed = 1;
         if (lane == 0 && quarter == 0) {
@@ -871,23 +927,28 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
         uint32_t out_hi[2][8], out_lo[2][8];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const float shift = -((m[g] == -INFINITY ? 0.f : m[g]) + kShift);
-          const float2 shift2 = make_float2(shift, shift);
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float4 r = *reinterpret_cast<const float4*>(meta + 2 * kBlk + (j / 2) * 16 + quad * 4);
-            const float2 d01 = add2(y[g][j], shift2), d23 = add2(y[g][j + 1], shift2);
-            const float2 w01 = make_float2(fast_exp2(d01.x), fast_exp2(d01.y));
-            const float2 w23 = make_float2(fast_exp2(d23.x), fast_exp2(d23.y));
-            l[g] = fma2(w01, make_float2(r.x, r.y), l[g]);
-            l[g] = fma2(w23, make_float2(r.z, r.w), l[g]);
-            uint32_t hi, lo;                             // codes of slots 8j + 2 quad, + 1; + 8, + 9
-            split_e4m3x4(w01, w23, hi, lo);
-            // Lanes of a pair trade, the even one for four slots in a row at
-            // 8j, the odd one at 8j + 8.
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, __byte_perm(hi, lo, sel_send), 1);
-            out_hi[g][j / 2] = __byte_perm(hi, got, sel_hi);
-            out_lo[g][j / 2] = __byte_perm(lo, got, sel_lo);
+          for (int k = 0; k < 4; ++k) {
+            const float2 shift2 = make_float2(-u[g][k], -u[g][k]);
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 4 * k; j < 4 * k + 4; j += 2) {
+              const float4 r = *reinterpret_cast<const float4*>(meta + 2 * kBlk + (j / 2) * 16 + quad * 4);
+              const float2 d01 = add2(y[g][j], shift2), d23 = add2(y[g][j + 1], shift2);
+              const float2 w01 = make_float2(fast_exp2(d01.x), fast_exp2(d01.y));
+              const float2 w23 = make_float2(fast_exp2(d23.x), fast_exp2(d23.y));
+              sum = fma2(w01, make_float2(r.x, r.y), sum);
+              sum = fma2(w23, make_float2(r.z, r.w), sum);
+              uint32_t hi, lo;                           // codes of slots 8j + 2 quad, + 1; + 8, + 9
+              split_e4m3x4(w01, w23, hi, lo);
+              // Lanes of a pair trade, the even one for four slots in a row at
+              // 8j, the odd one at 8j + 8.
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, __byte_perm(hi, lo, sel_send), 1);
+              out_hi[g][j / 2] = __byte_perm(hi, got, sel_hi);
+              out_lo[g][j / 2] = __byte_perm(lo, got, sel_lo);
+            }
+            const float f = __uint_as_float(((unit_of[g] >> (8 * k)) & 0xffu) << 23);
+            l[g] = fma2(sum, make_float2(f, f), l[g]);
           }
         }
         wait_note();
@@ -901,8 +962,12 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
         // P and O are this thread's once the previous block's products are done.
         if (e > 0 && !done_with(e - 1)) bad = true;
         __syncwarp();
+        tc_fence_after();
+        {                                                // the heads' factors, in every lane quarter
+          const uint32_t f0 = note->units[lane], f1 = note->units[32 + lane];
+          tmem_st4u(tmem + lanes + L::kTmemFHi, f0, f1, f0 - kFineSteps, f1 - kFineSteps);
+        }
         if (raised[0] | raised[1]) {                     // O of these heads, rescaled
-          tc_fence_after();
           const uint32_t o = tmem + lanes + L::kTmemO;
           // A column at a time, few as they mostly are: a second form for many heads at
           // once cost every call 1 to 2 % by its size alone.
@@ -916,7 +981,6 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
 #pragma unroll
               for (int c = 0; c < L::kChunks; ++c) tmem_st1(o + c * kHeads + h, v[c] * f);
             }
-          tmem_wait_st();
         }
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
@@ -929,6 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + L::kPieceBytes), "r"(out_lo[g][j]) : "memory");
           }
         }
+        tmem_wait_st();
         tc_fence_before();
         fence_proxy_async_smem();
         __syncwarp();
@@ -1013,7 +1078,7 @@ __global__ void __launch_bounds__(D < 128 ? D : 128) smqa_paged_join_kernel(cons
 #pragma unroll
   for (int h = 0; h < kJoinHeads; ++h) {
     top[h] = h < heads ? __ldg(p.sink + h0 + hb + h) * 1.4426950408889634f : 0.f;
-    total[h] = top[h] == -INFINITY ? 0.f : 0.25f;        // in units of 2^kShift
+    total[h] = top[h] == -INFINITY ? 0.f : 1.f;
   }
   for (int c0 = cta;;) {
     const int c = c0 + lane * groups;
@@ -1084,7 +1149,7 @@ __global__ void __launch_bounds__(D < 128 ? D : 128) smqa_paged_join_kernel(cons
     const float inv = total[h] == 0.f ? 0.f : kCodeUnit / total[h];
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) p.o[row * D + k * 128 + threadIdx.x] = __float2bfloat16(o[k][h] * inv);
-    if (threadIdx.x == 0) p.lse[row] = total[h] == 0.f ? -INFINITY : log2f(total[h]) + kShift + top[h];
+    if (threadIdx.x == 0) p.lse[row] = total[h] == 0.f ? -INFINITY : log2f(total[h]) + top[h];
   }
 }
 
