@@ -297,7 +297,7 @@ struct QLoader {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int k = -1 - exponent(min(top_of(16 * quarter + 2 * i + sub), 0x7f7fu));
-        const float x = k > -127 ? pow2f(k) : 0x1p-128f;
+        const float x = k > -127 ? pow2f(k) : k == -127 ? 0x1p-127f : 0x1p-128f;  // (pow2f is of normal numbers)
         f[i] = make_float2(x, x);
       }
 #pragma unroll

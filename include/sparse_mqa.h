@@ -472,6 +472,7 @@ smqa_status smqa_paged_append(const void* kv_new, const int32_t* slot_mapping, i
  * j < seq_lens[req].  A position whose block-table entry is outside
  * [0, n_pages) is masked.  A token with nothing to attend to gets O = 0 and
  * lse = sink / ln 2.  A head whose q row holds a NaN or an infinity gets NaN.
+ * |q . codes| stays below 2^128.
  * kv_scales lie in [2^-60, 2^120].
  *   workspace    at least smqa_paged_fwd_workspace_bytes(shape) bytes, 256-byte
  *                aligned (NULL allowed when that is 0); needs no

@@ -1,0 +1,33 @@
+"""The attention over the 8-bit paged cache at the ends of its number range."""
+import pytest
+import torch
+
+from tests import _paged as ref
+from tests.test_gpu_paged_weights import attn64, call
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("power", [-101, -100, -99, 0, 124, 125, 126, 127])
+@pytest.mark.parametrize("D", [64, 512])
+def test_query_rows_up_to_the_largest(D, power):
+    """A row's largest value in [2^power, 2^(power + 1)), the softmax scale (or the pages') such
+    that the logits are moderate. q.c stays below 2^128: one element of q meets codes up to 1."""
+    page, n, H = 16, 200, 6
+    g = torch.Generator().manual_seed(D + power)
+    n_pages = -(-n // page)
+    big = power > 0
+    scale = torch.full((n_pages,), 2.0 ** (-60 if big else 100 if power < -50 else 0), dtype=torch.float64)
+    val = ref.e4m3(torch.randn(n_pages, page, D, generator=g).double().clamp(-2, 2) / 2)
+    sm = 2.0 ** -66 if big else 1.0
+    q = torch.zeros(H, D)
+    q[torch.arange(H), torch.arange(H) * 7 + 3] = 2.0 ** power * torch.tensor([1.0, 1.5, -1.984375, 1.0, -1.0, 1.25])
+    q = q.bfloat16()
+    q[5, 40] = q[5, 38] * 2.0 ** -9                        # (two pieces: the finer one counts)
+    sink, pos = torch.zeros(H), torch.arange(n)
+    table = torch.arange(n_pages, dtype=torch.int32)[None].contiguous()
+    got = call(q, val, scale, table, sink, n, sm=sm)
+    o, b, lse = attn64(q, val, scale, sink, pos // page, pos % page, sm)
+    over = (got[0].cpu().double() - o).abs() - b
+    assert float(over.max()) <= 0, f"o: {float(over.max()):.3e} beyond its bound"
+    assert float((got[1].cpu().double() - lse).abs().max()) <= 1e-4
