@@ -12,7 +12,7 @@
 // costs as much tensor time as one bf16 operand (e4m3 runs at twice the rate):
 //   q  = 2^-k (hi + lo / 32), k per row so that the largest value of 2^k q
 //        lies in [128, 256): bf16's 8 bits fit the two pieces exactly down to
-//        2^-22 of the row's largest value;
+//        2^-22 of the row's largest value (or of 2^-119);
 //   w  = 2^(y_j - u), y_j = x_j + log2 s_j: the weight that multiplies the
 //        codes, 2^8 w = hi + lo / 32.  u is an integer for each head and group of
 //        32 slots, the least at or above the group's largest y, so that its
@@ -287,8 +287,9 @@ struct QLoader {
     }
     bar_sync(4 + quarter, 64);
     auto top_of = [&](int h) { return max(head_top[h], head_top[kHeads + h]); };
-    // floor(log2) of the largest magnitude, not below -100.
-    auto exponent = [](uint32_t m) { return max(static_cast<int>(m >> 7) - 127, -100); };
+    // floor(log2) of the largest magnitude, not below -119 (whose 2^-k is the
+    // smallest normal number).
+    auto exponent = [](uint32_t m) { return max(static_cast<int>(m >> 7) - 127, -119); };
     const uint32_t stage = base + L::kOffP + static_cast<uint32_t>(4 * half + quarter) * L::kQStage;
     if (D >= 128 || half == 0) {
       // In fp16, scaled so that the row's largest value lies in [1/2, 1): exact

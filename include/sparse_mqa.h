@@ -480,7 +480,7 @@ smqa_status smqa_paged_append(const void* kv_new, const int32_t* slot_mapping, i
  *                share it
  *   flags        0 or SMQA_FLAG_ZERO_PADDING
  * The codes enter the tensor core as they are.  A q row is exact down to 2^-22
- * of its largest value.  A weight p_j s_j has a relative error of 2^-8 + 2^-11 at
+ * of its largest value, or of 2^-119.  A weight p_j s_j has a relative error of 2^-8 + 2^-11 at
  * most, down to 2^-14 of the largest of its group of 32 slots (32 i to 32 i + 31
  * of the list, or of the positions), and one of 2^-22 of that largest below: O's
  * error does not grow with the number of slots, however much of the weight one

@@ -31,3 +31,26 @@ def test_query_rows_up_to_the_largest(D, power):
     over = (got[0].cpu().double() - o).abs() - b
     assert float(over.max()) <= 0, f"o: {float(over.max()):.3e} beyond its bound"
     assert float((got[1].cpu().double() - lse).abs().max()) <= 1e-4
+
+
+@pytest.mark.parametrize("power", [-104, -110, -115, -119, -120, -124])
+@pytest.mark.parametrize("D", [64, 512])
+def test_query_rows_down_to_the_smallest(D, power):
+    """Rows of q that are as small as bf16's normal numbers, over pages of scales up to 2^120: q's
+    pieces hold a row down to 2^-22 of its largest value, or of 2^-119."""
+    page, n, H = 16, 200, 6
+    g = torch.Generator().manual_seed(D - power)
+    n_pages = -(-n // page)
+    scale = torch.full((n_pages,), 2.0 ** min(-power, 120), dtype=torch.float64)
+    val = ref.e4m3(torch.randn(n_pages, page, D, generator=g).double().clamp(-3, 3) * 16)
+    q = (torch.randn(H, D, generator=g).clamp(-2, 2) / 2 * 2.0 ** power).bfloat16()
+    q[0] = 0
+    sink, pos = torch.zeros(H), torch.arange(n)
+    table = torch.arange(n_pages, dtype=torch.int32)[None].contiguous()
+    got = call(q, val, scale, table, sink, n, sm=1.0 / 64)
+    o, b, lse = attn64(q, val, scale, sink, pos // page, pos % page, 1.0 / 64)
+    # q's own floor, 2^-22 of 2^-119, in the logits and so in the weights and l
+    low = (2.0 ** -141 * (val * scale[:, None, None]).abs().sum(2).max() / 64).item()
+    over = (got[0].cpu().double() - o).abs() - b - 2 * low * (val * scale[:, None, None]).abs().max()
+    assert float(over.max()) <= 0, f"o: {float(over.max()):.3e} beyond its bound"
+    assert float((got[1].cpu().double() - lse).abs().max()) <= 1e-4 + 2 * low
