@@ -473,7 +473,9 @@ smqa_status smqa_paged_append(const void* kv_new, const int32_t* slot_mapping, i
  * [0, n_pages) is masked.  A token with nothing to attend to gets O = 0 and
  * lse = sink / ln 2.  A head whose q row holds a NaN or an infinity gets NaN.
  * |q . codes| stays below 2^128.
- * kv_scales lie in [2^-60, 2^120].
+ * kv_scales lie in [2^-60, 2^120], those of the pages that one token reads no
+ * more than 2^100 apart: a slot whose p_j s_j is below 2^-126 of the largest of
+ * its group (below) does not count in l, which is then off by 2^-21 at most.
  *   workspace    at least smqa_paged_fwd_workspace_bytes(shape) bytes, 256-byte
  *                aligned (NULL allowed when that is 0); needs no
  *                initialisation; calls whose kernels may overlap must not

@@ -1,4 +1,6 @@
 """The attention over the 8-bit paged cache at the ends of its number range."""
+import math
+
 import pytest
 import torch
 
@@ -54,3 +56,30 @@ def test_query_rows_down_to_the_smallest(D, power):
     over = (got[0].cpu().double() - o).abs() - b - 2 * low * (val * scale[:, None, None]).abs().max()
     assert float(over.max()) <= 0, f"o: {float(over.max()):.3e} beyond its bound"
     assert float((got[1].cpu().double() - lse).abs().max()) <= 1e-4 + 2 * low
+
+
+@pytest.mark.parametrize("low,high", [(-60, 40), (-60, 0), (20, 120), (-30, 70)])
+@pytest.mark.parametrize("page", [16, 64])
+def test_page_scales_as_far_apart_as_stated(low, high, page):
+    """Pages of all zeros, or nearly, beside pages 2^100 above them whose rows are orthogonal to
+    q: every position counts in l."""
+    D, H, n_pages = 64, 16, 12
+    g = torch.Generator().manual_seed(page + high)
+    n = n_pages * page
+    val = ref.e4m3(torch.randn(n_pages, page, D, generator=g).double().clamp(-3, 3) * 64)
+    val[:, :, ::2] = 0
+    scale = torch.where(torch.arange(n_pages) % 2 == 0, 2.0 ** low, 2.0 ** high).double()
+    val[0] = 0
+    q = torch.randn(H, D, generator=g)
+    q[:, 1::2] = 0
+    q = q.bfloat16()
+    sink, pos = torch.full((H,), 3.0), torch.arange(n)
+    table = torch.arange(n_pages, dtype=torch.int32)[None].contiguous()
+    for idx in (None, torch.randperm(n, generator=g)):
+        at = pos if idx is None else idx
+        got = call(q, val, scale, table, sink, n, idx)
+        o, b, lse = attn64(q, val, scale, sink, at // page, at % page, D ** -0.5)
+        assert torch.allclose(lse, torch.full((H,), math.log2(n + math.exp(3.0))).double())
+        # lse: sums of n terms, and top = log2 of the largest scale at most, in fp32
+        assert float((got[1].cpu().double() - lse).abs().max()) <= 2.0 ** -14
+        assert float(((got[0].cpu().double() - o).abs() - b).max()) <= 0
