@@ -40,8 +40,6 @@ class PagedPlan(NamedTuple):
 # call's kernel may take less time than Python needs to check its arguments:
 # the checks of a call are one expression, explained tensor by tensor only when
 # it fails, and the stream and device are read without building objects.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
 _LIM = 2 ** 31                                           # (the C ABI takes sizes as int32)
 _I32, _BF16, _F32, _E4M3 = torch.int32, torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
@@ -59,11 +57,12 @@ def _explain(why: str, *tensors: tuple) -> None:
 
 def _call(fn: str, device: int, f, *args) -> None:
     """f(*args, current stream of ``device``) with that device current."""
-    if _current_device() == device:
-        st = f(*args, _raw_stream(device))
+    c = torch._C                                         # (looked up here: a torch without CUDA lacks them)
+    if c._cuda_getDevice() == device:
+        st = f(*args, c._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
-            st = f(*args, _raw_stream(device))
+            st = f(*args, c._cuda_getCurrentRawStream(device))
     if st != _lib.SMQA_OK:
         _lib.check(fn, st)
 
