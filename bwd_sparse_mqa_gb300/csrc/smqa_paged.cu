@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kPlanThreads) smqa_paged_plan_kernel(const Pla
       const int r = static_cast<int>(e / p.W), col = static_cast<int>(e - static_cast<int64_t>(r) * p.W);
       const int64_t c = max(p.ctx[r], 0), q = max(p.qry[r], 0);
       const int64_t have = (c + page - 1) >> p.page_shift, full = (c + q + page - 1) >> p.page_shift;
-      p.table_out[e] = (col >= have && col < full) ? stack(s_pg[r] + col - have) : p.table[e];
+      p.table_out[e] = (col >= have && col < full) ? stack(static_cast<int64_t>(s_pg[r]) + col - have) : p.table[e];
     }
   } else {
     for (int r = gid >> 5; r < p.R; r += gthreads >> 5) {

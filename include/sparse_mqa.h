@@ -407,7 +407,8 @@ typedef struct {
  *                            pages); rows from the total on are -1 in all
  *                            three.  Tokens past max_tokens are left out.
  * Negative lengths and a negative free_count count as 0.  R <= 16384,
- * n_pages * page_size < 2^31, context + query < 2^31.  One launch.
+ * n_pages * page_size < 2^31, context + query < 2^31; sums over the requests
+ * (cu_query, the pages needed) stop at 2^31 - 1.  One launch.
  */
 smqa_status smqa_paged_plan(const int32_t* context_lens, const int32_t* query_lens,
                             const int32_t* block_table, const int32_t* free_pages,

@@ -1,0 +1,34 @@
+"""The paged-cache operators at sizes where 32-bit sums and roundings end."""
+import pytest
+import torch
+
+from bwd_sparse_mqa_gb300 import paged_plan
+
+pytestmark = pytest.mark.gpu
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _room(gib):
+    if torch.cuda.mem_get_info()[0] < gib << 30:
+        pytest.skip(f"needs {gib} GiB of device memory")
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+def test_plan_of_more_pages_than_an_int(inplace):
+    """All requests together need more than 2^31 pages: the stack's few go to the first request,
+    every other entry is -1, and the count ends at the most negative one it can."""
+    _room(32)
+    R, W, page = 16384, 131073, 16
+    table = torch.full((R, W), 7, dtype=torch.int32, device="cuda")
+    got = paged_plan(torch.zeros(R, dtype=torch.int32, device="cuda"),
+                     torch.full((R,), W * page, dtype=torch.int32, device="cuda"), table, _i32([11, 12, 13, 14, 15]),
+                     _i32([5]), page, 40, 100, inplace=inplace)
+    assert got.block_table[0, :6].tolist() == [15, 14, 13, 12, 11, -1]
+    got.block_table[0, :5] = -1
+    assert all(int(part.max()) == int(part.min()) == -1 for part in got.block_table.split(1024))
+    assert int(got.free_count) == 5 - (2 ** 31 - 1)
+    assert got.token_req.tolist() == [0] * 40 and got.slot_mapping.tolist() == [15 * 16 + i for i in range(16)] + \
+        [14 * 16 + i for i in range(16)] + [13 * 16 + i for i in range(8)]
