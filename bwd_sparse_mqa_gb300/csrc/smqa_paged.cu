@@ -165,32 +165,32 @@ __global__ void __launch_bounds__(1024)
     smqa_paged_release_kernel(int32_t* table, int32_t* seq, const uint8_t* release, int R, int W,
                               int n_pages, int32_t* free_pages, int32_t* free_count, int pool) {
   __shared__ int32_t cnt[32];
-  __shared__ int32_t base;
+  __shared__ int64_t base;                               // (pages counted, fitting or not)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) base = min(max(*free_count, 0), pool);
   __syncthreads();
-  for (int r0 = 0; r0 < R; r0 += 32) {
-    const int r = r0 + warp;
+  for (int64_t r0 = 0; r0 < R; r0 += 32) {
+    const int64_t r = r0 + warp;
     const bool mine = r < R && release[r] != 0;
-    int32_t* row = table + static_cast<int64_t>(r) * W;
+    int32_t* row = table + r * W;
     int n = 0;
     if (mine)
-      for (int c0 = 0; c0 < W; c0 += 32) {
+      for (int64_t c0 = 0; c0 < W; c0 += 32) {
         const int pg = c0 + lane < W ? row[c0 + lane] : -1;
         n += __popc(__ballot_sync(0xffffffffu,
                                   static_cast<unsigned>(pg) < static_cast<unsigned>(n_pages)));
       }
     if (lane == 0) cnt[warp] = n;
     __syncthreads();
-    int at = base;
+    int64_t at = base;
     for (int w = 0; w < warp; ++w) at += cnt[w];
     if (mine) {
-      for (int c0 = 0; c0 < W; c0 += 32) {
+      for (int64_t c0 = 0; c0 < W; c0 += 32) {
         const bool in = c0 + lane < W;
         const int pg = in ? row[c0 + lane] : -1;
         const bool ok = static_cast<unsigned>(pg) < static_cast<unsigned>(n_pages);
         const unsigned m = __ballot_sync(0xffffffffu, ok);
-        const int k = at + __popc(m & ((1u << lane) - 1));
+        const int64_t k = at + __popc(m & ((1u << lane) - 1));
         if (ok && k < pool) free_pages[k] = pg;
         if (in) row[c0 + lane] = -1;
         at += __popc(m);
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(1024)
       for (int w = 0; w < 32; ++w) base += cnt[w];
     __syncthreads();
   }
-  if (threadIdx.x == 0) *free_count = min(base, pool);
+  if (threadIdx.x == 0) *free_count = static_cast<int>(min(base, static_cast<int64_t>(pool)));
 }
 
 // ---------------------------------------------------------------------------

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from bwd_sparse_mqa_gb300 import paged_plan
+from bwd_sparse_mqa_gb300 import paged_plan, paged_release
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +32,16 @@ def test_plan_of_more_pages_than_an_int(inplace):
     assert int(got.free_count) == 5 - (2 ** 31 - 1)
     assert got.token_req.tolist() == [0] * 40 and got.slot_mapping.tolist() == [15 * 16 + i for i in range(16)] + \
         [14 * 16 + i for i in range(16)] + [13 * 16 + i for i in range(8)]
+
+
+def test_release_onto_a_full_stack_as_long_as_an_int():
+    """A stack of 2^31 - 1 entries with room for three: the rest is dropped, nothing is written
+    outside of the stack, and the count ends at its length."""
+    _room(24)
+    pool = 2 ** 31 - 1
+    free = torch.full((pool,), -5, dtype=torch.int32, device="cuda")
+    table = torch.arange(100, dtype=torch.int32, device="cuda").view(2, 50).contiguous()
+    count, gone = _i32([pool - 3]), torch.tensor([True, True], device="cuda")
+    paged_release(table, gone, free, count, 100)
+    assert int(count) == pool and free[-3:].tolist() == [0, 1, 2]
+    assert int(free[:-3].max()) == int(free[:-3].min()) == -5 and int(table.max()) == -1
