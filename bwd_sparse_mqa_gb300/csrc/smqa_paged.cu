@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kPlanThreads) smqa_paged_plan_kernel(const Pla
   };
   // Tokens.  (Before the barrier of the in-place form: they read ctx.)
   const int total = s_cu[p.R];
-  for (int t = gid; t < p.N; t += gthreads) {
+  for (int64_t i = gid; i < p.N; i += gthreads) {
+    const int t = static_cast<int>(i);
     int r = -1, ps = -1, sl = -1;
     if (t < total) {
       int lo = 0, hi = p.R;  // the last r with s_cu[r] <= t (it has tokens)

@@ -45,3 +45,16 @@ def test_release_onto_a_full_stack_as_long_as_an_int():
     paged_release(table, gone, free, count, 100)
     assert int(count) == pool and free[-3:].tolist() == [0, 1, 2]
     assert int(free[:-3].max()) == int(free[:-3].min()) == -5 and int(table.max()) == -1
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+def test_plan_of_as_many_token_rows_as_an_int(inplace):
+    """max_tokens up to 2^31 - 1: every row behind the tokens is -1, and nothing else is written."""
+    _room(64)
+    N = 2 ** 31 - 1
+    plan = paged_plan(_i32([3, 0]), _i32([2, 1]), _i32([[4], [-1]]), _i32([6]), _i32([1]), 16, N, 9, inplace=inplace)
+    assert plan.token_req[:4].tolist() == [0, 0, 1, -1] and plan.positions[:4].tolist() == [3, 4, 0, -1]
+    assert plan.slot_mapping[:4].tolist() == [67, 68, 96, -1]
+    for t in (plan.token_req, plan.positions, plan.slot_mapping):
+        assert t.numel() == N and int(t[3:].max()) == int(t[3:].min()) == -1
+    assert plan.seq_lens.tolist() == [5, 1] and plan.cu_query.tolist() == [0, 2, 3]
