@@ -378,6 +378,8 @@ smqa_status refuse(smqa_status st, const char* why) {
 }
 
 constexpr int64_t kLim = int64_t{1} << 31;
+// Slots of a token: the attention rounds them up to blocks of 128 in 32 bits.
+constexpr int64_t kMaxSlots = kLim - 128;
 
 smqa_status check_paged(const smqa_paged_shape& s) {
   if (s.T < 0 || s.R <= 0 || s.H <= 0 || s.D <= 0 || s.topk < 0 || s.page_size <= 0 ||
@@ -385,11 +387,11 @@ smqa_status check_paged(const smqa_paged_shape& s) {
     return refuse(SMQA_ERR_INVALID_ARG, "non-positive size in paged shape");
   if (s.H > 128 || (s.D != 64 && s.D != 512) || page_shift_of(s.page_size) < 0 ||
       static_cast<int64_t>(s.n_pages) * s.page_size >= kLim ||
-      static_cast<int64_t>(s.max_pages) * s.page_size >= kLim ||
+      static_cast<int64_t>(s.max_pages) * s.page_size > kMaxSlots || s.topk > kMaxSlots ||
       static_cast<int64_t>(s.T) * std::max(s.H, s.topk) >= kLim)
     return refuse(SMQA_ERR_UNSUPPORTED,
                   "unsupported paged shape (need 1<=H<=128, D in {64,512}, page_size in "
-                  "{16,32,64,128}, sizes < 2^31)");
+                  "{16,32,64,128}, topk and max_pages * page_size <= 2^31 - 128, sizes < 2^31)");
   return SMQA_OK;
 }
 

@@ -490,7 +490,7 @@ smqa_status smqa_paged_append(const void* kv_new, const int32_t* slot_mapping, i
  * of them holds.  S, O, the maxima and l are held in fp32, O is rounded to bf16
  * once.
  * 1 <= H <= 128, D in {64, 512}, n_pages * page_size < 2^31,
- * T * max(H, topk) < 2^31.
+ * T * max(H, topk) < 2^31, topk and max_pages * page_size <= 2^31 - 128.
  */
 size_t smqa_paged_fwd_workspace_bytes(smqa_paged_shape shape);
 smqa_status smqa_paged_fwd(const void* q, const void* kv_cache, const float* kv_scales,
