@@ -1203,16 +1203,19 @@ template <int D>
 cudaError_t launch(const PagedFwdParams& p, int ctas, cudaStream_t stream) {
   using L = PagedLayout<D>;
   // A split of registers above what the block is launched with would wait for
-  // ever: refuse to launch a kernel that was not built with 128 a thread.
-  static const cudaError_t built = [] {
+  // ever: refuse to launch a kernel that was not built with 128 a thread.  (Asked
+  // until it has been answered.)
+  static std::atomic<bool> built{false};
+  cudaError_t e;
+  if (!built.load(std::memory_order_relaxed)) {
     cudaFuncAttributes a;
-    const cudaError_t e = cudaFuncGetAttributes(&a, smqa_paged_fwd_kernel<D>);
+    e = cudaFuncGetAttributes(&a, smqa_paged_fwd_kernel<D>);
     if (e != cudaSuccess) return e;
-    return a.numRegs * kThreads >= 2 * 128 * (kSoftmaxRegs + kOtherRegs) ? cudaSuccess : cudaErrorInvalidConfiguration;
-  }();
-  if (built != cudaSuccess) return built;
+    if (a.numRegs * kThreads < 2 * 128 * (kSoftmaxRegs + kOtherRegs)) return cudaErrorInvalidConfiguration;
+    built.store(true, std::memory_order_relaxed);
+  }
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(smqa_paged_fwd_kernel<D>), L::kSmem, allowed);
+  e = allow_smem(reinterpret_cast<const void*>(smqa_paged_fwd_kernel<D>), L::kSmem, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

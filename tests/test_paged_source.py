@@ -20,3 +20,10 @@ def test_no_loads_through_the_read_only_path(name):
     __ldg and ld.global.nc are defined only for data that nothing writes while the kernel lives."""
     code = _code(name)
     assert "__ldg" not in code and ".nc." not in code and "__restrict__" not in code
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_no_error_is_kept_between_calls(name):
+    """A call that failed once (no memory, a busy device) must not decide the next: statics hold
+    what succeeded, never an error code."""
+    assert not re.search(r"static\s+(const\s+)?cudaError_t\s+\w+\s*(=|\{)", _code(name))
