@@ -1180,16 +1180,23 @@ int64_t blocks_per_token(const smqa_paged_shape& s) {
   return (slots + kBlk - 1) / kBlk;
 }
 // Whether ranges are whole tokens (index lists: all tokens have the same number
-// of blocks).  Splitting tokens evens the ranges out but costs a read-out and a Q
-// more per range, the parts' way through the workspace and the joining kernel,
-// together about as long as twelve blocks take (topk=2048, 16 blocks: 100 tokens
-// of 128 heads on 76 ranges 80 us whole (32 blocks at most per range), 87 split
-// (22); 160 tokens of 64 heads on 152 ranges 80 us whole (32), 76 split (17)).
+// of blocks).  Splitting tokens evens the ranges out but costs the joining kernel,
+// two blocks' time for a lone token, and a read-out and a Q more for the ranges
+// that hold parts of two tokens, the more the nearer the tokens are to the ranges
+// in number: up to 12 blocks' time (D = 64: 7).  GPU times, whole and split, in us:
+//   T=1   H=128 D=512: topk=256 12.4 15.3, 512 16.2 15.9, 1024 22.8 16.7, 1536 29.5 17.4
+//   T=8   H=128 D=512: topk=512 16.3 18.5, 1024 22.8 22.1, 1536 29.7 24.3
+//   T=32  H=128 D=512: topk=1024 23.2 32.2, 1536 30.1 36.1, 2048 37.0 40.6
+//   T=32  H=64  D=512: topk=1024 22.9 23.7, 1536 29.7 25.5
+//   T=32  H=128 D=64:  topk=1024 17.1 19.5, 1536 22.6 22.1, 2048 28.2 24.9
+//   T=100 H=128 D=512: topk=1024 44.6 55.1, 2048 73.5 75.2
+//   T=128 H=128 D=64:  topk=2048 54.0 56.4, 4096 98.7 93.8
 bool whole_tokens(const smqa_paged_shape& s) {
   if (s.topk == 0) return blocks_per_token(s) <= 1;
   const int groups = (s.H + kHeads - 1) / kHeads;
-  const int64_t parts = 152 / groups, nb = blocks_per_token(s);
-  return (s.T + parts - 1) / parts * nb <= s.T * nb / parts + 12;
+  const int64_t parts = 152 / groups, T = s.T, nb = blocks_per_token(s);
+  const int64_t spare = std::min<int64_t>(2 + 24 * T / parts, s.D == 512 ? 12 : 7);
+  return (T + parts - 1) / parts * nb <= std::max<int64_t>(T * nb / parts, 1) + spare;
 }
 // CTAs of a call: per head group, as many ranges as SMs (or as the tokens can
 // have blocks).
