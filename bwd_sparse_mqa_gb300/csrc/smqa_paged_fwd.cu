@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
           if (whole) {
             const float top = fmaxf(m_end, sink);
             float inv, lse;
-            if (top == -INFINITY) {                        // nothing at all (or only NaN)
+            if (top == -INFINITY && sink == -INFINITY) {   // nothing at all (or only NaN)
               inv = l_end * 0.f;
               lse = l_end != l_end ? l_end : -INFINITY;
             } else {

@@ -4,6 +4,7 @@ import math
 import pytest
 import torch
 
+from bwd_sparse_mqa_gb300 import sparse_mqa_paged_fwd
 from tests import _paged as ref
 from tests.test_gpu_paged_weights import attn64, call
 
@@ -83,3 +84,29 @@ def test_page_scales_as_far_apart_as_stated(low, high, page):
         # lse: sums of n terms, and top = log2 of the largest scale at most, in fp32
         assert float((got[1].cpu().double() - lse).abs().max()) <= 2.0 ** -14
         assert float(((got[0].cpu().double() - o).abs() - b).max()) <= 0
+
+
+@pytest.mark.parametrize("topk", [0, 100, 8000])
+def test_a_nan_sink_reaches_its_head(topk):
+    """A NaN sink makes its head's O and LSE NaN, in tokens that attend to something, to nothing,
+    whole or split, and leaves the other heads alone."""
+    D, page, n = 64, 16, 9000 if topk != 100 else 60
+    cache, scale = ref.fill_cache(-(-n // page), page, D, 3)
+    table = torch.arange(cache.shape[0], dtype=torch.int32)[None].contiguous()
+    g = torch.Generator().manual_seed(topk)
+    q = torch.randn(2, 3, D, generator=g).bfloat16()
+    sink = torch.tensor([0.5, math.nan, -math.inf])
+    pos = torch.tensor([n - 1, -1], dtype=torch.int32)
+    idx = None
+    if topk:
+        idx = torch.full((2, topk), -1, dtype=torch.int32)
+        idx[0, :min(topk, n)] = torch.randperm(n, generator=g)[:min(topk, n)].int()
+    got = sparse_mqa_paged_fwd(q.cuda(), cache.cuda(), scale.cuda(), sink.cuda(), table.cuda(),
+                               torch.tensor([n], dtype=torch.int32, device="cuda"),
+                               torch.zeros(2, dtype=torch.int32, device="cuda"), pos.cuda(),
+                               None if idx is None else idx.cuda(), check_status=True)
+    want = ref.attn(q, ref.codes(cache), scale.double(), torch.where(sink.isnan(), 0.0, sink), table, [n], [0, 0],
+                    pos.tolist(), idx)
+    for w in want:
+        w[:, 1] = math.nan
+    ref.check_attn(got, want)
