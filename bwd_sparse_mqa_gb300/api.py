@@ -75,8 +75,9 @@ def _scale(sm_scale: Optional[float], D: int) -> float:
     if sm_scale is None:
         return 1.0 / math.sqrt(D)
     s = float(sm_scale)
-    if not s > 0.0 or not math.isfinite(s):
-        raise ValueError("sm_scale must be a positive finite float or None")
+    f = ctypes.c_float(s).value  # (what the C ABI gets: of that, 0 and infinity select D^-1/2)
+    if not f > 0.0 or not math.isfinite(f):
+        raise ValueError("sm_scale must be positive and finite as a 32-bit float, or None")
     return s
 
 
