@@ -126,6 +126,9 @@ inline size_t det_stats_offset(const smqa_shape& s) {
   return (elems * 8 + 255) & ~static_cast<size_t>(255);
 }
 
+// SMs of a GB300: the paged cache's grids are made for one CTA on each.
+constexpr int kSMs = 152;
+
 // Attention over the 8-bit paged cache (smqa_paged_fwd).
 struct PagedFwdParams {
   const __nv_bfloat16* q;    // [T,H,D]

@@ -224,7 +224,7 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 // left to the whole CTA.  A run's rows are one flat range in kv_new and in the
 // cache, read twice, the second time from L1.  Bound by latency: 8192 rows
 // (D=512, pages of 64: 130 runs) took 11.9 us with a CTA per row, most of which
-// left at once, and take 7.0 us so; 128 single rows 2.5 us.
+// left // left at once, and take 7.2 us so; 128 single rows 2.6 us.
 constexpr int kAppendWarps = 16, kAppendThreads = 32 * kAppendWarps;
 constexpr int kShortRun = 8;                             // rows (512 runs of 6: 4.4 us by warps, 6.1 by CTAs)
 
@@ -459,7 +459,7 @@ smqa_status smqa_paged_plan(const int32_t* context_lens, const int32_t* query_le
   } else {
     const int64_t work = std::max<int64_t>(static_cast<int64_t>(R) * max_pages, max_tokens);
     cfg.gridDim = dim3(static_cast<unsigned>(
-        std::min<int64_t>(152, std::max<int64_t>(1, (work + kPlanThreads - 1) / kPlanThreads))));
+        std::min<int64_t>(kSMs, std::max<int64_t>(1, (work + kPlanThreads - 1) / kPlanThreads))));
   }
   e = cudaLaunchKernelEx(&cfg, kern, p);
   if (e != cudaSuccess) return cuda_failure(e, "paged plan launch");

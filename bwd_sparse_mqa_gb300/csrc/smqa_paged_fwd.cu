@@ -1062,7 +1062,9 @@ __global__ void __launch_bounds__(kThreads, 1) smqa_paged_fwd_kernel(const Paged
 // is one trip to L2, m, l and the first kAhead parts of O together the second.
 // Small blocks with many loads each: with four times larger ones, each warp with
 // all the reductions for a quarter of the columns, a call whose 152 CTAs all leave
-// parts took 16 us longer.  It adds 6 us to a lone token's 14.
+// parts took 16 us longer.  It adds 5.6 us to a lone token's 12 (H=128 D=512
+// topk=2048), 10 to 93 where all 152 CTAs leave parts (16 dense tokens of up to
+// 32768 positions).
 constexpr int kJoinHeads = 4;
 
 template <int D, int kAhead>
@@ -1194,7 +1196,7 @@ int64_t blocks_per_token(const smqa_paged_shape& s) {
 bool whole_tokens(const smqa_paged_shape& s) {
   if (s.topk == 0) return blocks_per_token(s) <= 1;
   const int groups = (s.H + kHeads - 1) / kHeads;
-  const int64_t parts = 152 / groups, T = s.T, nb = blocks_per_token(s);
+  const int64_t parts = kSMs / groups, T = s.T, nb = blocks_per_token(s);
   const int64_t spare = std::min<int64_t>(2 + 24 * T / parts, s.D == 512 ? 12 : 7);
   return (T + parts - 1) / parts * nb <= std::max<int64_t>(T * nb / parts, 1) + spare;
 }
@@ -1203,7 +1205,7 @@ bool whole_tokens(const smqa_paged_shape& s) {
 int ranges_of(const smqa_paged_shape& s) {
   const int groups = (s.H + kHeads - 1) / kHeads;
   const int64_t most = whole_tokens(s) ? s.T : s.T * blocks_per_token(s);
-  return static_cast<int>(std::min<int64_t>(152 / groups, std::max<int64_t>(most, 1)));
+  return static_cast<int>(std::min<int64_t>(kSMs / groups, std::max<int64_t>(most, 1)));
 }
 
 template <int D>
@@ -1236,7 +1238,11 @@ cudaError_t launch(const PagedFwdParams& p, int ctas, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, smqa_paged_fwd_kernel<D>, p);
   if (e != cudaSuccess || p.whole_tokens) return e;  // nothing to join
-  const bool few = ctas <= 64;                           // then with many parts each
+  // How many parts a thread asks for at once: a lone token's are many (32: 8 ahead
+  // 19.4 us, 2 ahead 22.3, H=64 topk=4096; 16: 17.3 and 18.5); where all CTAs leave
+  // parts a token has few, and more blocks fit an SM with fewer registers each (8
+  // tokens of topk=1024, 128 CTAs: 24.7 and 23.0 us; 16 dense ones, 152: 105.6, 102.4).
+  const bool few = ctas <= 64;
   cfg.gridDim = dim3(static_cast<unsigned>(ctas) * (kHeads / kJoinHeads));
   cfg.blockDim = dim3(D < 128 ? D : 128);
   cfg.dynamicSmemBytes = 0;
@@ -1247,7 +1253,7 @@ cudaError_t launch(const PagedFwdParams& p, int ctas, cudaStream_t stream) {
 
 size_t paged_fwd_workspace(const smqa_paged_shape& s) {
   const int groups = (s.H + kHeads - 1) / kHeads;
-  static_assert(152 <= kMaxCtas, "a leftover per CTA");
+  static_assert(kSMs <= kMaxCtas, "a leftover per CTA");
   if (whole_tokens(s)) return 0;
   return kLeftoverBytes + static_cast<size_t>(ranges_of(s)) * groups * 2 * part_floats(s.D) * sizeof(float);
 }
