@@ -45,9 +45,8 @@ __global__ void __launch_bounds__(kPlanThreads) smqa_paged_plan_kernel(const Pla
   const int page = 1 << p.page_shift;
   if (tid == 0) carry[0] = carry[1] = 0;
   __syncthreads();
-  // (Launched beside the kernel before, whose results are read from here on, by
-  // plain loads: the read-only path is for data that nothing writes while this
-  // kernel lives.  The next one may be launched beside this.)
+  // (Launched beside the kernel before, whose results are read from here on; the
+  // next one may be launched beside this.)
   grid_dependency_wait();
   grid_dependents_launch();
   for (int r0 = 0; r0 < p.R; r0 += kPlanThreads) {
@@ -100,7 +99,7 @@ __global__ void __launch_bounds__(kPlanThreads) smqa_paged_plan_kernel(const Pla
   const int gid = blockIdx.x * kPlanThreads + tid;
   auto stack = [&](int64_t nth) {  // the nth page taken in this step
     const int64_t at = count - 1 - nth;
-    return at >= 0 ? p.free_pages[at] : -1;
+    return at >= 0 ? load(p.free_pages + at) : -1;
   };
   // Tokens.  (Before the barrier of the in-place form: they read ctx.)
   const int total = s_cu[p.R];
@@ -224,7 +223,7 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 // left to the whole CTA.  A run's rows are one flat range in kv_new and in the
 // cache, read twice, the second time from L1.  Bound by latency: 8192 rows
 // (D=512, pages of 64: 130 runs) took 11.9 us with a CTA per row, most of which
-// left // left at once, and take 7.2 us so; 128 single rows 2.6 us.
+// left // left at once, and take 7.0 us so; 128 single rows 2.5 us.
 constexpr int kAppendWarps = 16, kAppendThreads = 32 * kAppendWarps;
 constexpr int kShortRun = 8;                             // rows (512 runs of 6: 4.4 us by warps, 6.1 by CTAs)
 
@@ -234,7 +233,7 @@ __device__ __forceinline__ uint32_t largest(const uint4* src, int i, int step, i
   uint32_t top = 0;
 #pragma unroll 8
   for (; i < n; i += step) {
-    const uint4 v = src[i];
+    const uint4 v = load(src + i);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -253,16 +252,10 @@ __device__ __forceinline__ void encode(const uint4* src, uint2* dst, int i, int 
     hi = ((w >> 16) & 0x7fffu) >= 0x7f80u ? __uint_as_float(0x7fffffffu) : hi * inv;
     return static_cast<uint32_t>(e4m3x2(lo, hi));
   };
-  constexpr int kBatch = 8;                              // loads before the first store
-  for (; i < n; i += kBatch * step) {
-    uint4 v[kBatch];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-      if (i + b * step < n) v[b] = src[i + b * step];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-      if (i + b * step < n)
-        dst[i + b * step] = make_uint2(code(v[b].x) | (code(v[b].y) << 16), code(v[b].z) | (code(v[b].w) << 16));
+#pragma unroll 8
+  for (; i < n; i += step) {
+    const uint4 v = load(src + i);
+    dst[i] = make_uint2(code(v.x) | (code(v.y) << 16), code(v.z) | (code(v.w) << 16));
   }
 }
 // Codes times f = 2^-k.
@@ -298,12 +291,12 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
     // The slots of the row before, of the warp's row and of those behind it that
     // can be in its page.
     const int t = blockIdx.x * kAppendWarps + warp;
-    const int before = t > 0 && t <= T ? slots[t - 1] : -2;
+    const int before = t > 0 && t <= T ? load(slots + t - 1) : -2;
     int x[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int i = 32 * k + lane;
-      x[k] = i < page && i < T - t ? slots[t + i] : -2;
+      x[k] = i < page && i < T - t ? load(slots + t + i) : -2;
     }
     const int s0 = __shfl_sync(0xffffffffu, x[0], 0);
     const int off = s0 & (page - 1);
@@ -346,7 +339,7 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
             grown_by[i]);
   }
   for (int i = 0; i < n_runs; ++i) {
-    const int t = run_at[i], s0 = slots[t], off = s0 & (page - 1);
+    const int t = run_at[i], s0 = load(slots + t), off = s0 & (page - 1);
     const int64_t pg = s0 >> page_shift;
     const float had = off ? scales[pg] : 0.f;            // (written behind a barrier)
     const int n = run_rows[i] * D / 8;

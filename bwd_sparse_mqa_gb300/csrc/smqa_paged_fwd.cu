@@ -79,26 +79,6 @@ namespace smqa {
 
 namespace {
 
-// Loads of what the kernel before may have written: through L1, but not by its
-// read-only path, which is for data that nothing writes while this kernel lives.
-// (As PTX: the compiler's own plain loads made 1024 tokens take 509 us, not 500, and
-// loads past L1 111 dense ones 26.4, not 23.5.)
-__device__ __forceinline__ int load(const int* p) {
-  int v;
-  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ float load(const float* p) {
-  float v;
-  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint2 load(const uint2* p) {
-  uint2 v;
-  asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
-
 constexpr int kBlk = 128;                 // slots per block
 constexpr int kHeads = 64;                // heads per CTA
 constexpr int kThreads = 512;
