@@ -223,7 +223,7 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 // left to the whole CTA.  A run's rows are one flat range in kv_new and in the
 // cache, read twice, the second time from L1.  Bound by latency: 8192 rows
 // (D=512, pages of 64: 130 runs) took 11.9 us with a CTA per row, most of which
-// left // left at once, and take 7.0 us so; 128 single rows 2.5 us.
+// left at once, and take 7.0 us so; 128 single rows 2.5 us.
 constexpr int kAppendWarps = 16, kAppendThreads = 32 * kAppendWarps;
 constexpr int kShortRun = 8;                             // rows (512 runs of 6: 4.4 us by warps, 6.1 by CTAs)
 
