@@ -35,6 +35,7 @@ EXPORTS = [
     "smqa_fwd_bwd_host", "smqa_host_chunk_plan", "smqa_set_wait_limit_ns", "smqa_debug_stall",
     "smqa_indexer_bwd", "smqa_batched_indexer_bwd", "smqa_paged_plan", "smqa_paged_release",
     "smqa_paged_append", "smqa_paged_fwd_workspace_bytes", "smqa_paged_fwd",
+    "smqa_paged_append_rope",
 ]
 STATIC_SCRATCH_BYTES = 64 << 20
 
@@ -103,6 +104,8 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.smqa_paged_release.restype = st
     lib.smqa_paged_append.argtypes = [P, P, I, I, I, I, P, P, P]
     lib.smqa_paged_append.restype = st
+    lib.smqa_paged_append_rope.argtypes = [P] * 4 + [I] * 8 + [P, P, P]
+    lib.smqa_paged_append_rope.restype = st
     lib.smqa_paged_fwd_workspace_bytes.argtypes = [PagedShape]
     lib.smqa_paged_fwd_workspace_bytes.restype = ctypes.c_size_t
     lib.smqa_paged_fwd.argtypes = [P] * 9 + [PagedShape, F, P, P, P, ctypes.c_size_t, U, P]

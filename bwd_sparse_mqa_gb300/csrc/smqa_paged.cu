@@ -258,6 +258,109 @@ __device__ __forceinline__ void encode(const uint4* src, uint2* dst, int i, int 
     dst[i] = make_uint2(code(v.x) | (code(v.y) << 16), code(v.z) | (code(v.w) << 16));
   }
 }
+// Rows with the position rotation applied on the way: rope_dim elements from
+// `offset` on, in pairs (x, y) of neighbours (kPairs) or half of rope_dim apart,
+//   x' = x cos - y sin,  y' = y cos + x sin,
+// each product and sum rounded to fp32 once (no fused multiply-add, so that the
+// result does not depend on the compiler), nothing rounded to bf16 in between.
+// A row's angle is row position[t] of cos_sin [table_rows][rope_dim]: the cosines,
+// then the sines; outside the table its rotated elements are NaN.
+struct Rope {
+  const float* cos_sin;
+  const int32_t* positions;
+  int table_rows, dim, offset;
+};
+enum : int { kRopeNone = 0, kRopePairs = 1, kRopeHalves = 2 };
+
+// Elements 8 i .. 8 i + 7 of the rows from token t on (`shift`: log2 of D / 8).
+template <int kRope>
+__device__ __forceinline__ void rotated(const uint4* src, int i, int t, int shift, const Rope& r, float (&x)[8]) {
+  auto unpack = [](uint4 v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[2 * k] = __uint_as_float(w[k] << 16);
+      f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  };
+  unpack(load(src + i), x);
+  const int at = ((i & ((1 << shift) - 1)) << 3) - r.offset;  // (a multiple of 8, as r.offset and r.dim / 2 are)
+  if (static_cast<unsigned>(at) >= static_cast<unsigned>(r.dim)) return;
+  const int half = r.dim >> 1;
+  const int pos = load(r.positions + t + (i >> shift));
+  if (static_cast<unsigned>(pos) >= static_cast<unsigned>(r.table_rows)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(0x7fffffffu);
+    return;
+  }
+  const float* row = r.cos_sin + static_cast<int64_t>(pos) * r.dim;
+  auto load4 = [](const float* p, float* f) {
+    const uint4 v = load(reinterpret_cast<const uint4*>(p));
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+  };
+  if constexpr (kRope == kRopePairs) {
+    float c[4], s[4];
+    load4(row + (at >> 1), c);
+    load4(row + half + (at >> 1), s);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float a = x[2 * k], b = x[2 * k + 1];
+      x[2 * k] = __fsub_rn(__fmul_rn(a, c[k]), __fmul_rn(b, s[k]));
+      x[2 * k + 1] = __fadd_rn(__fmul_rn(b, c[k]), __fmul_rn(a, s[k]));
+    }
+  } else {
+    const bool first = at < half;
+    const int m = first ? at : at - half;
+    float c[8], s[8], y[8];
+    load4(row + m, c);
+    load4(row + m + 4, c + 4);
+    load4(row + half + m, s);
+    load4(row + half + m + 4, s + 4);
+    unpack(load(src + (first ? i + (half >> 3) : i - (half >> 3))), y);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float a = __fmul_rn(x[k], c[k]), b = __fmul_rn(y[k], s[k]);
+      x[k] = first ? __fsub_rn(a, b) : __fadd_rn(a, b);
+    }
+  }
+}
+// As `largest` (the bits of an fp32 magnitude) and `encode`, of rotated rows.
+template <int kRope>
+__device__ __forceinline__ uint32_t largest_rotated(const uint4* src, int i, int step, int n, int t, int shift, const Rope& r) {
+  uint32_t top = 0;
+#pragma unroll 2
+  for (; i < n; i += step) {
+    float x[8];
+    rotated<kRope>(src, i, t, shift, r, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t b = __float_as_uint(x[k]) & 0x7fffffffu;
+      top = max(top, b < 0x7f800000u ? b : 0u);
+    }
+  }
+  return top;
+}
+template <int kRope>
+__device__ __forceinline__ void encode_rotated(const uint4* src, uint2* dst, int i, int step, int n, float inv, int t,
+                                               int shift, const Rope& r) {
+#pragma unroll 2
+  for (; i < n; i += step) {
+    float x[8];
+    rotated<kRope>(src, i, t, shift, r, x);
+    uint32_t c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      auto scaled = [&](float v) {  // (an infinity becomes NaN)
+        return (__float_as_uint(v) & 0x7fffffffu) >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : v * inv;
+      };
+      c[k] = e4m3x2(scaled(x[2 * k]), scaled(x[2 * k + 1]));
+    }
+    dst[i] = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  }
+}
 // Codes times f = 2^-k.
 __device__ __forceinline__ void rescale(uint4* row, int i, int step, int n, float f) {
 #pragma unroll 8
@@ -273,9 +376,10 @@ __device__ __forceinline__ void rescale(uint4* row, int i, int step, int n, floa
   }
 }
 
+template <int kRope>
 __global__ void __launch_bounds__(kAppendThreads, 2)
     smqa_paged_append_kernel(const __nv_bfloat16* kv_new, const int32_t* slots, int T, int D,
-                             int page_shift, int n_slots, uint8_t* cache, float* scales) {
+                             int page_shift, int n_slots, uint8_t* cache, float* scales, const Rope rope) {
   __shared__ int runs, grown;                            // long runs: first row, number of rows;
   __shared__ int run_at[kAppendWarps], run_rows[kAppendWarps];
   __shared__ int grown_to[kAppendWarps];                 // pages whose scale has grown: up to this
@@ -283,6 +387,20 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
   __shared__ uint32_t warp_top[2][kAppendWarps];         // (of even and odd runs)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int page = 1 << page_shift;
+  const int row_shift = __ffs(D) - 4;                    // log2 of a row's uint4
+  // The bits of the largest finite magnitude of rows t.. as fp32, and their codes.
+  auto top_of = [&](const uint4* src, int i, int step, int n, int t) {
+    if constexpr (kRope == kRopeNone)
+      return __reduce_max_sync(0xffffffffu, largest(src, i, step, n)) << 16;
+    else
+      return __reduce_max_sync(0xffffffffu, largest_rotated<kRope>(src, i, step, n, t, row_shift, rope));
+  };
+  auto write = [&](const uint4* src, uint2* dst, int i, int step, int n, float inv, int t) {
+    if constexpr (kRope == kRopeNone)
+      encode(src, dst, i, step, n, inv);
+    else
+      encode_rotated<kRope>(src, dst, i, step, n, inv, t, row_shift, rope);
+  };
   if (tid == 0) runs = grown = 0;
   __syncthreads();
   grid_dependency_wait();                                // (launched beside the kernel before,
@@ -313,9 +431,9 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
         const float had = __shfl_sync(0xffffffffu, off && lane == 0 ? scales[pg] : 0.f, 0);  // (which lane 0 writes)
         const int n = rows * D / 8;
         const uint4* src = reinterpret_cast<const uint4*>(kv_new + static_cast<int64_t>(t) * D);
-        const uint32_t top = __reduce_max_sync(0xffffffffu, largest(src, lane, 32, n));
-        const float s = fmaxf(pow2f(scale_exponent(__uint_as_float(top << 16))), had);
-        encode(src, reinterpret_cast<uint2*>(cache + static_cast<int64_t>(s0) * D), lane, 32, n, 1.f / s);
+        const uint32_t top = top_of(src, lane, 32, n, t);
+        const float s = fmaxf(pow2f(scale_exponent(__uint_as_float(top))), had);
+        write(src, reinterpret_cast<uint2*>(cache + static_cast<int64_t>(s0) * D), lane, 32, n, 1.f / s, t);
         if (lane == 0) {
           scales[pg] = s;
           if (off && s > had) {
@@ -344,13 +462,13 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
     const float had = off ? scales[pg] : 0.f;            // (written behind a barrier)
     const int n = run_rows[i] * D / 8;
     const uint4* src = reinterpret_cast<const uint4*>(kv_new + static_cast<int64_t>(t) * D);
-    uint32_t top = __reduce_max_sync(0xffffffffu, largest(src, tid, kAppendThreads, n));
+    uint32_t top = top_of(src, tid, kAppendThreads, n, t);
     if (lane == 0) warp_top[i & 1][warp] = top;
     __syncthreads();
     for (int w = 0; w < kAppendWarps; ++w) top = max(top, warp_top[i & 1][w]);
-    const float s = fmaxf(pow2f(scale_exponent(__uint_as_float(top << 16))), had);
+    const float s = fmaxf(pow2f(scale_exponent(__uint_as_float(top))), had);
     if (off && s > had) rescale(reinterpret_cast<uint4*>(cache + (pg << page_shift) * D), tid, kAppendThreads, off * D / 16, had / s);
-    encode(src, reinterpret_cast<uint2*>(cache + static_cast<int64_t>(s0) * D), tid, kAppendThreads, n, 1.f / s);
+    write(src, reinterpret_cast<uint2*>(cache + static_cast<int64_t>(s0) * D), tid, kAppendThreads, n, 1.f / s, t);
     if (tid == 0) scales[pg] = s;
   }
 }
@@ -385,6 +503,30 @@ smqa_status check_paged(const smqa_paged_shape& s) {
     return refuse(SMQA_ERR_UNSUPPORTED,
                   "unsupported paged shape (need 1<=H<=128, D in {64,512}, page_size in "
                   "{16,32,64,128}, topk and max_pages * page_size <= 2^31 - 128, sizes < 2^31)");
+  return SMQA_OK;
+}
+
+// T rows of checked sizes.
+template <int kRope>
+smqa_status launch_append(const void* kv_new, const int32_t* slots, int T, int D, int shift, int n_slots,
+                          void* kv_cache, float* kv_scales, const Rope& rope, cudaStream_t stream) {
+  if (T == 0) return SMQA_OK;
+  if (!kv_new || !slots || !kv_cache || !kv_scales || !is_aligned(kv_new, 16) || !is_aligned(kv_cache, 16) ||
+      !is_aligned(slots, 4) || !is_aligned(kv_scales, 4))
+    return refuse(SMQA_ERR_INVALID_ARG, "null or misaligned pointer");
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((T - 1) / kAppendWarps + 1));
+  cfg.blockDim = dim3(kAppendThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, smqa_paged_append_kernel<kRope>,
+                                           static_cast<const __nv_bfloat16*>(kv_new), slots, T, D, shift, n_slots,
+                                           static_cast<uint8_t*>(kv_cache), kv_scales, rope);
+  if (e != cudaSuccess) return cuda_failure(e, "paged append launch");
   return SMQA_OK;
 }
 
@@ -485,24 +627,31 @@ smqa_status smqa_paged_append(const void* kv_new, const int32_t* slot_mapping, i
     return refuse(SMQA_ERR_UNSUPPORTED,
                   "unsupported paged append (need D in {64,512}, page_size in {16,32,64,128}, "
                   "sizes < 2^31)");
-  if (T == 0) return SMQA_OK;
-  if (!kv_new || !slot_mapping || !kv_cache || !kv_scales || !is_aligned(kv_new, 16) ||
-      !is_aligned(kv_cache, 16) || !is_aligned(slot_mapping, 4) || !is_aligned(kv_scales, 4))
+  return launch_append<kRopeNone>(kv_new, slot_mapping, T, D, shift, n_pages * page_size, kv_cache, kv_scales, Rope{},
+                                  stream);
+}
+
+smqa_status smqa_paged_append_rope(const void* kv_new, const int32_t* slot_mapping,
+                                   const int32_t* positions, const float* cos_sin, int32_t T,
+                                   int32_t D, int32_t page_size, int32_t n_pages,
+                                   int32_t table_rows, int32_t rope_dim, int32_t rope_offset,
+                                   int32_t interleaved, void* kv_cache, float* kv_scales,
+                                   cudaStream_t stream) {
+  if (T < 0 || D <= 0 || page_size <= 0 || n_pages <= 0 || table_rows < 0 || rope_dim < 0 || rope_offset < 0)
+    return refuse(SMQA_ERR_INVALID_ARG, "negative or zero size in paged append");
+  const int shift = page_shift_of(page_size);
+  if ((D != 64 && D != 128 && D != 512) || shift < 0 || static_cast<int64_t>(n_pages) * page_size >= kLim ||
+      (rope_dim & 15) || (rope_offset & 7) || static_cast<int64_t>(rope_offset) + rope_dim > D)
+    return refuse(SMQA_ERR_UNSUPPORTED,
+                  "unsupported paged append (need D in {64,128,512}, page_size in {16,32,64,128}, sizes < 2^31, "
+                  "rope_dim a multiple of 16, rope_offset of 8, both within D)");
+  if (T > 0 && rope_dim > 0 &&
+      (!positions || (table_rows > 0 && !cos_sin) || !is_aligned(positions, 4) || !is_aligned(cos_sin, 16)))
     return refuse(SMQA_ERR_INVALID_ARG, "null or misaligned pointer");
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((T - 1) / kAppendWarps + 1));
-  cfg.blockDim = dim3(kAppendThreads);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(
-      &cfg, smqa_paged_append_kernel, static_cast<const __nv_bfloat16*>(kv_new), slot_mapping, T, D,
-      shift, n_pages * page_size, static_cast<uint8_t*>(kv_cache), kv_scales);
-  if (e != cudaSuccess) return cuda_failure(e, "paged append launch");
-  return SMQA_OK;
+  const Rope rope{cos_sin, positions, table_rows, rope_dim, rope_offset};
+  const auto launch = rope_dim == 0 ? launch_append<kRopeNone>
+                      : interleaved ? launch_append<kRopePairs> : launch_append<kRopeHalves>;
+  return launch(kv_new, slot_mapping, T, D, shift, n_pages * page_size, kv_cache, kv_scales, rope, stream);
 }
 
 size_t smqa_paged_fwd_workspace_bytes(smqa_paged_shape shape) {

@@ -151,17 +151,27 @@ def paged_release(block_table: torch.Tensor, release: torch.Tensor, free_pages: 
 
 
 def paged_kv_append(kv_new: torch.Tensor, slot_mapping: torch.Tensor, kv_cache: torch.Tensor,
-                    kv_scales: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+                    kv_scales: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                    cos_sin: Optional[torch.Tensor] = None, rope_offset: Optional[int] = None,
+                    interleaved: bool = False) -> tuple[torch.Tensor, torch.Tensor]:
     """Writes kv_new [T, D] bf16 into the cache at slot_mapping [T] int32 (C
-    ABI ``smqa_paged_append``); -1 skips a row.  In place; returns (kv_cache,
-    kv_scales).
+    ABI ``smqa_paged_append``, ``smqa_paged_append_rope``); -1 skips a row.  In
+    place; returns (kv_cache, kv_scales).  D is 64 or 512, or 128 for the
+    indexer's keys.
 
     A page's scale is the smallest power of two that keeps its values within
     e4m3's 448; it grows while the page fills (the page's older rows are
     rescaled) and starts afresh when the page's first row is written.  The rows
     of one page must be consecutive, with slots ascending by one, as
     paged_plan lists them; a page listed otherwise (a slot twice, its rows apart)
-    gets undefined codes and scale, the other pages theirs."""
+    gets undefined codes and scale, the other pages theirs.
+
+    With ``cos_sin`` [rows, rope_dim] fp32 (the cosines of a position's
+    rope_dim/2 angles, then their sines) and ``positions`` [T] int32 the rows are
+    rotated on the way, in fp32: rope_dim elements from ``rope_offset`` on (None:
+    the last ones), in pairs of neighbours (``interleaved``) or rope_dim/2 apart.
+    A position outside the table makes its row's rotated elements NaN."""
+    rope = cos_sin is not None
     try:
         dev = kv_cache.get_device()
         n_pages, page_size, D = kv_cache.shape
@@ -173,16 +183,36 @@ def paged_kv_append(kv_new: torch.Tensor, slot_mapping: torch.Tensor, kv_cache: 
               and slot_mapping.shape == (T,) and kv_cache.is_contiguous()
               and kv_scales.is_contiguous() and kv_new.is_contiguous()
               and slot_mapping.is_contiguous())
+        if rope and ok:
+            rows, dim = cos_sin.shape
+            offset = D - dim if rope_offset is None else rope_offset
+            ok = (cos_sin.dtype is _F32 and positions.dtype is _I32
+                  and cos_sin.get_device() == positions.get_device() == dev
+                  and positions.shape == (T,) and cos_sin.is_contiguous()
+                  and positions.is_contiguous() and dim > 0 and 0 <= offset < _LIM and rows < _LIM)
     except (AttributeError, ValueError, IndexError):
         ok = False
-    if not ok:
-        _explain("kv_cache [n_pages,page_size,D], kv_scales [n_pages], kv_new [T,D] and "
-                 "slot_mapping [T] do not have matching shapes",
+    if not ok or (not rope and (positions is not None or rope_offset is not None)):
+        more = [(positions, "positions", _I32, 1), (cos_sin, "cos_sin", _F32, 2)]
+        _explain("kv_cache [n_pages,page_size,D], kv_scales [n_pages], kv_new [T,D], "
+                 "slot_mapping [T], positions [T] and cos_sin [rows, 1 <= rope_dim <= D] (both or "
+                 "neither, rope_offset >= 0 only with them) do not have matching shapes",
                  (kv_cache, "kv_cache", _E4M3, 3), (kv_scales, "kv_scales", _F32, 1),
-                 (kv_new, "kv_new", _BF16, 2), (slot_mapping, "slot_mapping", _I32, 1))
-    _call("smqa_paged_append", dev, _lib.load().smqa_paged_append, kv_new.data_ptr(),
-          slot_mapping.data_ptr(), T, D, page_size, n_pages, kv_cache.data_ptr(),
-          kv_scales.data_ptr())
+                 (kv_new, "kv_new", _BF16, 2), (slot_mapping, "slot_mapping", _I32, 1),
+                 *(more if rope else []))
+    if rope:
+        _call("smqa_paged_append_rope", dev, _lib.load().smqa_paged_append_rope, kv_new.data_ptr(),
+              slot_mapping.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), T, D, page_size,
+              n_pages, rows, dim, offset, bool(interleaved), kv_cache.data_ptr(),
+              kv_scales.data_ptr())
+    elif D == 128:
+        _call("smqa_paged_append_rope", dev, _lib.load().smqa_paged_append_rope, kv_new.data_ptr(),
+              slot_mapping.data_ptr(), None, None, T, D, page_size, n_pages, 0, 0, 0, 0,
+              kv_cache.data_ptr(), kv_scales.data_ptr())
+    else:
+        _call("smqa_paged_append", dev, _lib.load().smqa_paged_append, kv_new.data_ptr(),
+              slot_mapping.data_ptr(), T, D, page_size, n_pages, kv_cache.data_ptr(),
+              kv_scales.data_ptr())
     return kv_cache, kv_scales
 
 

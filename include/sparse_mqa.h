@@ -454,6 +454,27 @@ smqa_status smqa_paged_append(const void* kv_new, const int32_t* slot_mapping, i
                               int32_t D, int32_t page_size, int32_t n_pages, void* kv_cache,
                               float* kv_scales, cudaStream_t stream);
 
+/*
+ * The same with the position rotation applied on the way, and for rows of 128
+ * as well (the indexer's keys): D in {64, 128, 512}.
+ *   positions    int32 [T]   position of each row
+ *   cos_sin      fp32 [table_rows, rope_dim]  cosines of a position's rope_dim/2
+ *                            angles, then their sines; 16-byte aligned
+ * Of each row the rope_dim elements from rope_offset on are rotated: pairs
+ * (x, y), neighbours if `interleaved` is nonzero, else rope_dim / 2 apart,
+ * become (x cos - y sin, y cos + x sin), each operation rounded to fp32; the
+ * scale and the codes are of those values.  Pairs with a NaN or an infinity, and
+ * all pairs of a row whose position lies outside [0, table_rows), are stored as
+ * NaN.  rope_dim is a multiple of 16 (0: no rotation; positions and cos_sin may
+ * be NULL), rope_offset of 8, both within D.  One launch.
+ */
+smqa_status smqa_paged_append_rope(const void* kv_new, const int32_t* slot_mapping,
+                                   const int32_t* positions, const float* cos_sin, int32_t T,
+                                   int32_t D, int32_t page_size, int32_t n_pages,
+                                   int32_t table_rows, int32_t rope_dim, int32_t rope_offset,
+                                   int32_t interleaved, void* kv_cache, float* kv_scales,
+                                   cudaStream_t stream);
+
 /* smqa_paged_fwd: write O = 0 and lse = -inf for tokens of no request
  * (padding); without it their rows of o and lse are left as they were. */
 #define SMQA_FLAG_ZERO_PADDING 16u
