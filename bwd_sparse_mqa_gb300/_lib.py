@@ -35,7 +35,8 @@ EXPORTS = [
     "smqa_fwd_bwd_host", "smqa_host_chunk_plan", "smqa_set_wait_limit_ns", "smqa_debug_stall",
     "smqa_indexer_bwd", "smqa_batched_indexer_bwd", "smqa_paged_plan", "smqa_paged_release",
     "smqa_paged_append", "smqa_paged_fwd_workspace_bytes", "smqa_paged_fwd",
-    "smqa_paged_append_rope",
+    "smqa_paged_append_rope", "smqa_indexer_topk_workspace_bytes", "smqa_indexer_topk",
+    "smqa_paged_indexer_topk_workspace_bytes", "smqa_paged_indexer_topk",
 ]
 STATIC_SCRATCH_BYTES = 64 << 20
 
@@ -110,6 +111,14 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.smqa_paged_fwd_workspace_bytes.restype = ctypes.c_size_t
     lib.smqa_paged_fwd.argtypes = [P] * 9 + [PagedShape, F, P, P, P, ctypes.c_size_t, U, P]
     lib.smqa_paged_fwd.restype = st
+    lib.smqa_indexer_topk_workspace_bytes.argtypes = [S, I]
+    lib.smqa_indexer_topk_workspace_bytes.restype = ctypes.c_size_t
+    lib.smqa_indexer_topk.argtypes = [P, P, P, S, I, I, ctypes.c_int64, P, P, ctypes.c_size_t, P]
+    lib.smqa_indexer_topk.restype = st
+    lib.smqa_paged_indexer_topk_workspace_bytes.argtypes = [PagedShape, I]
+    lib.smqa_paged_indexer_topk_workspace_bytes.restype = ctypes.c_size_t
+    lib.smqa_paged_indexer_topk.argtypes = [P] * 8 + [PagedShape, I, I, P, P, ctypes.c_size_t, U, P]
+    lib.smqa_paged_indexer_topk.restype = st
     lib.smqa_debug_stall.argtypes = [ctypes.c_int]
     lib.smqa_debug_stall.restype = None
     lib.smqa_set_wait_limit_ns.argtypes = [ctypes.c_uint64]

@@ -225,6 +225,8 @@ uint64_t current_wait_limit_ns() { return wait_limit_ns(); }
 
 int current_stall_cta() { return g_stall_cta.load(std::memory_order_relaxed); }
 
+void* tensor_map_encoder() { return reinterpret_cast<void*>(encode_fn()); }
+
 float effective_scale(float sm_scale, int D) {
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return 1.0f / std::sqrt(static_cast<float>(D));
   return sm_scale;

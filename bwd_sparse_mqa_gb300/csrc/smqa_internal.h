@@ -208,6 +208,8 @@ cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& don
 int* device_status_word(cudaError_t* err);
 uint64_t current_wait_limit_ns();
 int current_stall_cta();
+// cuTensorMapEncodeTiled of the driver (a PFN_cuTensorMapEncodeTiled_v12000; null if it lacks it).
+void* tensor_map_encoder();
 // The entry points' shape check (records the reason on failure).
 smqa_status validate_shape(const smqa_shape& s);
 // sm_scale as the entry points interpret it (<= 0 or NaN selects D^-1/2).

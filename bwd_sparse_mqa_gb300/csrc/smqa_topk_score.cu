@@ -1,0 +1,648 @@
+// smqa_topk_score.cu -- scores of the indexer's selection on sm_103a.
+//
+// For token t and the key rows j it sees,
+//   score[t, j] = sum_h w[t, h] ReLU(q[t, h] . k_j),
+// rows of up to 32 positions (a block) by their largest, as ordered integers in
+// the workspace; smqa_topk.cu chooses from them.
+//
+// A tile is 128 key rows (A, M = 128) against the heads of a group of up to
+// 256 / Hp tokens (B, N = Hp per token; Hp: H rounded up to 16, 32, 64 or 128,
+// with zero rows behind H), K = D: a thread of the epilogue has one key row in its TMEM lane, the
+// heads in columns, so the sum over heads needs no exchange between threads and
+// a warp writes 32 consecutive scores.  bf16 keys: kind::f16.  e4m3 keys (the
+// paged cache): kind::f8f6f4, the codes as they lie in the cache, the queries as
+// two e4m3 pieces added into one accumulator.
+//
+// The groups' tiles form one sequence, cut into equal ranges, one per CTA: a
+// lone token's context and the triangle of a causal prompt are spread over the
+// GPU alike.  A group's tiles share its queries, which stay in shared memory (two
+// buffers); key tiles come by TMA through a ring of 128-byte pieces.  Tokens that
+// see no more rows than they choose need no scores and are left out.
+//
+// 512 threads: warps 0-7 epilogue (two warpgroups, alternate tiles and
+// accumulators), 8 walks through the groups and issues the key tiles' copies, 9
+// feeds the tensor core, 12-15 bring the queries and weights of the next group and
+// bound the key rows' lengths (which the choice's error bound needs).
+#include <cuda_runtime.h>
+
+#include "smqa_topk.cuh"
+
+namespace smqa {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kHelpWarp0 = 12;
+constexpr int kCols = 256;                               // accumulator columns
+constexpr int kMaxGroup = 16;                            // tokens of a group
+
+// What the CTA does for one group (or the part of one that its range holds).
+struct Work {
+  int64_t tok;                                           // its first token
+  int ntok, tile0, ntiles, req;                          // (ntiles = 0: no more work)
+  int n[kMaxGroup];                                      // rows that each token sees (0: needs no scores)
+};
+
+template <int D, bool kPaged>
+struct ScoreLayout {
+  static constexpr int kRowBytes = kPaged ? D : 2 * D;
+  static constexpr int kPieces = kRowBytes > 128 ? kRowBytes / 128 : 1;  // of a key row
+  static constexpr int kPitch = kRowBytes > 128 ? 128 : kRowBytes;       // bytes of a row in a piece
+  static constexpr uint32_t kPieceBytes = kTile * kPitch;
+  static constexpr int kQParts = kPaged ? 2 : kPieces;   // (hi and lo, or 64 columns each)
+  static constexpr uint32_t kQPartBytes = kCols * kPitch;
+  static constexpr uint32_t kQBytes = kQParts * kQPartBytes;
+  static constexpr int kStages = kQBytes == 65536 ? 5 : 8;
+  static constexpr uint32_t kSwizzle = kPitch == 128 ? kSwizzle128B : kSwizzle64B;
+  static constexpr uint32_t kAtom = 8 * kPitch;          // 8 rows
+  static constexpr int kMeta = 16;                       // tiles whose page scales are kept
+  static constexpr uint32_t kOffQ = 0;
+  static constexpr uint32_t kOffK = 2 * kQBytes;
+  static constexpr uint32_t kOffW = kOffK + kStages * kPieceBytes;      // float [2][256]
+  static constexpr uint32_t kOffMeta = kOffW + 2 * kCols * 4;           // float [kMeta][8]
+  static constexpr uint32_t kOffWork = kOffMeta + kMeta * 8 * 4;        // Work [2]
+  static constexpr uint32_t kOffNorm = kOffWork + 2 * sizeof(Work);     // float [2][4]
+  static constexpr uint32_t kOffSum = kOffNorm + 32;                    // int64 [16], then the range's start
+  static constexpr uint32_t kOffBar = kOffSum + 16 * 8 + 32;
+  static constexpr int kBarKFull = 0;
+  static constexpr int kBarKEmpty = kBarKFull + kStages;
+  static constexpr int kBarAccFull = kBarKEmpty + kStages;  // [2]
+  static constexpr int kBarAccEmpty = kBarAccFull + 2;      // [2]
+  static constexpr int kBarWork = kBarAccEmpty + 2;         // [2] work described
+  static constexpr int kBarQFull = kBarWork + 2;            // [2] queries and weights there
+  static constexpr int kBarQEmpty = kBarQFull + 2;          // [2]
+  static constexpr int kBarDrain = kBarQEmpty + 2;
+  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr uint32_t kOffCtl = kOffBar + 8 * kNumBars;  // TMEM base, abort flag
+  static constexpr uint32_t kSmem = kOffCtl + 16 + 1024;
+  static_assert(kOffBar % 8 == 0 && kOffWork % 8 == 0 && kOffSum % 8 == 0 && kOffK % 1024 == 0, "alignment");
+  static_assert(kSmem <= 232448, "shared memory budget");
+  // Tiles between the copies of one and the epilogue of another: the ring, and the two
+  // accumulators.
+  static_assert(kMeta >= kStages + 4, "page scales are read before they are replaced");
+};
+
+// One lane of a converged warp issues; bf16 operands.
+__device__ __forceinline__ void mma16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ float relu(float x) {         // (a NaN stays one)
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Whether `ok` holds for all threads of barrier `id` (whole warps): they go on, or
+// leave, together.
+__device__ __forceinline__ bool bar_all(int id, int threads, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ int tiles_for(const TopkParams& p, int n) { return n > p.topk ? (n + kTile - 1) / kTile : 0; }
+
+// The tokens of unit u (a group of consecutive tokens; contiguous: of one batch
+// element), as [first, first + count).
+template <bool kPaged>
+__device__ __forceinline__ int unit_tokens(const TopkParams& p, int64_t u, int group, int64_t& first) {
+  if constexpr (kPaged) {
+    first = u * group;
+    return static_cast<int>(min(static_cast<int64_t>(group), p.T - first));
+  } else {
+    const int per = (p.S + group - 1) / group;
+    const int64_t b = u / per;
+    const int s = static_cast<int>(u - b * per) * group;
+    first = b * p.S + s;
+    return min(group, p.S - s);
+  }
+}
+
+// Tiles of the part of a unit that starts at token i, and its end (tokens of one
+// request).
+template <bool kPaged>
+__device__ __forceinline__ int part_tiles(const TopkParams& p, int64_t first, int count, int i, int& end, int& req) {
+  if constexpr (kPaged) {
+    int tiles = tiles_for(p, visible<true>(p, first + i, req));
+    for (end = i + 1; end < count; ++end) {
+      int r;
+      const int n = visible<true>(p, first + end, r);
+      if (r != req) break;
+      tiles = max(tiles, tiles_for(p, n));
+    }
+    return req < 0 ? 0 : tiles;
+  } else {
+    end = count;                                         // (the last token sees most)
+    return tiles_for(p, visible<false>(p, first + count - 1, req));
+  }
+}
+template <bool kPaged>
+__device__ __forceinline__ int64_t unit_tiles(const TopkParams& p, int64_t u, int group) {
+  int64_t first, tiles = 0;
+  const int count = unit_tokens<kPaged>(p, u, group, first);
+  for (int i = 0, end, req; i < count; i = end) tiles += part_tiles<kPaged>(p, first, count, i, end, req);
+  return tiles;
+}
+
+template <int D, bool kPaged, int Hp>
+__global__ void __launch_bounds__(kThreads, 1)
+    smqa_topk_score_kernel(const __grid_constant__ CUtensorMap tm_k, const TopkParams p) {
+  using L = ScoreLayout<D, kPaged>;
+  constexpr int kGroup = kCols / Hp;
+  extern __shared__ uint8_t smem_raw[];
+  uint32_t base = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (base & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;
+  base += pad;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  auto bar = [&](int i) -> uint32_t { return base + L::kOffBar + 8u * static_cast<uint32_t>(i); };
+  volatile uint32_t* tmem_holder = reinterpret_cast<volatile uint32_t*>(smem + L::kOffCtl);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffCtl + 4);
+  const WaitCtl ctl{abort_flag, p.status, p.limit_ns};
+  int64_t* warp_sum = reinterpret_cast<int64_t*>(smem + L::kOffSum);
+  int64_t* start = warp_sum + 16;                        // unit, tiles of it before the range, tiles of the range
+  Work* works = reinterpret_cast<Work*>(smem + L::kOffWork);
+
+  if (tid == 0) {
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(bar(L::kBarKFull + i), 1);
+      mbar_init(bar(L::kBarKEmpty + i), kPaged ? 5 : 1);  // tensor core (and four warps that bound the rows' lengths)
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(L::kBarAccFull + i), 1);
+      mbar_init(bar(L::kBarAccEmpty + i), 4);
+      mbar_init(bar(L::kBarWork + i), 1);
+      mbar_init(bar(L::kBarQFull + i), 4);
+      mbar_init(bar(L::kBarQEmpty + i), 1 + 8 + 4);      // tensor core, epilogue, helpers
+    }
+    mbar_init(bar(L::kBarDrain), 1);
+    start[2] = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(base + L::kOffCtl, 2 * kCols);
+  // (So far beside the kernel before, whose results are read from here on.)
+  grid_dependency_wait();
+  grid_dependents_launch();
+  if (tid == 0) *abort_flag = *reinterpret_cast<volatile int*>(p.status) != 0 ? 1 : 0;
+  // The CTA's range of tiles, and the unit it starts in (each thread sums a run of
+  // units).
+  {
+    const int64_t per = (p.units + kThreads - 1) / kThreads;
+    const int64_t u0 = min(tid * per, p.units), u1 = min(u0 + per, p.units);
+    int64_t mine = 0;
+    for (int64_t u = u0; u < u1; ++u) mine += unit_tiles<kPaged>(p, p.unit0 + u, kGroup);
+    int64_t incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += x;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      total += warp_sum[w];
+    }
+    const int64_t begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+    if (begin < end && before <= begin && begin < before + mine) {
+      int64_t at = before, u = u0, n;
+      while (at + (n = unit_tiles<kPaged>(p, p.unit0 + u, kGroup)) <= begin) {
+        at += n;
+        ++u;
+      }
+      start[0] = p.unit0 + u;
+      start[1] = begin - at;
+      start[2] = end - begin;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const int64_t count_all = start[2];
+
+  if (count_all == 0 && (kPaged || warp < kHelpWarp0)) {
+    // nothing to do
+  } else if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ walk and copy
+    int64_t u = start[0], skip = start[1], left = count_all;
+    int part = 0, e = 0, tile_no = 0;                    // pieces and tiles so far
+    int64_t first;
+    int count = unit_tokens<kPaged>(p, u, kGroup, first);
+    bool ok = *abort_flag == 0;
+    for (int seg = 0;; ++seg) {
+      // The next part with tiles in the range.
+      int end = 0, req = 0, tiles = 0;
+      if (left > 0) {
+        while (true) {
+          if (part >= count) {
+            count = unit_tokens<kPaged>(p, ++u, kGroup, first);
+            part = 0;
+          }
+          tiles = part_tiles<kPaged>(p, first, count, part, end, req);
+          if (skip < tiles) break;
+          skip -= tiles;
+          part = end;
+        }
+      }
+      if (seg >= 2) ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQEmpty + (seg & 1)), ((seg >> 1) - 1) & 1, ctl));
+      if (!ok) break;
+      Work* wk = works + (seg & 1);
+      const int tile0 = static_cast<int>(skip);
+      const int ntiles = static_cast<int>(min(left, static_cast<int64_t>(tiles) - skip));
+      if (lane < kMaxGroup) {
+        int n = 0, r;
+        if (left > 0 && lane < end - part) n = visible<kPaged>(p, first + part + lane, r);
+        wk->n[lane] = n > p.topk ? n : 0;
+      }
+      if (lane == 0) {
+        wk->tok = first + part;
+        wk->ntok = end - part;
+        wk->tile0 = tile0;
+        wk->ntiles = left > 0 ? ntiles : 0;
+        wk->req = req;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kBarWork + (seg & 1)));
+      if (left <= 0) break;
+      left -= ntiles;
+      skip = 0;
+      part = end;
+      for (int i = 0; ok && i < ntiles; ++i, ++tile_no) {
+        const int j0 = (tile0 + i) * kTile;
+        int page = -1;
+        bool live = true;
+        if constexpr (kPaged) {                          // lane = page of the tile
+          const int pages = kTile >> p.page_shift, col = (j0 >> p.page_shift) + lane;
+          page = lane < pages && col < p.max_pages ? load(p.table + static_cast<int64_t>(req) * p.max_pages + col) : -1;
+          live = static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages);
+        }
+        const unsigned pages_there = __ballot_sync(0xffffffffu, live);
+#pragma unroll
+        for (int c = 0; c < L::kPieces; ++c, ++e) {
+          const int st = e % L::kStages;
+          if (e >= L::kStages)
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(L::kBarKEmpty + st), ((e / L::kStages) - 1) & 1, ctl));
+          if (!ok) break;
+          const uint32_t to = base + L::kOffK + static_cast<uint32_t>(st) * L::kPieceBytes;
+          if constexpr (kPaged) {
+            const uint32_t bytes = static_cast<uint32_t>(D) << p.page_shift;
+            // (-1 for a page that is not there: its rows get no copy, what lies in
+            // their place is never used.)
+            if (lane < 8)
+              reinterpret_cast<float*>(smem + L::kOffMeta)[(tile_no % L::kMeta) * 8 + lane] = live ? load(p.scales + page) : -1.f;
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(bar(L::kBarKFull + st), bytes * __popc(pages_there));
+            __syncwarp();
+            if (live) tma_load_2d(to + lane * bytes, &tm_k, 0, page << p.page_shift, bar(L::kBarKFull + st));
+          } else if (lane == 0) {
+            mbar_arrive_expect_tx(bar(L::kBarKFull + st), L::kPieceBytes);
+            tma_load_2d(to, &tm_k, c * 64, req * p.S_kv + j0, bar(L::kBarKFull + st));
+          }
+        }
+      }
+      if (!ok) break;
+    }
+    // Copies in flight land before the CTA ends.
+    if (lane == 0)
+      for (int i = max(0, e - L::kStages); i < e; ++i)
+        mbar_wait_drain(bar(L::kBarKFull + i % L::kStages), (i / L::kStages) & 1);
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint64_t d_k = smem_desc(base + L::kOffK, 16u, L::kAtom, L::kSwizzle);
+    const uint64_t d_q = smem_desc(base + L::kOffQ, 16u, L::kAtom, L::kSwizzle);
+    auto wait = [&](int i, int phase) { return __all_sync(0xffffffffu, mbar_wait(bar(i), phase & 1, ctl)); };
+    bool ok = *abort_flag == 0;
+    int e = 0, tile_no = 0;
+    for (int seg = 0; ok; ++seg) {
+      const int qb = seg & 1;
+      ok = wait(L::kBarWork + qb, seg >> 1);
+      if (!ok) break;
+      const int ntiles = works[qb].ntiles, ntok = works[qb].ntok;
+      if (ntiles == 0) break;
+      ok = wait(L::kBarQFull + qb, seg >> 1);
+      const uint64_t qd = d_q + ((static_cast<uint32_t>(qb) * L::kQBytes) >> 4);
+      const uint32_t idesc = kPaged ? idesc_e4m3_f32(128, 16, false) : idesc_bf16_f32(128, 16, false, false);
+      const uint32_t id = (idesc & ~(0x3fu << 17)) | (static_cast<uint32_t>(ntok * Hp >> 3) << 17);
+      for (int i = 0; ok && i < ntiles; ++i, ++tile_no) {
+        const int acc = tile_no & 1;
+        if (tile_no >= 2) ok = wait(L::kBarAccEmpty + acc, (tile_no >> 1) - 1);
+        const uint32_t d = tmem + static_cast<uint32_t>(acc) * kCols;
+#pragma unroll
+        for (int c = 0; c < L::kPieces; ++c, ++e) {
+          const int st = e % L::kStages;
+          ok = ok && wait(L::kBarKFull + st, e / L::kStages);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kd = d_k + ((static_cast<uint32_t>(st) * L::kPieceBytes) >> 4);
+          if constexpr (kPaged) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k)
+                mma8_ss(d, kd + (k * 32u >> 4), qd + ((part * L::kQPartBytes + k * 32u) >> 4), id, (part | k) != 0);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma16_ss(d, kd + (k * 32u >> 4), qd + ((c * L::kQPartBytes + k * 32u) >> 4), id, (c | k) != 0);
+          }
+          mma_commit_elect(bar(L::kBarKEmpty + st));
+        }
+        if (!ok) break;
+        mma_commit_elect(bar(L::kBarAccFull + acc));
+        if (static_cast<int>(blockIdx.x) == p.stall_cta && tile_no == 0) {  // test hook only
+          ok = __any_sync(0xffffffffu, stall_until_limit(ctl));
+          break;
+        }
+      }
+      if (ok) mma_commit_elect(bar(L::kBarQEmpty + qb));
+    }
+    mma_commit_elect(bar(L::kBarDrain));
+    mbar_wait_drain(bar(L::kBarDrain), 0);
+    __syncwarp();
+  } else if (warp >= kHelpWarp0) {
+    // ------------------------------------------------------------ queries, weights, lengths
+    const int ht = tid - 32 * kHelpWarp0, hw = warp - kHelpWarp0;  // thread of 128
+    float* norm_of = reinterpret_cast<float*>(smem + L::kOffNorm);
+    if constexpr (!kPaged) {
+      // Bounds of the key rows' lengths, a tile at a time, over all CTAs.
+      const int tiles = static_cast<int>(p.norm_ld);
+      for (int64_t i = blockIdx.x; i < static_cast<int64_t>(p.B) * tiles; i += gridDim.x) {
+        const int64_t b = i / tiles;
+        const int j = static_cast<int>(i - b * tiles) * kTile + ht;
+        float s = 0.f;
+        if (j < p.S_kv) {
+          const uint4* row = reinterpret_cast<const uint4*>(p.k + (b * p.S_kv + j) * D);
+#pragma unroll 8
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = load(row + c);
+            const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float a = __uint_as_float(w4[k] << 16), d = __uint_as_float(w4[k] & 0xffff0000u);
+              s = fmaf(a, a, fmaf(d, d, s));
+            }
+          }
+          // (An infinite row's scores are infinite or NaN, and need no bound.)
+          s = s < INFINITY ? sqrtf(s) * 1.0001f : s == INFINITY ? s : 0.f;
+          if (s == INFINITY) {                           // finite, but its square is not?
+            for (int c = 0; c < D / 8; ++c) {
+              const uint4 v = load(row + c);
+              const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+              for (int k = 0; k < 4; ++k)
+                if ((w4[k] & 0x7f80u) == 0x7f80u || (w4[k] & 0x7f800000u) == 0x7f800000u) s = 0.f;
+            }
+          }
+        }
+        const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(s)));
+        if (lane == 0) norm_of[hw] = m;
+        bar_sync(2, 128);
+        if (ht == 0) p.norms[i] = fmaxf(fmaxf(norm_of[0], norm_of[1]), fmaxf(norm_of[2], norm_of[3]));
+        bar_sync(2, 128);
+      }
+    }
+    // (A wait that fails for one of these warps ends the work of all four.)
+    bool ok = count_all > 0;
+    int e = 0;
+    for (int seg = 0; ok; ++seg) {
+      const int qb = seg & 1;
+      ok = bar_all(3, 128, mbar_wait(bar(L::kBarWork + qb), (seg >> 1) & 1, ctl));
+      if (!ok) break;
+      const Work& wk = works[qb];
+      const int ntok = wk.ntok, ntiles = wk.ntiles, tile0 = wk.tile0;
+      const int64_t tok = wk.tok;
+      if (ntiles == 0) break;
+      float* ws = reinterpret_cast<float*>(smem + L::kOffW) + qb * kCols;
+      const uint32_t to = base + L::kOffQ + static_cast<uint32_t>(qb) * L::kQBytes;
+      if constexpr (!kPaged) {
+        // The rows' 16-byte pieces, and the weights; zeros behind H.
+        for (int i = ht; i < ntok * Hp; i += 128) {
+          const int h = i % Hp;
+          ws[i] = h < p.H ? load(p.w + (tok + i / Hp) * p.H + h) : 0.f;
+        }
+        constexpr int kPer = D / 8;
+        for (int i = ht; i < ntok * Hp * kPer; i += 128) {
+          const int r = i / kPer, c = i % kPer, h = r % Hp;
+          const bool there = h < p.H;
+          const __nv_bfloat16* src = p.q + ((tok + r / Hp) * p.H + (there ? h : 0)) * D + c * 8;
+          cp_async_16_or_zero(to + (c >> 3) * L::kQPartBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), src, there);
+        }
+        cp_async_wait_all();
+      } else {
+        // Two e4m3 pieces of each row times 2^k, which its weight takes back: four lanes
+        // share a row.  (A row with a NaN or an infinity becomes NaN.)
+        constexpr int kSeg = D / 4;                      // elements per lane
+        for (int r0 = hw * 8; r0 < ntok * Hp; r0 += 32) {
+          const int r = r0 + (lane >> 2), h = r % Hp, part = lane & 3;
+          const bool there = h < p.H;
+          uint4 v[kSeg / 8];
+          uint32_t m = 0;
+#pragma unroll
+          for (int c = 0; c < kSeg / 8; ++c) {
+            v[c] = there ? load(reinterpret_cast<const uint4*>(p.q + ((tok + r / Hp) * p.H + h) * D + part * kSeg) + c)
+                         : make_uint4(0, 0, 0, 0);
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu),
+                                     __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu)));
+          }
+          m = max(m & 0xffffu, m >> 16);
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          const int k = query_exponent(m);
+          const float f = m >= 0x7f80u ? __uint_as_float(0x7fffffffu) : pow2f(k);
+          if (part == 0) ws[r] = there ? load(p.w + (tok + r / Hp) * p.H + h) * pow2f(-k) : 0.f;
+#pragma unroll
+          for (int c = 0; c < kSeg / 16; ++c) {          // 16 elements: 16 bytes of each piece
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k2 = 0; k2 < 4; ++k2) {
+              const uint4& x = v[2 * c + (k2 >> 1)];
+              const uint32_t a = (k2 & 1) ? x.z : x.x, b = (k2 & 1) ? x.w : x.y;
+              uint16_t h0, l0, h1, l1;
+              split_query(make_float2(__uint_as_float(a << 16) * f, __uint_as_float(a & 0xffff0000u) * f), h0, l0);
+              split_query(make_float2(__uint_as_float(b << 16) * f, __uint_as_float(b & 0xffff0000u) * f), h1, l1);
+              hi[k2] = h0 | (static_cast<uint32_t>(h1) << 16);
+              lo[k2] = l0 | (static_cast<uint32_t>(l1) << 16);
+            }
+            const int piece = part * (kSeg / 16) + c;
+            const uint32_t at = to + r * L::kPitch +
+                                ((L::kPitch == 128 ? piece ^ (r & 7) : piece ^ ((r >> 1) & 3)) << 4);
+            st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+            st_shared_v4(at + L::kQPartBytes, lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kBarQFull + qb));
+      if constexpr (kPaged) {
+        // Bounds of the key rows' lengths, from the tiles as they pass: thread = row.
+        // |code| 2^-8 is the fp16 number with the code's seven bits at 7-13; squares and
+        // sums of 16 of them in fp16 are off by 2^-11 each step, and lose 2^-25 each
+        // where they are subnormal.
+        for (int i = 0; ok && i < ntiles; ++i, ++e) {
+          const int st = e % L::kStages;
+          const bool there = mbar_wait(bar(L::kBarKFull + st), (e / L::kStages) & 1, ctl);
+          const uint8_t* row = smem + L::kOffK + st * L::kPieceBytes + ht * L::kPitch;
+          float s = 0.f;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            const int at = L::kPitch == 128 ? c ^ (ht & 7) : c ^ ((ht >> 1) & 3);
+            const uint4 v = *reinterpret_cast<const uint4*>(row + at * 16);
+            const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+            __half2 a = __float2half2_rn(0.f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t x = (w4[k] & 0x007f007fu) << 7, y = (w4[k] & 0x7f007f00u) >> 1;
+              a = __hfma2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&x), a);
+              a = __hfma2(*reinterpret_cast<const __half2*>(&y), *reinterpret_cast<const __half2*>(&y), a);
+            }
+            const float2 f = __half22float2(a);
+            s += f.x + f.y;
+          }
+          const float scale = reinterpret_cast<const float*>(smem + L::kOffMeta)[(e % L::kMeta) * 8 + (ht >> p.page_shift)];
+          s = sqrtf(s * 1.02f + 0x1p-16f) * 256.f * fmaxf(scale, 0.f);
+          const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(s)));
+          if (lane == 0) {
+            mbar_arrive(bar(L::kBarKEmpty + st));
+            norm_of[(e & 1) * 4 + hw] = m;
+          }
+          ok = bar_all(2, 128, there);
+          if (ok && ht < ntok) {
+            const float* nm = norm_of + (e & 1) * 4;
+            p.norms[(tok + ht - p.tok0) * p.norm_ld + tile0 + i] = fmaxf(fmaxf(nm[0], nm[1]), fmaxf(nm[2], nm[3]));
+          }
+        }
+      }
+      if (lane == 0) mbar_arrive(bar(L::kBarQEmpty + qb));
+    }
+  } else if (warp < kLoadWarp) {
+    // ------------------------------------------------------------ epilogue
+    const int group = warp >> 2, quarter = warp & 3;     // group: the tiles and the accumulator it takes
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const int my = quarter * 32 + lane;                  // this thread's row of a tile
+    const int eshift = entry_shift(p.block_shift);
+    bool ok = *abort_flag == 0;
+    int tile_no = 0;
+    for (int seg = 0; ok; ++seg) {
+      const int qb = seg & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarWork + qb), (seg >> 1) & 1, ctl));
+      if (!ok) break;
+      const Work& wk = works[qb];
+      const int ntiles = wk.ntiles, ntok = wk.ntok, tile0 = wk.tile0;
+      if (ntiles == 0) break;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQFull + qb), (seg >> 1) & 1, ctl));
+      if (!ok) break;
+      int32_t* out = p.rows + (wk.tok - p.tok0) * p.ld;
+      const float* ws = reinterpret_cast<const float*>(smem + L::kOffW) + qb * kCols;
+      for (int i = 0; ok && i < ntiles; ++i, ++tile_no) {
+        if ((tile_no & 1) != group) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarAccFull + group), (tile_no >> 1) & 1, ctl));
+        if (!ok) break;
+        tc_fence_after();
+        const int j = (tile0 + i) * kTile + my;
+        float scale = 1.f;
+        if constexpr (kPaged)
+          scale = reinterpret_cast<const float*>(smem + L::kOffMeta)[(tile_no % L::kMeta) * 8 + (my >> p.page_shift)];
+        const uint32_t t_acc = tmem + lanes + static_cast<uint32_t>(group) * kCols;
+        // A token's score of this row, written as its block's.
+        auto put = [&](int tok, float s) {
+          const int n = wk.n[tok];
+          if (j - lane >= n) return;                     // (the same for the whole warp)
+          if constexpr (kPaged) s *= scale;
+          int32_t key = key_of(s);
+          if (j >= n - p.recent) key = kKeyAlways;
+          if (j >= n || (kPaged && scale < 0.f)) key = kKeyNever;
+          for (int off = 1; off < (1 << eshift); off <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, off));
+          if ((lane & ((1 << eshift) - 1)) == 0 && j < n)
+            out[static_cast<int64_t>(tok) * p.ld + (j >> eshift)] = key;
+        };
+        constexpr int kUnits = kCols / 64;
+        float2 a0, a1;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {               // 64 columns: a token or half of one, or several
+          if (u * 64 >= ntok * Hp) break;
+          float x[64];
+          tmem_ld32x2(t_acc + u * 64, t_acc + u * 64 + 32, *reinterpret_cast<float(*)[32]>(x),
+                      *reinterpret_cast<float(*)[32]>(x + 32));
+          const float4* w4 = reinterpret_cast<const float4*>(ws + u * 64);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            if ((u * 64 + 4 * c) % Hp == 0) a0 = a1 = make_float2(0.f, 0.f);
+            const float4 wv = w4[c];
+            a0 = fma2(make_float2(wv.x, wv.y), make_float2(relu(x[4 * c]), relu(x[4 * c + 1])), a0);
+            a1 = fma2(make_float2(wv.z, wv.w), make_float2(relu(x[4 * c + 2]), relu(x[4 * c + 3])), a1);
+            if ((u * 64 + 4 * c + 4) % Hp == 0) {
+              const int tok = (u * 64 + 4 * c) / Hp;
+              if (tok < ntok) put(tok, (a0.x + a0.y) + (a1.x + a1.y));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kBarAccEmpty + group));
+      }
+      if (lane == 0) mbar_arrive(bar(L::kBarQEmpty + qb));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * kCols);
+  }
+}
+
+template <int D, bool kPaged, int Hp>
+cudaError_t launch(const CUtensorMap& tm_k, const TopkParams& p, cudaStream_t stream) {
+  using L = ScoreLayout<D, kPaged>;
+  const auto kern = smqa_topk_score_kernel<D, kPaged, Hp>;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), L::kSmem, allowed);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kSMs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tm_k, p);
+}
+template <int D, bool kPaged>
+cudaError_t launch(const CUtensorMap& tm_k, const TopkParams& p, cudaStream_t stream) {
+  switch (padded_heads(p.H)) {
+    case 16: return launch<D, kPaged, 16>(tm_k, p, stream);
+    case 32: return launch<D, kPaged, 32>(tm_k, p, stream);
+    case 64: return launch<D, kPaged, 64>(tm_k, p, stream);
+    default: return launch<D, kPaged, 128>(tm_k, p, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_topk_score(const CUtensorMap& tm_k, const TopkParams& p, int D, bool paged, cudaStream_t stream) {
+  if (paged) return D == 64 ? launch<64, true>(tm_k, p, stream) : launch<128, true>(tm_k, p, stream);
+  return D == 64 ? launch<64, false>(tm_k, p, stream) : launch<128, false>(tm_k, p, stream);
+}
+
+}  // namespace smqa

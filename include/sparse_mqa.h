@@ -523,6 +523,58 @@ smqa_status smqa_paged_fwd(const void* q, const void* kv_cache, const float* kv_
                            cudaStream_t stream);
 
 /*
+ * The indexer's selection: the positions that each token attends to, as
+ * smqa_fwd, smqa_bwd and smqa_paged_fwd take them.  (The pages give the
+ * indexer's backward only.)  Token t scores every key row j that it sees,
+ *   score[t,j] = sum_h weights[t,h] ReLU(<index_q[t,h,:], index_k[j,:]>),
+ * blocks of block_size positions (from multiples of it) by their best row, and
+ * takes the topk / block_size best blocks.
+ *   topk_idxs  [B,S,topk] int32  their positions, ascending, those that the token
+ *                            does not see left out, then -1
+ * The choice is that of the scores as real numbers, ties to the lowest block: it
+ * does not depend on the order of a sum, on the batch or on the device.  A token
+ * that sees topk positions or fewer gets all of them.  The `recent` last positions
+ * that a token sees rank above all others (they count among topk; the blocks that
+ * they can touch must not exceed topk / block_size).  A NaN ranks below every
+ * number.  index_q and weights must be finite (else the choice is unspecified, but
+ * still of positions that the token sees), and |q.k|, sum_h |w q.k| below 2^127.
+ *   index_q   bf16 [B,S,H,D]   weights fp32 [B,S,H]   index_k bf16 [B,S_kv,D]
+ * Query s of a batch element stands at position first_position + s and sees the
+ * rows j <= that position (S_kv - S: the last S positions of a causal sequence;
+ * S_kv: every row).  1 <= H <= 128, D in {64, 128}, B*S < 2^31, B*S_kv < 2^31,
+ * block_size a power of two up to 128, topk a multiple of it.  Two launches for
+ * every 512 MB of scores.
+ *   workspace  256-byte aligned, smqa_indexer_topk_workspace_bytes(shape,
+ *              block_size) bytes (0: unsupported); needs no initialisation; calls
+ *              whose kernels may overlap must not share it
+ */
+size_t smqa_indexer_topk_workspace_bytes(smqa_shape shape, int32_t block_size);
+smqa_status smqa_indexer_topk(const void* index_q, const float* weights, const void* index_k,
+                              smqa_shape shape, int32_t block_size, int32_t recent,
+                              int64_t first_position, int32_t* topk_idxs, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The same over index keys in an 8-bit paged cache (as smqa_paged_append_rope
+ * writes it), for single tokens and for prompts:
+ *   index_q   bf16 [T,H,D], weights fp32 [T,H]
+ *   k_cache   e4m3 [n_pages,page_size,D], k_scales fp32 [n_pages] (positive)
+ *   block_table, seq_lens, token_req, positions  as in smqa_paged_fwd; a token
+ *             sees the positions j <= positions[t] (NULL: all), j <
+ *             seq_lens[req], on pages that the table has
+ *   topk_idxs [T,topk]  positions in the token's own request.  Rows of padding
+ *             tokens are left as they were, or -1 with SMQA_FLAG_ZERO_PADDING.
+ */
+size_t smqa_paged_indexer_topk_workspace_bytes(smqa_paged_shape shape, int32_t block_size);
+smqa_status smqa_paged_indexer_topk(const void* index_q, const float* weights, const void* k_cache,
+                                    const float* k_scales, const int32_t* block_table,
+                                    const int32_t* seq_lens, const int32_t* token_req,
+                                    const int32_t* positions, smqa_paged_shape shape,
+                                    int32_t block_size, int32_t recent, int32_t* topk_idxs,
+                                    void* workspace, size_t workspace_bytes, unsigned flags,
+                                    cudaStream_t stream);
+
+/*
  * Reads the device status word that kernels set when a bounded wait runs out
  * (SMQA_OK if none did).  Synchronizes the current device first.  A nonzero
  * `clear` resets the word afterwards.
