@@ -4,21 +4,25 @@
 //
 // The choice is that of the scores in real numbers, ties to the lowest position, so
 // that it does not depend on how a batch is cut or summed.  The score kernel's values
-// are off by E at most (below); with T the k-th largest of them, a block above T + 2E
-// is chosen and one below T - 2E is not.  The few between are scored again: products
-// of bf16 and of e4m3 numbers are exact in fp32, and each is added with its rounding
-// error kept in a second fp32 sum (two-sum), heads in fp64.
+// are off by E at most; with T the k-th largest of them, a block above T + 2E is
+// chosen and one below T - 2E is not.  The few between are scored again in fp32
+// fused multiply-adds, whose error is a fraction of E, and those that are still open
+// with each product (exact in fp32, as bf16 and e4m3 numbers are) added with its
+// rounding error kept in a second sum (two-sum), heads in fp64.
 //
 // E = K sum_h |w_h| (c |q_h| + rho_h), K the largest length of a key row that the
-// token sees: an fp32 accumulation of D products loses at most kDotError |q||k| (a
-// step is off by 2^-24 of a partial sum of at most |q||k|, D/16 or D/32 x 2 steps,
-// each with some 2^-21 for the sum inside the step), the sum over heads (H/4 + 4)
-// 2^-24, and rho_h is what two e4m3 pieces leave of a query row (0 with bf16 keys).
+// token sees.  The tensor core drops from every product what lies 2^24 below the
+// largest term of its step, and no term or partial sum exceeds |q||k|: D products and
+// 16 step sums, c = (D + 16) 2^-24 (twice the products with two pieces of q; measured:
+// up to 2^-18.5 |q||k| at D = 128, one large product beside 127 small ones).  The sum
+// over heads adds (H/4 + 4) 2^-24; rho_h is what two e4m3 pieces leave of a query row
+// (0 with bf16 keys).
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cstdio>
+#include <type_traits>
 
 #include "smqa_topk.cuh"
 
@@ -26,44 +30,91 @@ namespace smqa {
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kItems = 16;                               // candidates of a thread that stay in registers
 constexpr int kBins = 2048;
-constexpr int kList = 1024;
-constexpr float kDotError = 0x1p-19f;
+constexpr int kList = 512;                               // (of which 509 are used: nth_of)
 constexpr int32_t kKeyNegInf = -kKeyInf - 1;            // (key_of(-infinity): the bits 0xff800000 but for the sign flipped)
 
-template <int D, bool kPaged>
+// A CTA of NT threads takes a token; of up to kCap candidates it keeps the bins of their
+// scores in shared memory.
+template <int D, int NT>
 struct SelLayout {
-  static constexpr uint32_t kOffQ = 0;                   // bf16 [128][D], 16-byte pieces c at c ^ (h mod 8)
-  static constexpr uint32_t kOffHist = 128 * D * 2;      // int [kBins]
-  static constexpr uint32_t kOffVal = kOffHist + kBins * 4;   // double [kList]
-  static constexpr uint32_t kOffIdx = kOffVal + kList * 8;    // int [kList]
-  static constexpr uint32_t kOffRow = kOffIdx + kList * 4;    // float [kWarps][D]
-  static constexpr uint32_t kOffW = kOffRow + kWarps * D * 4;  // float [128]
+  static constexpr int kWarps = NT / 32;
+  static constexpr int kCap = NT == 1024 ? 65536 : 8192;
+  static constexpr int kBatch = NT == 1024 ? 32 : 16;    // key rows that are scored again together, at most
+  static constexpr int kPitch = D * 2 + 16;              // of a staged key row, bf16 (eight rows: other banks)
+  static constexpr uint32_t kPartBytes = NT == 1024 ? 16384 : 8192;
+  static constexpr uint32_t kOffHist = 0;                // int [kBins]; in its place the parts of scores
+  static constexpr uint32_t kOffVal = kPartBytes;        // int64 [kList], or two int [kList]
+  static constexpr uint32_t kOffIdx = kOffVal + kList * 8;    // int [kList]: candidates of a border
+  static constexpr uint32_t kOffOpen = kOffIdx + kList * 4;   // int [kList]: places in idx
+  static constexpr uint32_t kOffMark = kOffOpen + kList * 4;  // int [kList]: whether idx[i] is chosen
+  static constexpr uint32_t kOffRow = kOffMark + kList * 4;   // bf16 [kBatch][D], padded
+  static constexpr uint32_t kOffScale = kOffRow + kBatch * kPitch;  // float [kBatch]
+  static constexpr uint32_t kOffW = kOffScale + kBatch * 4;   // float [128]
   static constexpr uint32_t kOffRed = kOffW + 128 * 4;        // int [8][kWarps]
-  static constexpr uint32_t kOffMisc = kOffRed + 8 * kWarps * 4;
-  static constexpr uint32_t kSmem = kOffMisc + 64;
+  static constexpr uint32_t kOffMore = kOffRed + 8 * kWarps * 4;  // int [kWarps]
+  static constexpr uint32_t kOffMisc = kOffMore + kWarps * 4;
+  static constexpr uint32_t kOffBins = kOffMisc + 64;    // uint16 [kCap]
+  static constexpr uint32_t kOffQ = kOffBins + kCap * 2;  // bf16 [H][D], 16-byte pieces c at c ^ (h mod 8)
+  static constexpr uint32_t bytes(int H) { return kOffQ + static_cast<uint32_t>(H) * D * 2; }
 };
+static_assert(SelLayout<128, 1024>::bytes(128) <= 232448, "shared memory budget");
+static_assert(3 * (SelLayout<128, 256>::bytes(64) + 1024) <= 233472, "three CTAs per SM");
 
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
 
+// A value as two fp32 numbers, hi its nearest one and lo the rest (some 48 bits; fp64
+// would take 20 times as long here).
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair sum_of(float a, float b) {  // exactly
+  const float s = __fadd_rn(a, b), back = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, back)), __fsub_rn(b, back))};
+}
+__device__ __forceinline__ Pair normal(float a, float b) {  // |a| >= |b|, or a = 0
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const Pair s = sum_of(a.hi, b.hi);
+  return normal(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ Pair times(Pair a, float f) {
+  const float x = __fmul_rn(a.hi, f);
+  return normal(x, fmaf(a.lo, f, fmaf(a.hi, f, -x)));
+}
+// Pairs as integers that order like them (not of a NaN).
+__device__ __forceinline__ long long key64_of(Pair x) {
+  return (static_cast<long long>(key_of(x.hi)) << 32) |
+         (static_cast<uint32_t>(key_of(x.lo)) ^ 0x80000000u);
+}
+__device__ __forceinline__ double value64_of(long long k) {
+  return static_cast<double>(value_of(static_cast<int32_t>(k >> 32))) +
+         value_of(static_cast<int32_t>(static_cast<uint32_t>(k) ^ 0x80000000u));
+}
+
 // What a CTA knows of its token.
-template <int D, bool kPaged>
+template <int D, bool kPaged, int NT>
 struct Token {
-  using L = SelLayout<D, kPaged>;
+  using L = SelLayout<D, NT>;
   const TopkParams& p;
   uint8_t* smem;
   int64_t t;
   int n, req;
   int tid, warp, lane;
+  float e_score, e_plain;                                // error bounds of the score kernel's values, of plain ones
 
+  template <typename T>
+  __device__ __forceinline__ T* at(uint32_t off) const {
+    return reinterpret_cast<T*>(smem + off);
+  }
   // Over the CTA, the same in all threads: with kEnds the least of v[0] and the largest
   // of v[1], and the sums of the others.
   template <int N, bool kEnds>
   __device__ __forceinline__ void reduce(int (&v)[N]) {
     static_assert(N <= 8, "room for eight values");
-    int* red = reinterpret_cast<int*>(smem + L::kOffRed);
+    int* red = at<int>(L::kOffRed);
     auto over_warp = [](int i, int x) {
       return kEnds && i == 0   ? __reduce_min_sync(0xffffffffu, x)
              : kEnds && i == 1 ? __reduce_max_sync(0xffffffffu, x)
@@ -72,12 +123,12 @@ struct Token {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int x = over_warp(i, v[i]);
-      if (lane == 0) red[i * kWarps + warp] = x;
+      if (lane == 0) red[i * L::kWarps + warp] = x;
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int x = lane < kWarps ? red[i * kWarps + lane] : kEnds && i == 0 ? INT32_MAX : kEnds && i == 1 ? INT32_MIN : 0;
+      const int x = lane < L::kWarps ? red[i * L::kWarps + lane] : kEnds && i == 0 ? INT32_MAX : kEnds && i == 1 ? INT32_MIN : 0;
       v[i] = over_warp(i, x);
     }
     __syncthreads();
@@ -87,305 +138,452 @@ struct Token {
     const int pg = load(p.table + static_cast<int64_t>(req) * p.max_pages + (j >> p.page_shift));
     return static_cast<unsigned>(pg) < static_cast<unsigned>(p.n_pages) ? pg : -1;
   }
-  // Key row j's values, D/32 per lane, into the warp's row buffer, and its scale (-1: no such row).
-  __device__ __forceinline__ float bring(int j) {
-    float* buf = reinterpret_cast<float*>(smem + L::kOffRow) + warp * D;
-    __syncwarp();
-    float scale = 1.f;
-    if constexpr (kPaged) {
-      const int pg = page_of(j);
-      if (pg < 0) return -1.f;
-      const uint8_t* src = p.codes + ((static_cast<int64_t>(pg) << p.page_shift) + (j & ((1 << p.page_shift) - 1))) * D;
-      scale = load(p.scales + pg);
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        uint16_t v;
-        asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(src + (i * 32 + lane) * 2));
-        reinterpret_cast<float2*>(buf)[i * 32 + lane] = e4m3x2_value(v);
-      }
-    } else {
-      const __nv_bfloat16* src = p.k + (static_cast<int64_t>(req) * p.S_kv + j) * D;
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        const uint32_t v = static_cast<uint32_t>(load(reinterpret_cast<const int*>(src) + i * 32 + lane));
-        reinterpret_cast<float2*>(buf)[i * 32 + lane] = make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-      }
+  // Starts the copies of the queries into shared memory.
+  __device__ __forceinline__ void start_queries() const {
+    constexpr int kPer = D / 8;
+    const __nv_bfloat16* q = p.q + t * p.H * D;
+    const uint32_t to = smem_u32(smem) + L::kOffQ;
+    for (int i = tid; i < p.H * kPer; i += NT) {
+      const int h = i / kPer, c = i % kPer;
+      cp_async_16(to + (h * kPer + (c ^ (h & 7))) * 16, q + static_cast<int64_t>(i) * 8);
     }
-    __syncwarp();
-    return scale;
+    if (tid < p.H) at<float>(L::kOffW)[tid] = load(p.w + t * p.H + tid);
   }
-  // The score of the row in the buffer: lane = head.  kExact: products and sums with
-  // their errors kept; else plain fp32, off by kPlainError K sum |w||q| at most.
-  template <bool kExact>
-  __device__ __forceinline__ double dot_heads() {
-    const float4* kb = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + L::kOffRow) + warp * D);
-    const float* w = reinterpret_cast<const float*>(smem + L::kOffW);
-    double total = 0.;
-    for (int h = lane; h < p.H; h += 32) {
-      const uint4* qr = reinterpret_cast<const uint4*>(smem + L::kOffQ) + h * (D / 8);
-      float2 s = make_float2(0.f, 0.f), err = make_float2(0.f, 0.f);
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = qr[c ^ (h & 7)];
-        const float4 ka = kb[2 * c], kc = kb[2 * c + 1];
-        const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-        const float2 k4[4] = {make_float2(ka.x, ka.y), make_float2(ka.z, ka.w), make_float2(kc.x, kc.y), make_float2(kc.z, kc.w)};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 q = make_float2(__uint_as_float(w4[i] << 16), __uint_as_float(w4[i] & 0xffff0000u));
-          if constexpr (kExact) {
-            const float2 x = mul2(q, k4[i]);
-            const float2 sum = add2(s, x), back = sub2(sum, s);
-            err = add2(err, add2(sub2(s, sub2(sum, back)), sub2(x, back)));
-            s = sum;
-          } else {
-            s = fma2(q, k4[i], s);
-          }
-        }
-      }
-      double d = static_cast<double>(s.x) + s.y;
-      if (kExact && fabs(d) < static_cast<double>(INFINITY)) d += static_cast<double>(err.x) + err.y;
-      total += static_cast<double>(w[h]) * (d > 0. ? d : d == d ? 0. : d);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    return total;
-  }
-  // The exact score of block c (a NaN as -infinity), by the whole warp: of a larger
-  // block only the rows whose plain score may exceed the best so far.
-  __device__ __forceinline__ double exact(int c, float margin) {
-    const int j0 = c << p.block_shift, j1 = min(j0 + (1 << p.block_shift), n);
-    double best = -static_cast<double>(INFINITY);
-    for (int j = j0; j < j1; ++j) {
-      const float scale = bring(j);
-      if (scale < 0.f) continue;
-      if (p.block_shift > 0 && dot_heads<false>() * scale < best - margin) continue;
-      const double x = dot_heads<true>() * scale;
-      if (x > best) best = x;
-    }
-    return best;
-  }
-};
-
-// Of candidates with keys: the one whose number r (1-based, from the largest) is
-// asked for among those that are finite, between keys lo and hi; by histograms over
-// values, then by ranks.  get(f): f(candidate, key) for all candidates of the thread.
-template <int D, bool kPaged, typename Get>
-__device__ __forceinline__ int32_t find(Token<D, kPaged>& tk, int lo, int hi, int r, Get get) {
-  using L = SelLayout<D, kPaged>;
-  int* hist = reinterpret_cast<int*>(tk.smem + L::kOffHist);
-  int* list = reinterpret_cast<int*>(tk.smem + L::kOffIdx);
-  int* misc = reinterpret_cast<int*>(tk.smem + L::kOffMisc);
-  int* red = reinterpret_cast<int*>(tk.smem + L::kOffRed);
-  while (lo < hi) {
-    // Linear in the value, or (a range that fp32 cannot hold) in the key.
-    const float half = 0.5f * value_of(lo), range = 0.5f * value_of(hi) - half;
-    const bool linear = range > 1e-30f && range < 1e38f;
-    const float per = (kBins - 0.5f) / range;
-    const int shift = max(0, 22 - __clz(static_cast<unsigned>(hi) - static_cast<unsigned>(lo)));
-    auto bin_of = [&](int key) {
-      return linear ? min(kBins - 1, static_cast<int>((0.5f * value_of(key) - half) * per))
-                    : static_cast<int>((static_cast<unsigned>(key) - static_cast<unsigned>(lo)) >> shift);
-    };
-    for (int i = tk.tid; i < kBins; i += kThreads) hist[i] = 0;
+  // Once they are there: the error bounds.  D / 8 threads share a head.
+  __device__ __forceinline__ void bounds() {
+    cp_async_wait_all();
     __syncthreads();
-    get([&](int, int key) {
-      if (key >= lo && key <= hi) atomicAdd(hist + bin_of(key), 1);
-    });
-    __syncthreads();
-    // From the top: thread i has bins kBins - 1 - 4 i and the three below.
-    constexpr int kPer = kBins / kThreads;
-    int mine[kPer], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) sum += mine[i] = hist[kBins - 1 - kPer * tk.tid - i];
-    int incl = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, off);
-      if (tk.lane >= off) incl += x;
-    }
-    if (tk.lane == 31) red[tk.warp] = incl;
-    if (tk.tid == 0) misc[3] = 0;
-    __syncthreads();
-    int above = incl - sum;
-    for (int w = 0; w < tk.warp; ++w) above += red[w];
-    if (above < r && r <= above + sum) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (above < r && r <= above + mine[i]) {
-          misc[0] = kBins - 1 - kPer * tk.tid - i;
-          misc[1] = above;
-          misc[2] = mine[i];
-        }
-        above += mine[i];
-      }
-    }
-    __syncthreads();
-    const int bin = misc[0], members = misc[2];
-    r -= misc[1];
-    if (members <= kList) {
-      get([&](int, int key) {
-        if (key >= lo && key <= hi && bin_of(key) == bin) list[atomicAdd(misc + 3, 1)] = key;
-      });
-      __syncthreads();
-      for (int i = tk.tid; i < members; i += kThreads) {
-        const int v = list[i];
-        int more = 0, same = 0;
-        for (int k = 0; k < members; ++k) {
-          more += list[k] > v;
-          same += list[k] == v;
-        }
-        if (more < r && r <= more + same) misc[0] = v;
-      }
-      __syncthreads();
-      const int found = misc[0];
-      __syncthreads();
-      return found;
-    }
-    int ends[2] = {INT32_MAX, INT32_MIN};
-    get([&](int, int key) {
-      if (key >= lo && key <= hi && bin_of(key) == bin) {
-        ends[0] = min(ends[0], key);
-        ends[1] = max(ends[1], key);
-      }
-    });
-    tk.template reduce<2, true>(ends);
-    lo = ends[0];
-    hi = ends[1];
-  }
-  return lo;
-}
-
-// The token's choice, with more candidates than choices.  kReg: the keys stay in
-// registers (up to kThreads kItems candidates), else they are read again by every pass.
-template <int D, bool kPaged, bool kReg>
-__device__ __forceinline__ void choose(Token<D, kPaged>& tk) {
-  using L = SelLayout<D, kPaged>;
-  const TopkParams& p = tk.p;
-  const int bs = 1 << p.block_shift, nb = (tk.n + bs - 1) >> p.block_shift, want = p.topk >> p.block_shift;
-  const int eshift = entry_shift(p.block_shift), per = 1 << (p.block_shift - eshift), entries = (tk.n + (1 << eshift) - 1) >> eshift;
-  int32_t* row = p.rows + (tk.t - p.tok0) * p.ld;
-  int* misc = reinterpret_cast<int*>(tk.smem + L::kOffMisc);
-  int* idx = reinterpret_cast<int*>(tk.smem + L::kOffIdx);
-  double* val = reinterpret_cast<double*>(tk.smem + L::kOffVal);
-  // A warp has a run of candidates, lane by lane.
-  const int run = ((nb + kWarps - 1) / kWarps + 31) & ~31, c0 = tk.warp * run, steps = run / 32;
-  auto fetch = [&](int c) {
-    if (c >= nb) return kKeyNever;
-    if (per == 1) return load(row + c);
-    int key = kKeyNever;
-    for (int i = 0; i < per; ++i)
-      if (c * per + i < entries) key = max(key, load(row + c * per + i));
-    return key;
-  };
-  auto store = [&](int c, int key) {                     // (all of a block in its first entry)
-    row[static_cast<int64_t>(c) * per] = key;
-    for (int i = 1; i < per; ++i)
-      if (c * per + i < entries) row[static_cast<int64_t>(c) * per + i] = kKeyNever;
-  };
-  int reg[kReg ? kItems : 1];
-  auto refresh = [&] {
-    if constexpr (kReg) {
-#pragma unroll
-      for (int i = 0; i < kItems; ++i) reg[i] = i < steps ? fetch(c0 + i * 32 + tk.lane) : kKeyNever;
-    }
-  };
-  auto get = [&](auto f) {
-    if constexpr (kReg) {
-#pragma unroll
-      for (int i = 0; i < kItems; ++i)
-        if (i < steps) f(c0 + i * 32 + tk.lane, reg[i]);
-    } else {
-#pragma unroll 4
-      for (int i = 0; i < steps; ++i) f(c0 + i * 32 + tk.lane, fetch(c0 + i * 32 + tk.lane));
-    }
-  };
-  refresh();
-
-  // E and the margin of plain scores: four threads per head.
-  float e0 = 0.f, margin = 0.f;
-  {
-    const int h = tk.tid >> 2, part = tk.tid & 3;
-    float len = 0.f, rest = 0.f, wh = 0.f;
-    if (h < p.H) {
-      const uint4* qr = reinterpret_cast<const uint4*>(tk.smem + L::kOffQ) + h * (D / 8);
-      uint4 v[D / 32];
-      uint32_t m = 0;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        v[c] = qr[(part * (D / 32) + c) ^ (h & 7)];
-        m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu), __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu)));
-      }
+    constexpr int kPer = D / 8, kHeads = NT / kPer;
+    const int c = tid % kPer;
+    float len = 0.f, rest = 0.f;
+#pragma unroll 2
+    for (int h0 = 0; h0 < p.H; h0 += kHeads) {
+      const int h = h0 + tid / kPer;
+      const bool there = h < p.H;
+      const uint4 v = there ? at<uint4>(L::kOffQ)[h * kPer + (c ^ (h & 7))] : make_uint4(0, 0, 0, 0);
+      const float w = there ? at<float>(L::kOffW)[h] : 0.f;
+      // In units that make a row's largest value 2^7 to 2^8, as the score kernel has them.
+      uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
       m = max(m & 0xffffu, m >> 16);
-      m = max(m, __shfl_xor_sync(0xfu << (tk.lane & 28), m, 1));
-      m = max(m, __shfl_xor_sync(0xfu << (tk.lane & 28), m, 2));
+#pragma unroll
+      for (int off = 1; off < kPer; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
       const int k = query_exponent(m);
-      const float f = pow2f(k), back = pow2f(-k);
+      const float f = pow2f(k);
+      const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+      float sq = 0.f, sr = 0.f;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        const uint32_t w4[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x = make_float2(__uint_as_float(w4[i] << 16) * f, __uint_as_float(w4[i] & 0xffff0000u) * f);
-          len = fmaf(x.x, x.x, fmaf(x.y, x.y, len));
-          if constexpr (kPaged) {
-            uint16_t hi, lo;
-            split_query(x, hi, lo);
-            const float2 a = e4m3x2_value(hi), b = e4m3x2_value(lo);
-            const float dx = x.x - a.x - b.x, dy = x.y - a.y - b.y;
-            rest = fmaf(dx, dx, fmaf(dy, dy, rest));
-          }
+      for (int i = 0; i < 4; ++i) {
+        const float2 y = make_float2(__uint_as_float(w4[i] << 16) * f, __uint_as_float(w4[i] & 0xffff0000u) * f);
+        sq = fmaf(y.x, y.x, fmaf(y.y, y.y, sq));
+        if constexpr (kPaged) {
+          uint16_t hi, lo;
+          split_query(y, hi, lo);
+          const float2 a = e4m3x2_value(hi), b = e4m3x2_value(lo);
+          const float dx = y.x - a.x - b.x, dy = y.y - a.y - b.y;
+          sr = fmaf(dx, dx, fmaf(dy, dy, sr));
         }
       }
-      len += __shfl_xor_sync(0xfu << (tk.lane & 28), len, 1);
-      rest += __shfl_xor_sync(0xfu << (tk.lane & 28), rest, 1);
-      len += __shfl_xor_sync(0xfu << (tk.lane & 28), len, 2);
-      rest += __shfl_xor_sync(0xfu << (tk.lane & 28), rest, 2);
-      wh = part == 0 ? fabsf(reinterpret_cast<const float*>(tk.smem + L::kOffW)[h]) * back : 0.f;
-      len = wh * sqrtf(len);
-      rest = wh * sqrtf(rest);
+#pragma unroll
+      for (int off = 1; off < kPer; off <<= 1) {
+        sq += __shfl_xor_sync(0xffffffffu, sq, off);
+        if constexpr (kPaged) sr += __shfl_xor_sync(0xffffffffu, sr, off);
+      }
+      const float wh = c == 0 ? fabsf(w) * pow2f(-k) : 0.f;
+      len = fmaf(wh, sqrtf(sq), len);
+      if constexpr (kPaged) rest = fmaf(wh, sqrtf(sr), rest);
     }
     // The longest row of the tiles that the token sees.
-    const int tiles = (tk.n + kTile - 1) / kTile;
-    const float* norms = p.norms + (kPaged ? tk.t - p.tok0 : static_cast<int64_t>(tk.req)) * p.norm_ld;
+    const int tiles = (n + kTile - 1) / kTile;
+    const float* norms = p.norms + (kPaged ? t - p.tok0 : static_cast<int64_t>(req)) * p.norm_ld;
     float top = 0.f;
-    for (int i = tk.tid; i < tiles; i += kThreads) top = fmaxf(top, load(norms + i));
+    for (int i = tid; i < tiles; i += NT) top = fmaxf(top, load(norms + i));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       len += __shfl_xor_sync(0xffffffffu, len, off);
-      rest += __shfl_xor_sync(0xffffffffu, rest, off);
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      if constexpr (kPaged) rest += __shfl_xor_sync(0xffffffffu, rest, off);
     }
-    float* red = reinterpret_cast<float*>(tk.smem + L::kOffRed);
-    if (tk.lane == 0) {
-      red[tk.warp] = len;
-      red[kWarps + tk.warp] = rest;
-      red[2 * kWarps + tk.warp] = top;
-    }
-    __syncthreads();
-    len = rest = top = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      len += red[w];
-      rest += red[kWarps + w];
-      top = fmaxf(top, red[2 * kWarps + w]);
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    float* red = at<float>(L::kOffRed);
+    if (lane == 0) {
+      red[warp] = len;
+      red[L::kWarps + warp] = rest;
+      red[2 * L::kWarps + warp] = top;
     }
     __syncthreads();
-    // (1.01 for the rounding of these sums, 2^-110 for what underflows: a lone factor of 0
+    len = lane < L::kWarps ? red[lane] : 0.f;
+    rest = lane < L::kWarps ? red[L::kWarps + lane] : 0.f;
+    top = lane < L::kWarps ? red[2 * L::kWarps + lane] : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      len += __shfl_xor_sync(0xffffffffu, len, off);
+      if constexpr (kPaged) rest += __shfl_xor_sync(0xffffffffu, rest, off);
+    }
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    __syncthreads();
+    // (1.01 for the rounding of these sums, 2^-110 for what underflows; a factor of 0
     // leaves scores of exactly 0.)
-    const float c = kDotError + (static_cast<float>(p.H) * 0.25f + 4.f) * 0x1p-24f;
-    e0 = len * top == 0.f ? 0.f : 1.01f * top * (len * c + rest) + top * 0x1p-110f;
-    margin = 1.01f * top * len * 0x1p-17f + top * 0x1p-110f;
-    if (!(e0 < INFINITY)) e0 = INFINITY;
+    const float c_score = (static_cast<float>(kPaged ? 2 * D + 16 : D + 16) + static_cast<float>(p.H) * 0.25f + 4.f) * 0x1p-24f;
+    const float tiny = top * 0x1p-110f;
+    e_score = len * top == 0.f ? 0.f : 1.01f * top * (len * c_score + rest) + tiny;
+    if (!(e_score < INFINITY)) e_score = INFINITY;
+    // Plain values: 16 products and their sum, D / 16 of these, then 16 roundings of the
+    // sum over heads and the scale.
+    e_plain = 1.01f * top * len * (static_cast<float>(17 + D / 16 + 16) * 0x1p-24f) + tiny;
+    if (!(e_plain < INFINITY)) e_plain = INFINITY;
   }
 
-  // `level` 0: the score kernel's values.  Where more candidates than the list holds lie
-  // in the window, their exact scores less T take the values' place, off by a rounding
-  // of what is left (level 1), and so again (level 2: what is still equal ties).
-  int klo = 0, khi = 0, r = 0;                           // chosen: above khi, and the first r of [klo, khi]
+  // Scores of the rows of candidates (blocks) cand(0 .. m - 1) once more, plain or exact:
+  // put(i, value) for every row that is there, by one lane each.  A batch of rows is
+  // staged as bf16 (which holds an e4m3 number).  Of larger blocks, exact scores only of
+  // rows whose plain one is `floor` or more.
+  template <bool kExact, typename Cand, typename Put>
+  __device__ __forceinline__ void score(Cand cand, int m, float floor, Put put) {
+    // (Copies: a call's parameters behind a pointer would be loaded again after every store.)
+    const int H = p.H, shift = p.block_shift, page_shift = p.page_shift, n_pages = p.n_pages, seen = n;
+    const int32_t* table = kPaged ? p.table + static_cast<int64_t>(req) * p.max_pages : nullptr;
+    const uint8_t* codes = p.codes;
+    const float* page_scales = p.scales;
+    const __nv_bfloat16* keys = kPaged ? nullptr : p.k + static_cast<int64_t>(req) * p.S_kv * D;
+    const int bs = 1 << shift, total = m << shift;
+    float* scale = at<float>(L::kOffScale);
+    // Exact: a warp has 32 elements of a row, its lanes 32 heads (or, with few heads, the
+    // heads of several rows).
+    constexpr int kParts = D / 32;
+    int nh = 1;
+    while (nh < H && nh < 32) nh <<= 1;
+    const int groups = (H + 31) / 32, heads = groups > 1 ? 32 * groups : nh, together = 32 / nh;
+    const int units = groups * kParts, slots = max(1, L::kWarps / units), slot = warp / units;
+    const int batch = kExact ? min(L::kBatch, static_cast<int>(L::kPartBytes / 8) / (kParts * heads)) : L::kBatch;
+    for (int b0 = 0; b0 < total; b0 += batch) {
+      const int rows = min(batch, total - b0);
+      for (int r = warp; r < rows; r += L::kWarps) {
+        const int j = (cand((b0 + r) >> shift) << shift) + ((b0 + r) & (bs - 1));
+        uint32_t* to = reinterpret_cast<uint32_t*>(smem + L::kOffRow + r * L::kPitch);
+        float s = -1.f;
+        if (j < seen) {
+          if constexpr (kPaged) {
+            const int pg = load(table + (j >> page_shift));
+            if (static_cast<unsigned>(pg) < static_cast<unsigned>(n_pages)) {
+              const uint8_t* src = codes + ((static_cast<int64_t>(pg) << page_shift) + (j & ((1 << page_shift) - 1))) * D;
+              s = load(page_scales + pg);
+#pragma unroll
+              for (int i = 0; i < D / 64; ++i) {
+                uint16_t v;
+                asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(src + (i * 32 + lane) * 2));
+                const float2 x = e4m3x2_value(v);
+                to[i * 32 + lane] = pack_bf16x2(x.x, x.y);
+              }
+            }
+          } else {
+            const int* src = reinterpret_cast<const int*>(keys + static_cast<int64_t>(j) * D);
+            s = 1.f;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) to[i * 32 + lane] = static_cast<uint32_t>(load(src + i * 32 + lane));
+          }
+        }
+        if (lane == 0) scale[r] = s;
+      }
+      __syncthreads();
+      if (!kExact || shift > 0) {
+        // Plain: 16 heads x 8 rows by a warp, 16 elements at a time into fresh sums, which
+        // are added in fp32 (a running sum in the tensor core would lose bits at every step).
+        const int mt = (H + 15) / 16, nt = (rows + 7) / 8;
+        float* part = at<float>(L::kOffHist);            // [mt][kBatch]
+        for (int u = warp; u < mt * nt; u += L::kWarps) {
+          const int h0 = u % mt * 16, r0 = u / mt * 8;
+          const int hl = min(h0 + (lane & 15), H - 1);
+          const uint32_t qa = smem_u32(smem) + L::kOffQ + hl * (D * 2);
+          const uint32_t* kr = reinterpret_cast<const uint32_t*>(smem + L::kOffRow + (r0 + (lane >> 2)) * L::kPitch) + (lane & 3);
+          float sum[4] = {};
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t a0, a1, a2, a3;
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
+                         : "r"(qa + (((2 * c + (lane >> 4)) ^ (hl & 7)) << 4))
+                         : "memory");
+            float d[4];
+            asm volatile(
+                "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                "{%10, %10, %10, %10};"
+                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(kr[8 * c]), "r"(kr[8 * c + 4]), "f"(0.f));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] += d[i];
+          }
+          // Heads h0 + lane / 4 and 8 more, rows r0 + 2 (lane mod 4) and the next.
+          const int ha = h0 + (lane >> 2), hb = ha + 8;
+          float x = 0.f, y = 0.f;
+          if (ha < H) {
+            x = at<float>(L::kOffW)[ha] * fmaxf(sum[0], 0.f);
+            y = at<float>(L::kOffW)[ha] * fmaxf(sum[1], 0.f);
+          }
+          if (hb < H) {
+            x = fmaf(at<float>(L::kOffW)[hb], fmaxf(sum[2], 0.f), x);
+            y = fmaf(at<float>(L::kOffW)[hb], fmaxf(sum[3], 0.f), y);
+          }
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) {
+            x += __shfl_xor_sync(0xffffffffu, x, off);
+            y += __shfl_xor_sync(0xffffffffu, y, off);
+          }
+          if (lane < 4) *reinterpret_cast<float2*>(part + u % mt * L::kBatch + r0 + 2 * lane) = make_float2(x, y);
+        }
+        __syncthreads();
+        if (tid < rows && scale[tid] >= 0.f) {
+          float x = 0.f;
+          for (int i = 0; i < mt; ++i) x += part[i * L::kBatch + tid];
+          x *= scale[tid];
+          if constexpr (kExact) {
+            if (x < floor) scale[tid] = -1.f;
+          } else {
+            put((b0 + tid) >> shift, x);
+          }
+        }
+        __syncthreads();
+      }
+      if constexpr (kExact) {
+        for (int u = warp % units; u < units && slot < slots; u += L::kWarps) {
+          const int part = u % kParts, h = u / kParts * 32 + lane % nh, hq = min(h, H - 1);
+          const uint4* qr = at<uint4>(L::kOffQ) + hq * (D / 8);
+          for (int r0 = slot * together; r0 < rows; r0 += slots * together) {
+            const int r = r0 + lane / nh;
+            if (r >= rows || scale[r] < 0.f) continue;
+            const uint4* kr = reinterpret_cast<const uint4*>(smem + L::kOffRow + r * L::kPitch) + part * 4;
+            float2 s0 = {}, s1 = {}, e0 = {}, e1 = {};
+            auto two_sum = [](float2& s, float2& err, float2 x) {
+              const float2 sum = add2(s, x), back = sub2(sum, s);
+              err = add2(err, add2(sub2(s, sub2(sum, back)), sub2(x, back)));
+              s = sum;
+            };
+            auto pair = [](uint32_t v) { return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); };
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint4 q = qr[(part * 4 + i) ^ (hq & 7)], k = kr[i];
+              two_sum(s0, e0, mul2(pair(q.x), pair(k.x)));
+              two_sum(s1, e1, mul2(pair(q.y), pair(k.y)));
+              two_sum(s0, e0, mul2(pair(q.z), pair(k.z)));
+              two_sum(s1, e1, mul2(pair(q.w), pair(k.w)));
+            }
+            two_sum(s0, e0, s1);
+            const Pair d = sum_of(s0.x, s0.y);
+            const float2 e = add2(e0, e1);
+            // (An infinity's error is no number.)
+            at<float2>(L::kOffHist)[(r * kParts + part) * heads + h] =
+                fabsf(d.hi) < INFINITY ? make_float2(d.hi, d.lo + (e.x + e.y)) : make_float2(d.hi, 0.f);
+          }
+        }
+        __syncthreads();
+        for (int r = warp; r < rows; r += L::kWarps) {
+          if (scale[r] < 0.f) continue;
+          Pair sum{0.f, 0.f};
+          for (int h = lane; h < H; h += 32) {
+            Pair d{0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+              const float2 x = at<float2>(L::kOffHist)[(r * kParts + i) * heads + h];
+              d = add(d, Pair{x.x, x.y});
+            }
+            if (d.hi > 0.f) sum = add(sum, times(d, at<float>(L::kOffW)[h]));
+          }
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1)
+            sum = add(sum, Pair{__shfl_xor_sync(0xffffffffu, sum.hi, off), __shfl_xor_sync(0xffffffffu, sum.lo, off)});
+          if (lane == 0) put((b0 + r) >> shift, times(sum, scale[r]));
+        }
+        __syncthreads();
+      }
+    }
+  }
+};
+
+// val[i] = the exact score of block cand[i] (of cand[at[i]], if `at`), as an ordered
+// integer.  (A function of its own: one copy of the code.)
+template <int D, bool kPaged, int NT>
+__device__ __noinline__ void exact_scores(Token<D, kPaged, NT> tk, const int* cand, const int* at, int m, long long* val,
+                                          float floor) {
+  for (int i = tk.tid; i < m; i += NT) val[i] = key64_of(Pair{-INFINITY, 0.f});
+  __syncthreads();
+  tk.template score<true>([&](int i) { return cand[at ? at[i] : i]; }, m, floor, [&](int i, Pair x) {
+    if (x.hi == x.hi) atomicMax(val + i, key64_of(fabsf(x.hi) < INFINITY ? x : Pair{x.hi, 0.f}));
+  });
+}
+
+// The candidates (blocks) of a token: their keys, in the token's row.  A warp has a run
+// of them, lane by lane, in `steps` steps.
+template <int D, bool kPaged, int NT>
+struct Keys {
+  using L = SelLayout<D, NT>;
+  int32_t* row;
+  int nb, per, entries, steps, c0, lane;
+
+  __device__ __forceinline__ Keys(const Token<D, kPaged, NT>& tk) {
+    const TopkParams& p = tk.p;
+    const int eshift = entry_shift(p.block_shift);
+    row = p.rows + (tk.t - p.tok0) * p.ld;
+    nb = (tk.n + (1 << p.block_shift) - 1) >> p.block_shift;
+    per = 1 << (p.block_shift - eshift);
+    entries = (tk.n + (1 << eshift) - 1) >> eshift;
+    const int run = ((nb + L::kWarps - 1) / L::kWarps + 63) & ~63;
+    steps = run / 32;
+    c0 = tk.warp * run;
+    lane = tk.lane;
+  }
+  __device__ __forceinline__ int fetch(int c) const {    // (every load made, where it is not needed of another)
+    int key = kKeyNever;
+    for (int i = 0; i < per; ++i) key = max(key, load(row + min(c * per + i, entries - 1)));
+    return c < nb ? key : kKeyNever;
+  }
+  __device__ __forceinline__ void store(int c, int key) const {  // (all of a block in its first entry)
+    row[c * per] = key;
+    for (int i = 1; i < per; ++i)
+      if (c * per + i < entries) row[c * per + i] = kKeyNever;
+  }
+  // f(candidate, key) for all of the thread's, in order (the warp's lanes together).
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    constexpr int kAhead = 8;
+    for (int i0 = 0; i0 < steps; i0 += kAhead) {
+      int key[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) key[i] = per == 1 ? load(row + min(c0 + (i0 + i) * 32 + lane, nb - 1)) : 0;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int c = c0 + (i0 + i) * 32 + lane;
+        if (i0 + i < steps) f(c, per != 1 ? fetch(c) : c < nb ? key[i] : kKeyNever);
+      }
+    }
+  }
+};
+
+// What is chosen: keys above khi, and the first r candidates of [klo, khi].
+struct Cut {
+  int klo, khi, r;
+};
+
+// The keys of x - 2 e and x + 2 e, rounded outwards.
+__device__ __forceinline__ void window(float x, float e, int& klo, int& khi) {
+  const float lo = __fadd_rd(x, -2.f * e), hi = __fadd_ru(x, 2.f * e);
+  klo = lo == lo ? key_of(lo) : kKeyNegInf;              // (infinities of opposite signs: everything)
+  khi = hi == hi ? key_of(hi) : kKeyInf;
+}
+
+// The bin that holds number r from the top, how many lie above it, and in it, into
+// misc[0..2]; 0 into misc[3].
+template <int D, bool kPaged, int NT>
+__device__ __forceinline__ void find_bin(Token<D, kPaged, NT>& tk, int r) {
+  using L = SelLayout<D, NT>;
+  const int* hist = tk.template at<int>(L::kOffHist);
+  int *misc = tk.template at<int>(L::kOffMisc), *red = tk.template at<int>(L::kOffRed);
+  constexpr int kPer = kBins / NT;                       // thread i: bins kBins - 1 - kPer i and those below
+  int mine[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) sum += mine[i] = hist[kBins - 1 - kPer * tk.tid - i];
+  int incl = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, off);
+    if (tk.lane >= off) incl += x;
+  }
+  if (tk.lane == 31) red[tk.warp] = incl;
+  if (tk.tid == 0) misc[3] = 0;
+  __syncthreads();
+  int above = incl - sum + __reduce_add_sync(0xffffffffu, tk.lane < tk.warp ? red[tk.lane] : 0);
+  if (above < r && r <= above + sum) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (above < r && r <= above + mine[i]) {
+        misc[0] = kBins - 1 - kPer * tk.tid - i;
+        misc[1] = above;
+        misc[2] = mine[i];
+      }
+      above += mine[i];
+    }
+  }
+  __syncthreads();
+}
+
+// Of keys[0 .. m): number r from the largest.  (Room for three more.)
+template <int D, bool kPaged, int NT>
+__device__ __forceinline__ int nth_of(Token<D, kPaged, NT>& tk, int* keys, int m, int r) {
+  int* misc = tk.template at<int>(SelLayout<D, NT>::kOffMisc);
+  if (tk.tid < 3) keys[m + tk.tid] = INT32_MIN;          // (below every finite value's)
+  __syncthreads();
+  const int4* k4 = reinterpret_cast<const int4*>(keys);
+  for (int i = tk.tid; i < m; i += NT) {
+    const int v = keys[i];
+    int more = 0, same = 0;
+#pragma unroll 4
+    for (int k = 0; k < (m + 3) / 4; ++k) {
+      const int4 x = k4[k];
+      more += (x.x > v) + (x.y > v) + (x.z > v) + (x.w > v);
+      same += (x.x == v) + (x.y == v) + (x.z == v) + (x.w == v);
+    }
+    if (more < r && r <= more + same) misc[0] = v;
+  }
+  __syncthreads();
+  const int found = misc[0];
+  __syncthreads();
+  return found;
+}
+
+// Of idx[0 .. m), r are to be chosen: mark[i] = 1 for those with the best exact scores,
+// ties by number.
+template <int D, bool kPaged, int NT>
+__device__ __noinline__ void settle(Token<D, kPaged, NT> tk, int m, int r) {
+  using L = SelLayout<D, NT>;
+  int *misc = tk.template at<int>(L::kOffMisc), *idx = tk.template at<int>(L::kOffIdx), *open = tk.template at<int>(L::kOffOpen);
+  int* mark = tk.template at<int>(L::kOffMark);
+  long long* val = tk.template at<long long>(L::kOffVal);
+  int* pk = reinterpret_cast<int*>(val);
+  // By plain scores first.
+  for (int i = tk.tid; i < m; i += NT) pk[i] = kKeyNegInf;
+  if (tk.tid == 0) misc[3] = 0;
+  __syncthreads();
+  tk.template score<false>([&](int i) { return idx[i]; }, m, 0.f, [&](int i, float x) { if (x == x) atomicMax(pk + i, key_of(x)); });
+  int klo, khi;
+  const float at = value_of(nth_of(tk, pk, m, r));
+  window(at, tk.e_plain, klo, khi);
+  int cnt[1] = {0};
+  for (int i = tk.tid; i < m; i += NT) {
+    const int key = pk[i];
+    mark[i] = key > khi;
+    cnt[0] += key > khi;
+    if (key >= klo && key <= khi) open[atomicAdd(misc + 3, 1)] = i;
+  }
+  tk.template reduce<1, false>(cnt);
+  m = misc[3];
+  r -= cnt[0];
+  if (m == r) {
+    for (int i = tk.tid; i < m; i += NT) mark[open[i]] = 1;
+  } else {
+    // (Their best rows' plain scores are at - 2 e_plain or more.)
+    exact_scores(tk, idx, open, m, val, at - 4.f * tk.e_plain);
+    for (int i = tk.tid; i < m; i += NT) {
+      const long long x = val[i];
+      const int c = idx[open[i]];
+      int before = 0;
+      for (int k = 0; k < m; ++k) before += val[k] > x || (val[k] == x && idx[open[k]] < c);
+      mark[open[i]] = before < r;
+    }
+  }
+  __syncthreads();
+}
+
+// The cut of any scores.  `level` 0: the score kernel's values.  Where more
+// candidates than the list holds lie in the window, their exact scores less T take the
+// values' place, off by a rounding of what is left (level 1), and so again (level 2:
+// what is still equal ties).
+template <int D, bool kPaged, int NT>
+__device__ __forceinline__ Cut any_cut(Token<D, kPaged, NT>& tk, const Keys<D, kPaged, NT>& keys, int want) {
+  using L = SelLayout<D, NT>;
+  int *hist = tk.template at<int>(L::kOffHist), *misc = tk.template at<int>(L::kOffMisc), *idx = tk.template at<int>(L::kOffIdx);
+  long long* val = tk.template at<long long>(L::kOffVal);
   double base = 0.;
   for (int level = 0;; ++level) {
+    __syncthreads();
     int v[7] = {INT32_MAX, INT32_MIN, 0, 0, 0, 0, 0};    // finite: least, largest, number; >= inf; always; NaN; never
-    get([&](int c, int key) {
+    keys.each([&](int c, int key) {
       if (key > kKeyNegInf && key < kKeyInf) {
         v[0] = min(v[0], key);
         v[1] = max(v[1], key);
@@ -394,35 +592,67 @@ __device__ __forceinline__ void choose(Token<D, kPaged>& tk) {
       v[3] += key >= kKeyInf;
       v[4] += key == kKeyAlways;
       v[5] += key == kKeyNan;
-      v[6] += c < nb && key == kKeyNever;
+      v[6] += c < keys.nb && key == kKeyNever;
     });
     tk.template reduce<7, true>(v);
-    if (nb - v[6] <= want) {                             // all there are
-      klo = khi = kKeyNever;
-      r = 0;
-      break;
-    }
-    if (want <= v[3]) {
-      klo = khi = want <= v[4] ? kKeyAlways : kKeyInf;
-      r = want <= v[4] ? want : want - v[4];
-      break;
-    }
+    if (keys.nb - v[6] <= want) return Cut{kKeyNever, kKeyNever, 0};  // all there are
+    if (want <= v[4]) return Cut{kKeyAlways, kKeyAlways, want};
+    if (want <= v[3]) return Cut{kKeyInf, kKeyInf, want - v[4]};
     if (want > v[3] + v[2]) {
-      const int neg = nb - v[6] - v[5] - v[3] - v[2];
-      r = want - v[3] - v[2];
-      klo = khi = r <= neg ? kKeyNegInf : kKeyNan;
-      if (r > neg) r -= neg;
-      break;
+      const int neg = keys.nb - v[6] - v[5] - v[3] - v[2], r = want - v[3] - v[2];
+      return r <= neg ? Cut{kKeyNegInf, kKeyNegInf, r} : Cut{kKeyNan, kKeyNan, r - neg};
     }
-    const int32_t at = find<D, kPaged>(tk, v[0], v[1], want - v[3], get);
+    // Number r of the finite keys in [lo, hi].
+    int lo = v[0], hi = v[1], r = want - v[3], at = lo;
+    while (lo < hi) {
+      // Linear in the value, or (a range that fp32 cannot hold) in the key.
+      const float half = 0.5f * value_of(lo), range = 0.5f * value_of(hi) - half;
+      const bool linear = range > 1e-30f && range < 1e38f;
+      const float per = (kBins - 0.5f) / range;
+      const int shift = max(0, 21 - __clz(static_cast<unsigned>(hi) - static_cast<unsigned>(lo)));
+      auto bin_of = [&](int key) {
+        return linear ? min(kBins - 1, static_cast<int>((0.5f * value_of(key) - half) * per))
+                      : static_cast<int>((static_cast<unsigned>(key) - static_cast<unsigned>(lo)) >> shift);
+      };
+      for (int i = tk.tid; i < kBins; i += NT) hist[i] = 0;
+      __syncthreads();
+      keys.each([&](int, int key) {
+        if (key >= lo && key <= hi) atomicAdd(hist + bin_of(key), 1);
+      });
+      __syncthreads();
+      find_bin(tk, r);
+      const int bin = misc[0], members = misc[2];
+      r -= misc[1];
+      if (members <= kList - 3) {
+        keys.each([&](int, int key) {
+          if (key >= lo && key <= hi && bin_of(key) == bin) idx[atomicAdd(misc + 3, 1)] = key;
+        });
+        __syncthreads();
+        lo = hi = nth_of(tk, idx, members, r);
+      } else {
+        int ends[2] = {INT32_MAX, INT32_MIN};
+        keys.each([&](int, int key) {
+          if (key >= lo && key <= hi && bin_of(key) == bin) {
+            ends[0] = min(ends[0], key);
+            ends[1] = max(ends[1], key);
+          }
+        });
+        tk.template reduce<2, true>(ends);
+        lo = ends[0];
+        hi = ends[1];
+      }
+      at = lo;
+    }
     const float mid = value_of(at);
-    const float e = level == 0 ? e0 : level == 1 ? fmaxf(fabsf(value_of(v[0])), fabsf(value_of(v[1]))) * 0x1p-23f : 0.f;
-    klo = max(key_of(__fadd_rd(mid, -2.f * e)), kKeyNegInf + 1);
-    khi = min(key_of(__fadd_ru(mid, 2.f * e)), kKeyInf - 1);
+    const float e = level == 0 ? tk.e_score : level == 1 ? fmaxf(fabsf(value_of(v[0])), fabsf(value_of(v[1]))) * 0x1p-23f : 0.f;
+    int klo, khi;
+    window(mid, e, klo, khi);
+    klo = max(klo, kKeyNegInf + 1);
+    khi = min(khi, kKeyInf - 1);
     if (tk.tid == 0) misc[3] = 0;
     __syncthreads();
     int cnt[2] = {0, 0};
-    get([&](int c, int key) {
+    keys.each([&](int c, int key) {
       cnt[0] += key > khi;
       if (key >= klo && key <= khi) {
         ++cnt[1];
@@ -433,117 +663,277 @@ __device__ __forceinline__ void choose(Token<D, kPaged>& tk) {
     tk.template reduce<2, false>(cnt);
     const int m = cnt[1];
     r = want - cnt[0];
-    if (m == r || klo == khi) break;
-    if (m <= kList) {
-      for (int i = tk.warp; i < m; i += kWarps) {
-        const double x = tk.exact(idx[i], margin);
-        if (tk.lane == 0) val[i] = x;
-      }
-      __syncthreads();
-      for (int i = tk.tid; i < m; i += kThreads) {
-        const double x = val[i];
-        const int c = idx[i];
-        int before = 0;
-        for (int k = 0; k < m; ++k) before += val[k] > x || (val[k] == x && idx[k] < c);
-        store(c, before < r ? kKeyAlways : kKeyNever);
-      }
-      __syncthreads();
-      r = 0;
-      if constexpr (kReg) {
-#pragma unroll
-        for (int i = 0; i < kItems; ++i)
-          if (i < steps && reg[i] >= klo && reg[i] <= khi) reg[i] = fetch(c0 + i * 32 + tk.lane);
-      }
-      klo = khi;
-      break;
+    if (m == r || klo == khi) return Cut{klo, khi, r};
+    if (m <= kList - 3) {
+      settle(tk, m, r);
+      const int* mark = tk.template at<int>(L::kOffMark);
+      for (int i = tk.tid; i < m; i += NT) keys.store(idx[i], mark[i] ? kKeyAlways : kKeyNever);
+      return Cut{khi, khi, 0};
     }
-    // (base: of the values so far; the new ones' is T.)
+    // (base: of the values so far; the new ones' is T.)  As many candidates as the list
+    // holds at a time.
     base += static_cast<double>(mid);
-    for (int i = 0; i < steps; ++i) {
-      const int c = c0 + i * 32 + tk.lane, key = fetch(c);
-      const bool in = c < nb && key >= klo && key <= khi;
-      for (unsigned todo = __ballot_sync(0xffffffffu, in); todo != 0; todo &= todo - 1) {
-        const int cc = c0 + i * 32 + __ffs(todo) - 1;
-        const double x = tk.exact(cc, margin);
-        if (tk.lane == 0) store(cc, key_of(static_cast<float>(x - base)));
+    for (int x0 = 0; x0 < keys.nb; x0 += kList) {
+      __syncthreads();
+      if (tk.tid == 0) misc[3] = 0;
+      __syncthreads();
+      for (int c = x0 + tk.tid; c < min(x0 + kList, keys.nb); c += NT) {
+        const int key = keys.fetch(c);
+        if (key >= klo && key <= khi) idx[atomicAdd(misc + 3, 1)] = c;
+        else keys.store(c, key > khi ? kKeyAlways : kKeyNever);
       }
-      if (c < nb && !in) store(c, key > khi ? kKeyAlways : kKeyNever);
-      __syncwarp();
+      __syncthreads();
+      const int some = misc[3];
+      exact_scores(tk, idx, nullptr, some, val, -INFINITY);
+      for (int i = tk.tid; i < some; i += NT) keys.store(idx[i], key_of(static_cast<float>(value64_of(val[i]) - base)));
     }
-    __syncthreads();
-    refresh();
   }
+}
 
-  // Positions in order: the warps' numbers of ties, then of rows, then the rows.
-  int* red = reinterpret_cast<int*>(tk.smem + L::kOffRed);
-  auto before_warp = [&](int mine) {                     // sum over the warps before, and over all in red[kWarps]
-    if (tk.lane == 0) red[tk.warp] = mine;
-    __syncthreads();
-    int sum = 0;
-    for (int w = 0; w < tk.warp; ++w) sum += red[w];
-    return sum;
-  };
-  int ties = 0;
-  if (r > 0) get([&](int, int key) { ties += key >= klo && key <= khi; });
-  ties = __reduce_add_sync(0xffffffffu, ties);
-  int tie0 = before_warp(ties);
+// Rows of block c: those the token sees, on pages that are there; and their positions
+// into out, by the warp.
+template <int D, bool kPaged, int NT>
+__device__ __forceinline__ int rows_of(const Token<D, kPaged, NT>& tk, int c) {
+  const TopkParams& p = tk.p;
+  const int j0 = c << p.block_shift, j1 = min(j0 + (1 << p.block_shift), tk.n);
+  int sum = j1 - j0;
+  if constexpr (kPaged)
+    if (p.block_shift > p.page_shift)
+      for (int j = j0; j < j1; j += 1 << p.page_shift)
+        if (tk.page_of(j) < 0) sum -= min(1 << p.page_shift, j1 - j);
+  return sum;
+}
+template <int D, bool kPaged, int NT>
+__device__ __forceinline__ int write_block(const Token<D, kPaged, NT>& tk, int32_t* out, int at, int c) {
+  const TopkParams& p = tk.p;
+  const int j0 = c << p.block_shift, j1 = min(j0 + (1 << p.block_shift), tk.n);
+  const unsigned below = (1u << tk.lane) - 1;
+  for (int j = j0; j < j1; j += 32) {
+    bool there = j + tk.lane < j1;
+    if constexpr (kPaged) there = there && tk.page_of(j + tk.lane) >= 0;
+    const unsigned m = __ballot_sync(0xffffffffu, there);
+    if (there && at + __popc(m & below) < p.topk) out[at + __popc(m & below)] = j + tk.lane;
+    at += __popc(m);
+  }
+  return at;
+}
+// Sum of `mine` (a warp's number) over the warps before this one.
+template <int D, bool kPaged, int NT>
+__device__ __forceinline__ int before_warp(Token<D, kPaged, NT>& tk, int mine) {
+  int* red = tk.template at<int>(SelLayout<D, NT>::kOffRed);
   __syncthreads();
-  // Rows of a chosen block: those the token sees, on pages that are there.
-  auto rows_of = [&](int c) {
-    const int j0 = c << p.block_shift, j1 = min(j0 + bs, tk.n);
-    int rows = j1 - j0;
-    if constexpr (kPaged)
-      if (p.block_shift > p.page_shift)
-        for (int j = j0; j < j1; j += 1 << p.page_shift)
-          if (tk.page_of(j) < 0) rows -= min(1 << p.page_shift, j1 - j);
-    return rows;
-  };
+  if (tk.lane == 0) red[tk.warp] = mine;
+  __syncthreads();
+  return __reduce_add_sync(0xffffffffu, tk.lane < tk.warp ? red[tk.lane] : 0);
+}
+// Nothing behind the last position (after before_warp).
+template <int D, bool kPaged, int NT>
+__device__ __forceinline__ void fill_rest(Token<D, kPaged, NT>& tk, int32_t* out) {
+  using L = SelLayout<D, NT>;
+  const int* red = tk.template at<int>(L::kOffRed);
+  const int total = __reduce_add_sync(0xffffffffu, tk.lane < L::kWarps ? red[tk.lane] : 0);
+  for (int i = total + tk.tid; i < tk.p.topk; i += NT) out[i] = -1;
+}
+
+// The token's choice whatever its scores and their number: every pass reads the keys
+// again.
+template <int D, bool kPaged, int NT>
+__device__ __noinline__ void choose_any(Token<D, kPaged, NT> tk) {
+  const TopkParams& p = tk.p;
+  const Keys<D, kPaged, NT> keys(tk);
+  const Cut cut = any_cut(tk, keys, p.topk >> p.block_shift);
+  __syncthreads();
+  int tie0 = 0;
+  if (cut.r > 0) {
+    int ties = 0;
+    keys.each([&](int, int key) { ties += key >= cut.klo && key <= cut.khi; });
+    tie0 = before_warp(tk, __reduce_add_sync(0xffffffffu, ties));
+  }
   const unsigned below = (1u << tk.lane) - 1;
   auto chosen = [&](int key, int& tie) {                 // (a warp's candidates in order; tie: ties so far)
-    const bool is_tie = r > 0 && key >= klo && key <= khi;
-    const unsigned m = __ballot_sync(0xffffffffu, is_tie);
-    const bool in = (key > khi) || (is_tie && tie + __popc(m & below) < r);
-    tie += __popc(m);
+    bool in = key > cut.khi;
+    if (cut.r > 0) {
+      const bool is_tie = !in && key >= cut.klo;
+      const unsigned m = __ballot_sync(0xffffffffu, is_tie);
+      in = in || (is_tie && tie + __popc(m & below) < cut.r);
+      tie += __popc(m);
+    }
     return in;
   };
-  int rows = 0, tie = tie0;
-  get([&](int c, int key) {
-    const bool in = chosen(key, tie);
-    if (in) rows += rows_of(c);
-  });
-  rows = __reduce_add_sync(0xffffffffu, rows);
-  int at = before_warp(rows);
   int32_t* out = p.out + tk.t * p.topk;
+  int rows = 0, tie = tie0;
+  keys.each([&](int c, int key) {
+    if (chosen(key, tie)) rows += p.block_shift == 0 ? 1 : rows_of(tk, c);
+  });
+  int at = before_warp(tk, __reduce_add_sync(0xffffffffu, rows));
   tie = tie0;
-  get([&](int c, int key) {
+  keys.each([&](int c, int key) {
     const bool in = chosen(key, tie);
     unsigned m = __ballot_sync(0xffffffffu, in);
     if (p.block_shift == 0) {
-      if (in && at + __popc(m & below) < p.topk) out[at + __popc(m & below)] = c;
+      const int to = at + __popc(m & below);
+      if (in && to < p.topk) out[to] = c;
       at += __popc(m);
     } else {
-      for (; m != 0; m &= m - 1) {
-        const int cc = __shfl_sync(0xffffffffu, c, __ffs(m) - 1);
-        const int j0 = cc << p.block_shift, j1 = min(j0 + bs, tk.n);
-        for (int j = j0; j < j1; j += 32) {
-          bool there = j + tk.lane < j1;
-          if constexpr (kPaged) there = there && tk.page_of(j + tk.lane) >= 0;
-          const unsigned rm = __ballot_sync(0xffffffffu, there);
-          if (there && at + __popc(rm & below) < p.topk) out[at + __popc(rm & below)] = j + tk.lane;
-          at += __popc(rm);
-        }
-      }
+      for (; m != 0; m &= m - 1) at = write_block(tk, out, at, __shfl_sync(0xffffffffu, c, __ffs(m) - 1));
     }
   });
-  // Nothing behind the last row.
-  int total = 0;
-  for (int w = 0; w < kWarps; ++w) total += red[w];
-  for (int i = total + tk.tid; i < p.topk; i += kThreads) out[i] = -1;
+  fill_rest(tk, out);
 }
 
-template <int D, bool kPaged>
-__global__ void __launch_bounds__(kThreads) smqa_topk_select_kernel(const TopkParams p) {
-  using L = SelLayout<D, kPaged>;
+// The choice among ordinary scores: bins over the range that a sample of them suggests,
+// kept for every candidate (16 bits each: the scores are read once); what lies in and
+// next to the bin of number `want` is looked at one by one, and its bin becomes all
+// ones or 0.  False where that will not do (scores that are not numbers, a border in the
+// ends, many ties).
+template <int D, bool kPaged, int NT>
+__device__ __forceinline__ bool choose_ordinary(Token<D, kPaged, NT>& tk) {
+  using L = SelLayout<D, NT>;
+  const TopkParams& p = tk.p;
+  const Keys<D, kPaged, NT> keys(tk);
+  int *hist = tk.template at<int>(L::kOffHist), *misc = tk.template at<int>(L::kOffMisc), *idx = tk.template at<int>(L::kOffIdx);
+  int *more = tk.template at<int>(L::kOffMore), *mark = tk.template at<int>(L::kOffMark), *list = tk.template at<int>(L::kOffVal);
+  uint32_t* bins = tk.template at<uint32_t>(L::kOffBins);  // two candidates a word
+  const int want = p.topk >> p.block_shift, words = keys.steps / 2, w0 = keys.c0 / 2 + tk.lane;
+  // A lane's candidates c, c + 1 of word i: c = c0 + 64 i + 2 lane.
+  constexpr int kAhead = 8;
+  int2 key[kAhead];
+  auto ask = [&](int i) {                                // (a row is padded to whole words of four)
+    const int c = keys.c0 + i * 64 + 2 * tk.lane;
+    if (keys.per == 1) {
+      const uint2 v = load(reinterpret_cast<const uint2*>(keys.row) + min(c, keys.nb - 1) / 2);
+      return make_int2(c < keys.nb ? static_cast<int>(v.x) : kKeyNever, c + 1 < keys.nb ? static_cast<int>(v.y) : kKeyNever);
+    }
+    return make_int2(keys.fetch(c), keys.fetch(c + 1));
+  };
+  tk.start_queries();
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) key[i] = i < words ? ask(i) : make_int2(kKeyNever, kKeyNever);
+  for (int i = tk.tid; i < kBins / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+  if (tk.tid < L::kWarps) more[tk.tid] = 0;
+  tk.bounds();
+  const bool fin = key[0].x > kKeyNegInf && key[0].x < kKeyInf;
+  int ends[2] = {fin ? key[0].x : INT32_MAX, fin ? key[0].x : INT32_MIN};
+  tk.template reduce<2, true>(ends);
+  if (ends[0] >= ends[1]) return false;
+  const float a = value_of(ends[0]), b = value_of(ends[1]), range = b - a;
+  const float lo = a - 0.5f * range, per = (0.5f * kBins) / range;  // (twice the range)
+  // (fp32 has to resolve the bins.)
+  if (!(range > 1e-30f && range < 1e30f && range > 0x1p-11f * fmaxf(fabsf(a), fabsf(b)) && tk.e_score < range)) return false;
+  auto bin_of_value = [&](float x) { return max(0, min(kBins - 1, static_cast<int>((x - lo) * per))); };
+  auto bin_of = [&](int k) { return k >= kKeyInf ? kBins - 1 : bin_of_value(value_of(k)); };  // (a NaN: 0)
+  for (int i0 = 0; i0 < words; i0 += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i >= words) break;
+      const int c = keys.c0 + (i0 + i) * 64 + 2 * tk.lane;
+      const int x = bin_of(key[i].x), y = bin_of(key[i].y);
+      if (i0 + i + kAhead < words) key[i] = ask(i0 + i + kAhead);
+      if (c < keys.nb) atomicAdd(hist + x, 1);
+      if (c + 1 < keys.nb) atomicAdd(hist + y, 1);
+      bins[w0 + (i0 + i) * 32] = static_cast<uint32_t>(x) | (static_cast<uint32_t>(y) << 16);
+    }
+  }
+  __syncthreads();
+  find_bin(tk, want);
+  const int bin = misc[0];
+  // The bins that T +- 2E can reach, and one more on either side for the roundings.
+  const float w = 1.f / per, e2 = 2.f * tk.e_score;
+  const int bl = bin_of_value(lo + static_cast<float>(bin) * w - e2) - 1, bh = bin_of_value(lo + static_cast<float>(bin + 1) * w + e2) + 1;
+  if (bl < 1 || bh > kBins - 2 || bh - bl > 31) return false;
+  const int here = tk.lane <= bh - bl ? hist[bl + tk.lane] : 0;
+  const int above = misc[1] - __reduce_add_sync(0xffffffffu, bl + tk.lane > bin ? here : 0);
+  const int near = __reduce_add_sync(0xffffffffu, here);
+  if (near > kList - 3) return false;
+  int sure = 0;
+#pragma unroll 8
+  for (int i = 0; i < words; ++i) {
+    const uint32_t v = bins[w0 + i * 32];
+    const int x = v & 0xffff, y = v >> 16, c = keys.c0 + i * 64 + 2 * tk.lane;
+    sure += (x > bh) + (y > bh);
+    if (x >= bl && x <= bh) list[kList + atomicAdd(misc + 3, 1)] = c;
+    if (y >= bl && y <= bh) list[kList + atomicAdd(misc + 3, 1)] = c + 1;
+  }
+  __syncthreads();
+  for (int i = tk.tid; i < near; i += NT) list[i] = keys.fetch(list[kList + i]);
+  __syncthreads();
+  int klo, khi;
+  const float mid = value_of(nth_of(tk, list, near, want - above));
+  window(mid, tk.e_score, klo, khi);
+  // Of the list: those above the window, and those in it.
+  uint16_t* bin16 = reinterpret_cast<uint16_t*>(bins);
+  const int run = keys.steps * 32;
+  auto decide = [&](int c, bool in) {
+    bin16[c] = in ? 0xffff : 0;
+    if (in) atomicAdd(more + c / run, 1);
+  };
+  if (tk.tid == 0) misc[3] = 0;
+  __syncthreads();
+  int cnt[1] = {0};
+  for (int i = tk.tid; i < near; i += NT) {
+    const int k = list[i], c = list[kList + i];
+    cnt[0] += k > khi;
+    if (k >= klo && k <= khi) idx[atomicAdd(misc + 3, 1)] = c;
+    else decide(c, k > khi);
+  }
+  tk.template reduce<1, false>(cnt);
+  const int m = misc[3], r = want - above - cnt[0];
+  if (m == r) {
+    for (int i = tk.tid; i < m; i += NT) decide(idx[i], true);
+  } else if (klo == khi) {                               // (exact scores that tie)
+    for (int i = tk.tid; i < m; i += NT) {
+      int before = 0;
+      for (int k = 0; k < m; ++k) before += idx[k] < idx[i];
+      decide(idx[i], before < r);
+    }
+  } else {
+    settle(tk, m, r);
+    for (int i = tk.tid; i < m; i += NT) decide(idx[i], mark[i] != 0);
+  }
+  __syncthreads();
+
+  // Positions in order.
+  int32_t* out = p.out + tk.t * p.topk;
+  const unsigned below = (1u << tk.lane) - 1;
+  if (p.block_shift == 0) {
+    int at = before_warp(tk, __reduce_add_sync(0xffffffffu, sure) + more[tk.warp]);
+#pragma unroll 4
+    for (int i = 0; i < words; ++i) {
+      const uint32_t v = bins[w0 + i * 32];
+      const bool x = static_cast<int>(v & 0xffff) > bh, y = static_cast<int>(v >> 16) > bh;
+      const unsigned mx = __ballot_sync(0xffffffffu, x), my = __ballot_sync(0xffffffffu, y);
+      const int c = keys.c0 + i * 64 + 2 * tk.lane, to = at + __popc(mx & below) + __popc(my & below);
+      if (x && to < p.topk) out[to] = c;
+      if (y && to + x < p.topk) out[to + x] = c + 1;
+      at += __popc(mx) + __popc(my);
+    }
+  } else {
+    int rows = 0;
+    for (int i = 0; i < words; ++i) {
+      const uint32_t v = bins[w0 + i * 32];
+      const int c = keys.c0 + i * 64 + 2 * tk.lane;
+      if (static_cast<int>(v & 0xffff) > bh) rows += rows_of(tk, c);
+      if (static_cast<int>(v >> 16) > bh) rows += rows_of(tk, c + 1);
+    }
+    int at = before_warp(tk, __reduce_add_sync(0xffffffffu, rows));
+    for (int i = 0; i < words; ++i) {
+      const uint32_t v = bins[w0 + i * 32];
+      const unsigned mx = __ballot_sync(0xffffffffu, static_cast<int>(v & 0xffff) > bh);
+      const unsigned my = __ballot_sync(0xffffffffu, static_cast<int>(v >> 16) > bh);
+      for (unsigned todo = mx | my; todo != 0; todo &= todo - 1) {
+        const int from = __ffs(todo) - 1, c = keys.c0 + i * 64 + 2 * from;
+        if ((mx >> from) & 1u) at = write_block(tk, out, at, c);
+        if ((my >> from) & 1u) at = write_block(tk, out, at, c + 1);
+      }
+    }
+  }
+  fill_rest(tk, out);
+  return true;
+}
+
+template <int D, bool kPaged, int NT>
+__global__ void __launch_bounds__(NT, NT == 1024 ? 1 : 3) smqa_topk_select_kernel(const __grid_constant__ TopkParams p) {
+  using L = SelLayout<D, NT>;
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x;
   const int64_t t = p.tok0 + blockIdx.x;
@@ -555,70 +945,67 @@ __global__ void __launch_bounds__(kThreads) smqa_topk_select_kernel(const TopkPa
   int32_t* out = p.out + t * p.topk;
   if (req < 0) {
     if (p.zero_padding)
-      for (int i = tid; i < p.topk; i += kThreads) out[i] = -1;
+      for (int i = tid; i < p.topk; i += NT) out[i] = -1;
     return;
   }
-  Token<D, kPaged> tk{p, smem, t, n, req, tid, tid >> 5, tid & 31};
+  Token<D, kPaged, NT> tk{p, smem, t, n, req, tid, tid >> 5, tid & 31, 0.f, 0.f};
   if (n <= p.topk) {
     // All that the token sees.
     if constexpr (kPaged) {
-      int* red = reinterpret_cast<int*>(smem + L::kOffRed);
+      int* red = tk.template at<int>(L::kOffRed);
       int at = 0;
-      for (int j0 = 0; j0 < p.topk; j0 += kThreads) {
+      for (int j0 = 0; j0 < p.topk; j0 += NT) {
         const int j = j0 + tid;
         const bool there = j < n && tk.page_of(j) >= 0;
         const unsigned m = __ballot_sync(0xffffffffu, there);
         if (tk.lane == 0) red[tk.warp] = __popc(m);
         __syncthreads();
-        int before = at;
-        for (int w = 0; w < kWarps; ++w) {
-          before += w < tk.warp ? red[w] : 0;
-          at += red[w];
-        }
+        const int mine = tk.lane < L::kWarps ? red[tk.lane] : 0;
+        const int before = at + __reduce_add_sync(0xffffffffu, tk.lane < tk.warp ? mine : 0);
+        at += __reduce_add_sync(0xffffffffu, mine);
         if (there) out[before + __popc(m & ((1u << tk.lane) - 1))] = j;
         __syncthreads();
       }
-      for (int i = at + tid; i < p.topk; i += kThreads) out[i] = -1;
+      for (int i = at + tid; i < p.topk; i += NT) out[i] = -1;
     } else {
-      for (int i = tid; i < p.topk; i += kThreads) out[i] = i < n ? i : -1;
+      for (int i = tid; i < p.topk; i += NT) out[i] = i < n ? i : -1;
     }
     return;
   }
-  // Queries and weights.
-  const uint32_t q_at = smem_u32(smem) + L::kOffQ;
-  const __nv_bfloat16* q = p.q + t * p.H * D;
-  for (int i = tid; i < p.H * (D / 8); i += kThreads) {
-    const int h = i / (D / 8), c = i % (D / 8);
-    cp_async_16(q_at + h * D * 2 + ((c ^ (h & 7)) << 4), q + static_cast<int64_t>(i) * 8);
+  if ((n + (1 << p.block_shift) - 1) >> p.block_shift <= L::kCap) {
+    if (choose_ordinary(tk)) return;
+  } else {
+    tk.start_queries();
+    tk.bounds();
   }
-  if (tid < p.H) reinterpret_cast<float*>(smem + L::kOffW)[tid] = load(p.w + t * p.H + tid);
-  cp_async_wait_all();
   __syncthreads();
-  const int nb = (n + (1 << p.block_shift) - 1) >> p.block_shift;
-  if (nb <= kThreads * kItems)
-    choose<D, kPaged, true>(tk);
-  else
-    choose<D, kPaged, false>(tk);
+  choose_any(tk);
 }
 
-template <int D, bool kPaged>
+template <int D, bool kPaged, int NT>
 cudaError_t launch_select(const TopkParams& p, cudaStream_t stream) {
-  using L = SelLayout<D, kPaged>;
-  const auto kern = smqa_topk_select_kernel<D, kPaged>;
+  using L = SelLayout<D, NT>;
+  const auto kern = smqa_topk_select_kernel<D, kPaged, NT>;
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), L::kSmem, allowed);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), L::bytes(128), allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.toks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = L::kSmem;
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = L::bytes(p.H);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
+}
+// Long rows, or few tokens: 1024 threads and one CTA per SM; else 256 and three.
+template <int D, bool kPaged>
+cudaError_t launch_select(const TopkParams& p, cudaStream_t stream) {
+  return p.ld > SelLayout<D, 256>::kCap || p.toks <= kSMs ? launch_select<D, kPaged, 1024>(p, stream)
+                                                          : launch_select<D, kPaged, 256>(p, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -626,7 +1013,7 @@ cudaError_t launch_select(const TopkParams& p, cudaStream_t stream) {
 // ---------------------------------------------------------------------------
 constexpr int64_t kLim = int64_t{1} << 31;
 // Bytes of scores that a chunk of tokens may take.
-constexpr int64_t kChunkBytes = int64_t{512} << 20;
+constexpr int64_t kChunkBytes = int64_t{64} << 20;
 
 smqa_status refuse(smqa_status st, const char* why) {
   set_last_error(why);
