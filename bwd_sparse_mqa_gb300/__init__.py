@@ -15,8 +15,9 @@ from .api import (SparseMQAFunction, batched_indexer_bwd, bwd_workspace_bytes,  
                   sparse_mqa, sparse_mqa_bwd_interface, sparse_mqa_fwd_bwd_host,
                   indexer_bwd_interface, set_wait_limit_ns, sparse_mqa_fwd_host,
                   sparse_mqa_fwd_interface)
-from .indexer import (indexer_topk, indexer_topk_workspace_bytes, paged_indexer_topk,  # noqa: F401
-                      paged_indexer_topk_workspace_bytes)
+from .indexer import (IndexerScoresFunction, indexer_scores, indexer_scores_bwd,  # noqa: F401
+                      indexer_scores_fwd, indexer_topk, indexer_topk_workspace_bytes,
+                      paged_indexer_topk, paged_indexer_topk_workspace_bytes)
 from .paged import (PagedPlan, paged_fwd_workspace_bytes, paged_kv_append,  # noqa: F401
                     paged_plan, paged_release, sparse_mqa_paged_fwd)
 
@@ -26,4 +27,5 @@ __all__ = ["sparse_mqa_fwd_interface", "sparse_mqa_bwd_interface", "sparse_mqa",
            "fwd_bwd_host_workspace_bytes", "set_wait_limit_ns", "indexer_bwd_interface",
            "batched_indexer_bwd", "PagedPlan", "paged_plan", "paged_release", "paged_kv_append",
            "sparse_mqa_paged_fwd", "paged_fwd_workspace_bytes", "indexer_topk",
-           "indexer_topk_workspace_bytes", "paged_indexer_topk", "paged_indexer_topk_workspace_bytes"]
+           "indexer_topk_workspace_bytes", "paged_indexer_topk", "paged_indexer_topk_workspace_bytes",
+           "indexer_scores", "indexer_scores_fwd", "indexer_scores_bwd", "IndexerScoresFunction"]

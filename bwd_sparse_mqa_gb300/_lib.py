@@ -37,6 +37,7 @@ EXPORTS = [
     "smqa_paged_append", "smqa_paged_fwd_workspace_bytes", "smqa_paged_fwd",
     "smqa_paged_append_rope", "smqa_indexer_topk_workspace_bytes", "smqa_indexer_topk",
     "smqa_paged_indexer_topk_workspace_bytes", "smqa_paged_indexer_topk",
+    "smqa_indexer_scores", "smqa_indexer_scores_bwd_workspace_bytes", "smqa_indexer_scores_bwd",
 ]
 STATIC_SCRATCH_BYTES = 64 << 20
 
@@ -119,6 +120,12 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.smqa_paged_indexer_topk_workspace_bytes.restype = ctypes.c_size_t
     lib.smqa_paged_indexer_topk.argtypes = [P] * 8 + [PagedShape, I, I, P, P, ctypes.c_size_t, U, P]
     lib.smqa_paged_indexer_topk.restype = st
+    lib.smqa_indexer_scores.argtypes = [P, P, P, P, S, P, P]
+    lib.smqa_indexer_scores.restype = st
+    lib.smqa_indexer_scores_bwd_workspace_bytes.argtypes = [S, U]
+    lib.smqa_indexer_scores_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.smqa_indexer_scores_bwd.argtypes = [P] * 5 + [S, P, P, P, P, ctypes.c_size_t, U, P]
+    lib.smqa_indexer_scores_bwd.restype = st
     lib.smqa_debug_stall.argtypes = [ctypes.c_int]
     lib.smqa_debug_stall.restype = None
     lib.smqa_set_wait_limit_ns.argtypes = [ctypes.c_uint64]

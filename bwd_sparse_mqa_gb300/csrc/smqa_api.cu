@@ -101,10 +101,13 @@ bool encode_bf16_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t ou
   cuuint64_t strides[1] = {inner * 2};
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims,
-                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  auto encode = [&] {
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT && smqa::make_context_current()) r = encode();
   if (r != CUDA_SUCCESS) {
     std::snprintf(g_last_error, sizeof g_last_error, "cuTensorMapEncodeTiled failed (%d)",
                   static_cast<int>(r));
@@ -224,6 +227,11 @@ int* device_status_word(cudaError_t* err) { return status_ptr(err); }
 uint64_t current_wait_limit_ns() { return wait_limit_ns(); }
 
 int current_stall_cta() { return g_stall_cta.load(std::memory_order_relaxed); }
+
+bool make_context_current() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+}
 
 void* tensor_map_encoder() { return reinterpret_cast<void*>(encode_fn()); }
 
@@ -557,9 +565,106 @@ smqa_status indexer_impl(const void* q, const float* w, const void* k, const int
   return SMQA_OK;
 }
 
+// Shape and parameters of the scores and their gradients (batch-major layouts).
+smqa_status scores_shape(const smqa_shape& s) {
+  if (s.B <= 0 || s.S <= 0 || s.S_kv <= 0 || s.H <= 0 || s.D <= 0 || s.topk <= 0) {
+    std::snprintf(g_last_error, sizeof g_last_error, "non-positive size in shape");
+    return SMQA_ERR_INVALID_ARG;
+  }
+  const int64_t lim = int64_t{1} << 31;
+  if (s.H > 128 || (s.D != 64 && s.D != 128) || static_cast<int64_t>(s.B) * s.S_kv >= lim ||
+      static_cast<int64_t>(s.B) * s.S * s.H >= lim || s.topk > lim - 128) {
+    std::snprintf(g_last_error, sizeof g_last_error,
+                  "unsupported indexer shape (need 1<=H<=128, D in {64,128}, B*S*H, B*S_kv, topk < 2^31)");
+    return SMQA_ERR_UNSUPPORTED;
+  }
+  return SMQA_OK;
+}
+smqa::IdxParams scores_params(const float* w, const void* k, const int32_t* idx, const float* g, const smqa_shape& s) {
+  smqa::IdxParams p{};
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.idx = idx;
+  p.g = g;
+  p.w = w;
+  p.B = s.B;
+  p.S = s.S;
+  p.S_kv = s.S_kv;
+  p.H = s.H;
+  p.D = s.D;
+  p.topk = s.topk;
+  p.q_tok_rows = s.H;
+  p.q_b_rows = static_cast<int64_t>(s.S) * s.H;
+  p.k_row_stride = s.D;
+  p.k_b_stride = static_cast<int64_t>(s.S_kv) * s.D;
+  p.limit_ns = wait_limit_ns();
+  p.stall_cta = g_stall_cta.load(std::memory_order_relaxed);
+  return p;
+}
+
 }  // namespace
 
 extern "C" {
+
+smqa_status smqa_indexer_scores(const void* index_q, const float* weights, const void* index_k,
+                                const int32_t* topk_indices, smqa_shape s, float* scores, cudaStream_t stream) {
+  const smqa_status sc = scores_shape(s);
+  if (sc != SMQA_OK) return sc;
+  if (!index_q || !weights || !index_k || !topk_indices || !scores || !aligned(index_q, 16) || !aligned(index_k, 16) ||
+      !aligned(weights, 4) || !aligned(topk_indices, 4) || !aligned(scores, 4)) {
+    std::snprintf(g_last_error, sizeof g_last_error, "null or misaligned pointer");
+    return SMQA_ERR_INVALID_ARG;
+  }
+  smqa::IdxParams p = scores_params(weights, index_k, topk_indices, nullptr, s);
+  cudaError_t e;
+  p.status = status_ptr(&e);
+  if (!p.status) return cuda_fail(e, "status word");
+  e = smqa::launch_indexer_scores(p, static_cast<const __nv_bfloat16*>(index_q), scores, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "indexer scores launch");
+  return SMQA_OK;
+}
+
+size_t smqa_indexer_scores_bwd_workspace_bytes(smqa_shape s, unsigned flags) {
+  if (scores_shape(s) != SMQA_OK || (flags & SMQA_FLAG_RETURN_DKV_FP32)) return 0;
+  return static_cast<size_t>(s.B) * s.S_kv * s.D * 4;
+}
+
+smqa_status smqa_indexer_scores_bwd(const void* index_q, const float* weights, const void* index_k,
+                                    const int32_t* topk_indices, const float* grad_scores, smqa_shape s,
+                                    void* dq, float* dweights, void* dindex_k, void* workspace,
+                                    size_t workspace_bytes, unsigned flags, cudaStream_t stream) {
+  const smqa_status sc = scores_shape(s);
+  if (sc != SMQA_OK) return sc;
+  const bool fp32 = flags & SMQA_FLAG_RETURN_DKV_FP32;
+  const size_t need = smqa_indexer_scores_bwd_workspace_bytes(s, flags);
+  if ((flags & ~SMQA_FLAG_RETURN_DKV_FP32) || !index_q || !weights || !index_k || !topk_indices || !grad_scores || !dq ||
+      !dweights || !dindex_k || (need != 0 && !workspace) || !aligned(index_q, 16) || !aligned(index_k, 16) ||
+      !aligned(dq, 16) || !aligned(dindex_k, 16) || !aligned(weights, 4) || !aligned(topk_indices, 4) ||
+      !aligned(grad_scores, 4) || !aligned(dweights, 4) || !aligned(workspace, 256)) {
+    std::snprintf(g_last_error, sizeof g_last_error, "null or misaligned pointer, or bad flags");
+    return SMQA_ERR_INVALID_ARG;
+  }
+  if (workspace_bytes < need) {
+    std::snprintf(g_last_error, sizeof g_last_error, "workspace too small (%zu < %zu bytes)", workspace_bytes, need);
+    return SMQA_ERR_UNSUPPORTED;
+  }
+  smqa::IdxParams p = scores_params(weights, index_k, topk_indices, grad_scores, s);
+  cudaError_t e;
+  p.status = status_ptr(&e);
+  if (!p.status) return cuda_fail(e, "status word");
+  const uint64_t rows = static_cast<uint64_t>(s.B) * s.S * s.H;
+  CUtensorMap tq, tdq;
+  if (!encode_bf16_2d(&tq, index_q, s.D, rows, 64, static_cast<uint32_t>(s.H)) ||
+      !encode_bf16_2d(&tdq, dq, s.D, rows, 64, static_cast<uint32_t>(s.H)))
+    return SMQA_ERR_CUDA;
+  float* acc = static_cast<float*>(fp32 ? dindex_k : workspace);
+  const int64_t elems = static_cast<int64_t>(s.B) * s.S_kv * s.D;
+  e = cudaMemsetAsync(acc, 0, static_cast<size_t>(elems) * 4, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "indexer scores bwd");
+  e = smqa::launch_indexer_scores_bwd(tq, tdq, p, dweights, acc, stream);
+  if (e == cudaSuccess && !fp32) e = smqa::launch_bwd_postprocess(acc, static_cast<__nv_bfloat16*>(dindex_k), elems, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "indexer scores bwd launch");
+  return SMQA_OK;
+}
 
 smqa_status smqa_indexer_bwd(const void* index_q, const float* weights, const void* index_k,
                              const int32_t* topk_indices, const float* grad_scores,

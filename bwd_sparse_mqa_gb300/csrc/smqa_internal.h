@@ -166,6 +166,13 @@ cudaError_t launch_bwd_main(const CUtensorMap& tm_q, const CUtensorMap& tm_do,
                             cudaStream_t stream);
 cudaError_t launch_indexer_bwd(const CUtensorMap& tm_q, const CUtensorMap& tm_dq,
                                const IdxParams& p, cudaStream_t stream);
+// The indexer's scores (q [B,S,H,D], idx [B,S,topk]; p.g unused), and their gradients: dq
+// through tm_dq, dw [B,S,H], and dk [B,S_kv,D] added into fp32 (zeroed beforehand).
+cudaError_t launch_indexer_scores(const IdxParams& p, const __nv_bfloat16* q, float* scores,
+                                  cudaStream_t stream);
+cudaError_t launch_indexer_scores_bwd(const CUtensorMap& tm_q, const CUtensorMap& tm_dq,
+                                      const IdxParams& p, float* dw, float* dk,
+                                      cudaStream_t stream);
 cudaError_t launch_bwd_preprocess(const __nv_bfloat16* o, const __nv_bfloat16* dout,
                                   float* delta, float* dkv_acc, int64_t rows, int D,
                                   int64_t acc_elems, cudaStream_t stream);
@@ -210,6 +217,9 @@ uint64_t current_wait_limit_ns();
 int current_stall_cta();
 // cuTensorMapEncodeTiled of the driver (a PFN_cuTensorMapEncodeTiled_v12000; null if it lacks it).
 void* tensor_map_encoder();
+// Makes the current device's context this thread's (a thread that has made no CUDA call yet has
+// none, and the encoder above, a driver call, then refuses with CUDA_ERROR_INVALID_CONTEXT).
+bool make_context_current();
 // The entry points' shape check (records the reason on failure).
 smqa_status validate_shape(const smqa_shape& s);
 // sm_scale as the entry points interpret it (<= 0 or NaN selects D^-1/2).

@@ -1084,10 +1084,13 @@ bool encode_keys(CUtensorMap* m, const void* ptr, bool codes, int D, uint64_t ro
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), rows};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * (codes ? 1 : 2)};
   const cuuint32_t box[2] = {codes ? static_cast<cuuint32_t>(D) : 64u, box_rows}, estr[2] = {1, 1};
-  const CUresult r = fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims,
-                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        codes && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  auto encode = [&] {
+    return fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, codes && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT && make_context_current()) r = encode();
   if (r != CUDA_SUCCESS) set_last_error("cuTensorMapEncodeTiled failed");
   return r == CUDA_SUCCESS;
 }

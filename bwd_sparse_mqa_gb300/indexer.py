@@ -1,4 +1,4 @@
-"""The lightning indexer's selection: which positions sparse MQA attends to.
+"""The lightning indexer: which positions sparse MQA attends to, and its training.
 
 A token's score of a key row is sum_h weights[h] ReLU(index_q[h] . index_k); the
 blocks with the best rows give the ``topk_idxs`` of sparse_mqa (contiguous keys,
@@ -7,6 +7,7 @@ blocks with the best rows give the ``topk_idxs`` of sparse_mqa (contiguous keys,
 
     idx = indexer_topk(index_q, weights, index_k, topk)
     o, lse = sparse_mqa(q, kv, attn_sink, idx)
+    scores = indexer_scores(index_q, weights, index_k, idx)   # differentiable, -inf where masked
 
 and of a server's step, behind paged_plan,
 
@@ -174,3 +175,105 @@ def paged_indexer_topk(index_q: torch.Tensor, weights: torch.Tensor, k_cache: to
     if check_status:
         _check_device(index_q.device, "smqa_paged_indexer_topk")
     return out
+
+
+def _scores_args(index_q, weights, index_k, topk_indices):
+    """(device, shape) of checked arguments."""
+    try:
+        dev = index_q.get_device()
+        B, S, H, D = index_q.shape
+        S_kv, topk = index_k.shape[1], topk_indices.shape[2]
+        ok = (dev >= 0 and index_q.dtype is index_k.dtype is _BF16 and weights.dtype is _F32
+              and topk_indices.dtype is _I32 and weights.get_device() == index_k.get_device()
+              == topk_indices.get_device() == dev and weights.shape == (B, S, H)
+              and index_k.shape == (B, S_kv, D) and topk_indices.shape == (B, S, topk)
+              and index_q.is_contiguous() and weights.is_contiguous() and index_k.is_contiguous()
+              and topk_indices.is_contiguous())
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _explain("index_q [B,S,H,D], weights [B,S,H], index_k [B,S_kv,D] and topk_indices [B,S,topk] "
+                 "do not have matching shapes", (index_q, "index_q", _BF16, 4),
+                 (weights, "weights", _F32, 3), (index_k, "index_k", _BF16, 3),
+                 (topk_indices, "topk_indices", _I32, 3))
+    return dev, _lib.Shape(B, S, S_kv, H, D, topk)
+
+
+def indexer_scores_fwd(index_q: torch.Tensor, weights: torch.Tensor, index_k: torch.Tensor,
+                       topk_indices: torch.Tensor, check_status: bool = False) -> torch.Tensor:
+    """The indexer's scores at topk_indices (C ABI ``smqa_indexer_scores``):
+    scores[b,s,j] = sum_h weights[b,s,h] ReLU(index_q[b,s,h] . index_k[b,idx[b,s,j]]),
+    -inf where an index lies outside [0,S_kv).
+
+    index_q [B,S,H,D] bf16, weights [B,S,H] fp32, index_k [B,S_kv,D] bf16,
+    topk_indices [B,S,topk] int32; returns scores [B,S,topk] fp32, freshly
+    allocated.  ``check_status`` as in indexer_topk."""
+    dev, shp = _scores_args(index_q, weights, index_k, topk_indices)
+    scores = torch.empty((shp.B, shp.S, shp.topk), dtype=_F32, device=index_q.device)
+    _call("smqa_indexer_scores", dev, _lib.load().smqa_indexer_scores, index_q.data_ptr(),
+          weights.data_ptr(), index_k.data_ptr(), topk_indices.data_ptr(), shp, scores.data_ptr())
+    if check_status:
+        _check_device(index_q.device, "smqa_indexer_scores")
+    return scores
+
+
+def indexer_scores_bwd(index_q: torch.Tensor, weights: torch.Tensor, index_k: torch.Tensor,
+                       topk_indices: torch.Tensor, grad_scores: torch.Tensor,
+                       return_dk_accum_dtype: bool = False,
+                       workspace: Optional[torch.Tensor] = None, check_status: bool = False
+                       ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients of indexer_scores_fwd for grad_scores [B,S,topk] fp32 (C ABI
+    ``smqa_indexer_scores_bwd``): (dq like index_q, dweights [B,S,H] fp32, dindex_k
+    like index_k, or fp32 with ``return_dk_accum_dtype``), freshly allocated.
+    Masked slots' gradients are not looked at.  dindex_k is summed by fp32 atomics:
+    its last bits may change from run to run.  ``workspace`` (uint8 CUDA tensor) is
+    reused when large enough; ``check_status`` as in indexer_topk."""
+    dev, shp = _scores_args(index_q, weights, index_k, topk_indices)
+    _need(grad_scores, "grad_scores", _F32, 3)
+    if grad_scores.shape != topk_indices.shape or grad_scores.get_device() != dev:
+        raise ValueError("grad_scores must be like topk_indices, on the same device")
+    lib = _lib.load()
+    flags = _lib.FLAG_RETURN_DKV_FP32 if return_dk_accum_dtype else 0
+    need = lib.smqa_indexer_scores_bwd_workspace_bytes(shp, flags)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, 1)
+        if workspace.get_device() != dev:
+            raise ValueError("workspace must be on the tensors' device")
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=index_q.device)
+    dq, dw = torch.empty_like(index_q), torch.empty_like(weights)
+    dk = torch.empty_like(index_k, dtype=_F32 if return_dk_accum_dtype else _BF16)
+    _call("smqa_indexer_scores_bwd", dev, lib.smqa_indexer_scores_bwd, index_q.data_ptr(),
+          weights.data_ptr(), index_k.data_ptr(), topk_indices.data_ptr(), grad_scores.data_ptr(),
+          shp, dq.data_ptr(), dw.data_ptr(), dk.data_ptr(), workspace.data_ptr() or None,
+          workspace.numel(), flags)
+    if check_status:
+        _check_device(index_q.device, "smqa_indexer_scores_bwd")
+    return dq, dw, dk
+
+
+class IndexerScoresFunction(torch.autograd.Function):
+    """Autograd around the scores' forward and backward kernels: gradients flow
+    to index_q, weights and index_k."""
+
+    @staticmethod
+    def forward(ctx, index_q, weights, index_k, topk_indices, check_status=False):
+        ctx.save_for_backward(index_q, weights, index_k, topk_indices)
+        ctx.check_status = check_status
+        return indexer_scores_fwd(index_q, weights, index_k, topk_indices, check_status)
+
+    @staticmethod
+    def backward(ctx, grad_scores):
+        index_q, weights, index_k, topk_indices = ctx.saved_tensors
+        dq, dw, dk = indexer_scores_bwd(index_q, weights, index_k, topk_indices,
+                                        grad_scores.to(_F32).contiguous(),
+                                        check_status=ctx.check_status)
+        return dq, dw, dk, None, None
+
+
+def indexer_scores(index_q: torch.Tensor, weights: torch.Tensor, index_k: torch.Tensor,
+                   topk_indices: torch.Tensor, check_status: bool = False) -> torch.Tensor:
+    """Differentiable indexer_scores_fwd: gradients with respect to index_q, weights
+    and index_k.  With ``check_status`` the forward and the backward each
+    synchronize and raise SMQAError if a kernel's bounded wait ran out."""
+    return IndexerScoresFunction.apply(index_q, weights, index_k, topk_indices, check_status)

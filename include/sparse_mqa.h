@@ -356,6 +356,37 @@ smqa_status smqa_batched_indexer_bwd(const void* index_q, const float* weights,
                                      cudaStream_t stream);
 
 /*
+ * The indexer's scores at given positions, for training it (batch-major layouts;
+ * the pages give dq alone, above):
+ *   scores[b,s,j] = sum_h weights[b,s,h] ReLU(<index_q[b,s,h,:], index_k[b,idx[b,s,j],:]>)
+ * and -inf where the index lies outside [0, S_kv).
+ *   index_q      bf16 [B,S,H,D]       weights fp32 [B,S,H]     index_k bf16 [B,S_kv,D]
+ *   topk_indices int32 [B,S,topk]     scores  fp32 [B,S,topk]
+ * 1 <= H <= 128, D in {64, 128}.  Logits and sums are fp32.
+ *
+ * The backward takes grad_scores fp32 [B,S,topk] (masked slots' are not looked
+ * at; a slot listed twice counts twice; the ReLU's slope at 0 is 0) and writes
+ *   dq bf16 [B,S,H,D], dweights fp32 [B,S,H], dindex_k bf16 [B,S_kv,D] (fp32 with
+ *   SMQA_FLAG_RETURN_DKV_FP32)
+ * Logits are fp32 (where one lies within their rounding of 0 the gate may differ
+ * from an exact evaluation); weights * grad_scores enter the tensor core as bf16;
+ * dindex_k is summed by fp32 atomics, whose order is not fixed.
+ *   workspace    256-byte aligned, smqa_indexer_scores_bwd_workspace_bytes(shape,
+ *                flags) bytes (the fp32 sums; 0 with SMQA_FLAG_RETURN_DKV_FP32);
+ *                needs no initialisation; calls whose kernels may overlap must not
+ *                share it
+ */
+smqa_status smqa_indexer_scores(const void* index_q, const float* weights, const void* index_k,
+                                const int32_t* topk_indices, smqa_shape shape, float* scores,
+                                cudaStream_t stream);
+size_t smqa_indexer_scores_bwd_workspace_bytes(smqa_shape shape, unsigned flags);
+smqa_status smqa_indexer_scores_bwd(const void* index_q, const float* weights, const void* index_k,
+                                    const int32_t* topk_indices, const float* grad_scores,
+                                    smqa_shape shape, void* dq, float* dweights, void* dindex_k,
+                                    void* workspace, size_t workspace_bytes, unsigned flags,
+                                    cudaStream_t stream);
+
+/*
  * Serving: an 8-bit paged kv cache, and sparse MQA over it.  (The sparse MQA
  * pages have no counterpart: their interfaces take one contiguous bf16 kv.)
  *
