@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(384, 2)
       tc_fence_after();
       // (The block's rows were written before its L was formed, long before this.)
       if (quarter * 32 < D) {
-        const volatile int* rows = row_of + (i % L::kInfo) * L::kBI;
+        const int4* rows = reinterpret_cast<const int4*>(smem + L::kOffRow) + (i % L::kInfo) * (L::kBI / 4);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float x[32];
@@ -430,11 +430,15 @@ __global__ void __launch_bounds__(384, 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(L::kBarDkFree));
           }
-          const int mine = rows[c * 32 + lane];
+          // (Four rows per load, the same in all lanes: with a shuffle per row the adds of a
+          // warp came one latency apart.)
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const int r = __shfl_sync(0xffffffffu, mine, k);
-            if (r >= 0) red_add_f32(dk0 + static_cast<int64_t>(r) * D, x[k]);
+          for (int k = 0; k < 8; ++k) {
+            const int4 r = rows[8 * c + k];
+            if (r.x >= 0) red_add_f32(dk0 + static_cast<int64_t>(r.x) * D, x[4 * k]);
+            if (r.y >= 0) red_add_f32(dk0 + static_cast<int64_t>(r.y) * D, x[4 * k + 1]);
+            if (r.z >= 0) red_add_f32(dk0 + static_cast<int64_t>(r.z) * D, x[4 * k + 2]);
+            if (r.w >= 0) red_add_f32(dk0 + static_cast<int64_t>(r.w) * D, x[4 * k + 3]);
           }
         }
       } else {
