@@ -218,7 +218,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w < warp) before += warp_sum[w];
       total += warp_sum[w];
     }
-    const int64_t begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+    // Equal ranges, the first total mod grid of them one tile longer.
+    const int64_t parts = gridDim.x, part = blockIdx.x;
+    const int64_t each = (total >> 32) != 0 ? total / parts : static_cast<uint32_t>(total) / static_cast<uint32_t>(parts);
+    const int64_t extra = total - each * parts;
+    const int64_t begin = each * part + min(part, extra), end = begin + each + (part < extra ? 1 : 0);
     if (begin < end && before <= begin && begin < before + mine) {
       int64_t at = before, u = u0, n;
       while (at + (n = unit_tiles<kPaged>(p, p.unit0 + u, kGroup)) <= begin) {
