@@ -94,6 +94,13 @@ __device__ __forceinline__ double value64_of(long long k) {
          value_of(static_cast<int32_t>(static_cast<uint32_t>(k) ^ 0x80000000u));
 }
 
+// (By name where a function of its own needs it: through a pointer that it was given, the
+// compiler could not tell that this is shared memory.)
+__device__ __forceinline__ uint8_t* dynamic_smem() {
+  extern __shared__ __align__(16) uint8_t select_smem[];
+  return select_smem;
+}
+
 // What a CTA knows of its token.
 template <int D, bool kPaged, int NT>
 struct Token {
@@ -397,14 +404,17 @@ struct Token {
   }
 };
 
-// val[i] = the exact score of block cand[i] (of cand[at[i]], if `at`), as an ordered
+// val[i] = the exact score of block idx[open[i]] (kOpen) or idx[i], as an ordered
 // integer.  (A function of its own: one copy of the code.)
-template <int D, bool kPaged, int NT>
-__device__ __noinline__ void exact_scores(Token<D, kPaged, NT> tk, const int* cand, const int* at, int m, long long* val,
-                                          float floor) {
+template <int D, bool kPaged, int NT, bool kOpen>
+__device__ __noinline__ void exact_scores(Token<D, kPaged, NT> tk, int m, float floor) {
+  using L = SelLayout<D, NT>;
+  tk.smem = dynamic_smem();
+  const int *idx = tk.template at<int>(L::kOffIdx), *open = tk.template at<int>(L::kOffOpen);
+  long long* val = tk.template at<long long>(L::kOffVal);
   for (int i = tk.tid; i < m; i += NT) val[i] = key64_of(Pair{-INFINITY, 0.f});
   __syncthreads();
-  tk.template score<true>([&](int i) { return cand[at ? at[i] : i]; }, m, floor, [&](int i, Pair x) {
+  tk.template score<true>([&](int i) { return idx[kOpen ? open[i] : i]; }, m, floor, [&](int i, Pair x) {
     if (x.hi == x.hi) atomicMax(val + i, key64_of(fabsf(x.hi) < INFINITY ? x : Pair{x.hi, 0.f}));
   });
 }
@@ -532,6 +542,7 @@ __device__ __forceinline__ int nth_of(Token<D, kPaged, NT>& tk, int* keys, int m
 template <int D, bool kPaged, int NT>
 __device__ __noinline__ void settle(Token<D, kPaged, NT> tk, int m, int r) {
   using L = SelLayout<D, NT>;
+  tk.smem = dynamic_smem();
   int *misc = tk.template at<int>(L::kOffMisc), *idx = tk.template at<int>(L::kOffIdx), *open = tk.template at<int>(L::kOffOpen);
   int* mark = tk.template at<int>(L::kOffMark);
   long long* val = tk.template at<long long>(L::kOffVal);
@@ -558,7 +569,7 @@ __device__ __noinline__ void settle(Token<D, kPaged, NT> tk, int m, int r) {
     for (int i = tk.tid; i < m; i += NT) mark[open[i]] = 1;
   } else {
     // (Their best rows' plain scores are at - 2 e_plain or more.)
-    exact_scores(tk, idx, open, m, val, at - 4.f * tk.e_plain);
+    exact_scores<D, kPaged, NT, true>(tk, m, at - 4.f * tk.e_plain);
     for (int i = tk.tid; i < m; i += NT) {
       const long long x = val[i];
       const int c = idx[open[i]];
@@ -684,7 +695,7 @@ __device__ __forceinline__ Cut any_cut(Token<D, kPaged, NT>& tk, const Keys<D, k
       }
       __syncthreads();
       const int some = misc[3];
-      exact_scores(tk, idx, nullptr, some, val, -INFINITY);
+      exact_scores<D, kPaged, NT, false>(tk, some, -INFINITY);
       for (int i = tk.tid; i < some; i += NT) keys.store(idx[i], key_of(static_cast<float>(value64_of(val[i]) - base)));
     }
   }
@@ -739,6 +750,7 @@ __device__ __forceinline__ void fill_rest(Token<D, kPaged, NT>& tk, int32_t* out
 // again.
 template <int D, bool kPaged, int NT>
 __device__ __noinline__ void choose_any(Token<D, kPaged, NT> tk) {
+  tk.smem = dynamic_smem();
   const TopkParams& p = tk.p;
   const Keys<D, kPaged, NT> keys(tk);
   const Cut cut = any_cut(tk, keys, p.topk >> p.block_shift);
@@ -786,7 +798,8 @@ __device__ __noinline__ void choose_any(Token<D, kPaged, NT> tk) {
 // next to the bin of number `want` is looked at one by one, and its bin becomes all
 // ones or 0.  False where that will not do (scores that are not numbers, a border in the
 // ends, many ties).
-template <int D, bool kPaged, int NT>
+// kOne: a candidate has one entry in the row.
+template <int D, bool kPaged, int NT, bool kOne>
 __device__ __forceinline__ bool choose_ordinary(Token<D, kPaged, NT>& tk) {
   using L = SelLayout<D, NT>;
   const TopkParams& p = tk.p;
@@ -795,25 +808,28 @@ __device__ __forceinline__ bool choose_ordinary(Token<D, kPaged, NT>& tk) {
   int *more = tk.template at<int>(L::kOffMore), *mark = tk.template at<int>(L::kOffMark), *list = tk.template at<int>(L::kOffVal);
   uint32_t* bins = tk.template at<uint32_t>(L::kOffBins);  // two candidates a word
   const int want = p.topk >> p.block_shift, words = keys.steps / 2, w0 = keys.c0 / 2 + tk.lane;
-  // A lane's candidates c, c + 1 of word i: c = c0 + 64 i + 2 lane.
+  // A lane's candidates c, c + 1 of word i: c = c0 + 64 i + 2 lane.  Loads without a
+  // branch, and nothing made of them before the next are on their way; what lies behind the
+  // last candidate (a row is padded to whole words of four) is seen to where it is used.
   constexpr int kAhead = 8;
-  int2 key[kAhead];
-  auto ask = [&](int i) {                                // (a row is padded to whole words of four)
+  uint2 key[kAhead];
+  const uint2* pairs = reinterpret_cast<const uint2*>(keys.row);
+  const int last_pair = (keys.nb - 1) / 2;
+  auto ask = [&](int i) {
     const int c = keys.c0 + i * 64 + 2 * tk.lane;
-    if (keys.per == 1) {
-      const uint2 v = load(reinterpret_cast<const uint2*>(keys.row) + min(c, keys.nb - 1) / 2);
-      return make_int2(c < keys.nb ? static_cast<int>(v.x) : kKeyNever, c + 1 < keys.nb ? static_cast<int>(v.y) : kKeyNever);
-    }
-    return make_int2(keys.fetch(c), keys.fetch(c + 1));
+    if constexpr (kOne) return load(pairs + min(c / 2, last_pair));
+    return make_uint2(keys.fetch(c), keys.fetch(c + 1));
   };
+  auto of = [&](uint32_t k, int c) { return c < keys.nb ? static_cast<int>(k) : kKeyNever; };
   tk.start_queries();
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) key[i] = i < words ? ask(i) : make_int2(kKeyNever, kKeyNever);
+  for (int i = 0; i < kAhead; ++i) key[i] = ask(i);
   for (int i = tk.tid; i < kBins / 4; i += NT) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
   if (tk.tid < L::kWarps) more[tk.tid] = 0;
   tk.bounds();
-  const bool fin = key[0].x > kKeyNegInf && key[0].x < kKeyInf;
-  int ends[2] = {fin ? key[0].x : INT32_MAX, fin ? key[0].x : INT32_MIN};
+  const int first = of(key[0].x, keys.c0 + 2 * tk.lane);
+  const bool fin = first > kKeyNegInf && first < kKeyInf;
+  int ends[2] = {fin ? first : INT32_MAX, fin ? first : INT32_MIN};
   tk.template reduce<2, true>(ends);
   if (ends[0] >= ends[1]) return false;
   const float a = value_of(ends[0]), b = value_of(ends[1]), range = b - a;
@@ -827,8 +843,8 @@ __device__ __forceinline__ bool choose_ordinary(Token<D, kPaged, NT>& tk) {
     for (int i = 0; i < kAhead; ++i) {
       if (i0 + i >= words) break;
       const int c = keys.c0 + (i0 + i) * 64 + 2 * tk.lane;
-      const int x = bin_of(key[i].x), y = bin_of(key[i].y);
-      if (i0 + i + kAhead < words) key[i] = ask(i0 + i + kAhead);
+      const int x = bin_of(of(key[i].x, c)), y = bin_of(of(key[i].y, c + 1));
+      key[i] = ask(i0 + i + kAhead);
       if (c < keys.nb) atomicAdd(hist + x, 1);
       if (c + 1 < keys.nb) atomicAdd(hist + y, 1);
       bins[w0 + (i0 + i) * 32] = static_cast<uint32_t>(x) | (static_cast<uint32_t>(y) << 16);
@@ -846,13 +862,21 @@ __device__ __forceinline__ bool choose_ordinary(Token<D, kPaged, NT>& tk) {
   const int near = __reduce_add_sync(0xffffffffu, here);
   if (near > kList - 3) return false;
   int sure = 0;
-#pragma unroll 8
-  for (int i = 0; i < words; ++i) {
-    const uint32_t v = bins[w0 + i * 32];
-    const int x = v & 0xffff, y = v >> 16, c = keys.c0 + i * 64 + 2 * tk.lane;
-    sure += (x > bh) + (y > bh);
-    if (x >= bl && x <= bh) list[kList + atomicAdd(misc + 3, 1)] = c;
-    if (y >= bl && y <= bh) list[kList + atomicAdd(misc + 3, 1)] = c + 1;
+  for (int i0 = 0; i0 < words; i0 += kAhead) {
+    uint32_t v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) v[i] = i0 + i < words ? bins[w0 + (i0 + i) * 32] : 0;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int x = v[i] & 0xffff, y = v[i] >> 16;
+      sure += (x > bh) + (y > bh);
+      const bool nx = x >= bl && x <= bh, ny = y >= bl && y <= bh;
+      if (nx || ny) {
+        const int c = keys.c0 + (i0 + i) * 64 + 2 * tk.lane;
+        if (nx) list[kList + atomicAdd(misc + 3, 1)] = c;
+        if (ny) list[kList + atomicAdd(misc + 3, 1)] = c + 1;
+      }
+    }
   }
   __syncthreads();
   for (int i = tk.tid; i < near; i += NT) list[i] = keys.fetch(list[kList + i]);
@@ -934,7 +958,7 @@ __device__ __forceinline__ bool choose_ordinary(Token<D, kPaged, NT>& tk) {
 template <int D, bool kPaged, int NT>
 __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : 3) smqa_topk_select_kernel(const __grid_constant__ TopkParams p) {
   using L = SelLayout<D, NT>;
-  extern __shared__ __align__(16) uint8_t smem[];
+  uint8_t* smem = dynamic_smem();
   const int tid = threadIdx.x;
   const int64_t t = p.tok0 + blockIdx.x;
   grid_dependency_wait();
@@ -973,7 +997,7 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : 3) smqa_topk_select_kerne
     return;
   }
   if ((n + (1 << p.block_shift) - 1) >> p.block_shift <= L::kCap) {
-    if (choose_ordinary(tk)) return;
+    if (p.block_shift <= 5 ? choose_ordinary<D, kPaged, NT, true>(tk) : choose_ordinary<D, kPaged, NT, false>(tk)) return;
   } else {
     tk.start_queries();
     tk.bounds();
