@@ -39,7 +39,7 @@ constexpr int32_t kKeyNegInf = -kKeyInf - 1;            // (key_of(-infinity): t
 template <int D, int NT>
 struct SelLayout {
   static constexpr int kWarps = NT / 32;
-  static constexpr int kCap = NT == 1024 ? 65536 : 8192;
+  static constexpr int kCap = NT == 1024 ? 65536 : 16384;
   static constexpr int kBatch = NT == 1024 ? 32 : 16;    // key rows that are scored again together, at most
   static constexpr int kPitch = D * 2 + 16;              // of a staged key row, bf16 (eight rows: other banks)
   static constexpr uint32_t kPartBytes = NT == 1024 ? 16384 : 8192;

@@ -19,10 +19,14 @@
 // buffers); key tiles come by TMA through a ring of 128-byte pieces.  Tokens that
 // see no more rows than they choose need no scores and are left out.
 //
-// 512 threads: warps 0-7 epilogue (two warpgroups, alternate tiles and
-// accumulators), 8 walks through the groups and issues the key tiles' copies, 9
-// feeds the tensor core, 12-15 bring the queries and weights of the next group and
-// bound the key rows' lengths (which the choice's error bound needs).
+// 512 threads: warps 0-7 epilogue, 8 walks through the groups and issues the key
+// tiles' copies, 9 feeds the tensor core, 12-15 bring the queries and weights of the
+// next group and bound the key rows' lengths (which the choice's error bound needs).
+// An epilogue thread keeps the weights of its 128 columns in registers for a whole
+// group: read from shared memory for every tile, 4 bytes a lane, they took as long as
+// the tensor core (1024 clocks a tile of 256 columns) from the bandwidth that it needs
+// for its operands.  A wide tile's columns are shared by the two warpgroups, narrow
+// tiles (up to 128 columns) go to them in turn.
 #include <cuda_runtime.h>
 
 #include "smqa_topk.cuh"
@@ -34,6 +38,11 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kHelpWarp0 = 12;
 constexpr int kCols = 256;                               // accumulator columns
+constexpr int kMine = 128;                               // columns of an epilogue warpgroup
+// Registers of the epilogue's warpgroups and of the other two: their sum is what the
+// block is launched with.
+constexpr int kEpilogueRegs = 192, kOtherRegs = 64;
+static_assert(2 * kEpilogueRegs + 2 * kOtherRegs <= 512 && kLoadWarp == 8, "registers of the launch, roles by warpgroup");
 constexpr int kMaxGroup = 16;                            // tokens of a group
 
 // What the CTA does for one group (or the part of one that its range holds).
@@ -184,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(L::kBarAccFull + i), 1);
-      mbar_init(bar(L::kBarAccEmpty + i), 4);
+      mbar_init(bar(L::kBarAccEmpty + i), 8);
       mbar_init(bar(L::kBarWork + i), 1);
       mbar_init(bar(L::kBarQFull + i), 4);
       mbar_init(bar(L::kBarQEmpty + i), 1 + 8 + 4);      // tensor core, epilogue, helpers
@@ -242,7 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (count_all == 0 && (kPaged || warp < kHelpWarp0)) {
     // nothing to do
-  } else if (warp == kLoadWarp) {
+  } else if (warp >= kLoadWarp && warp < kHelpWarp0) {
+    reg_dealloc<kOtherRegs>();                           // (the warpgroup's other warps have no role)
+    if (warp == kLoadWarp) {
     // ------------------------------------------------------------ walk and copy
     int64_t u = start[0], skip = start[1], left = count_all;
     int part = 0, e = 0, tile_no = 0;                    // pieces and tiles so far
@@ -327,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = max(0, e - L::kStages); i < e; ++i)
         mbar_wait_drain(bar(L::kBarKFull + i % L::kStages), (i / L::kStages) & 1);
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
     const uint64_t d_k = smem_desc(base + L::kOffK, 16u, L::kAtom, L::kSwizzle);
     const uint64_t d_q = smem_desc(base + L::kOffQ, 16u, L::kAtom, L::kSwizzle);
@@ -380,7 +391,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit_elect(bar(L::kBarDrain));
     mbar_wait_drain(bar(L::kBarDrain), 0);
     __syncwarp();
+    }
   } else if (warp >= kHelpWarp0) {
+    reg_dealloc<kOtherRegs>();
     // ------------------------------------------------------------ queries, weights, lengths
     const int ht = tid - 32 * kHelpWarp0, hw = warp - kHelpWarp0;  // thread of 128
     float* norm_of = reinterpret_cast<float*>(smem + L::kOffNorm);
@@ -535,12 +548,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane == 0) mbar_arrive(bar(L::kBarQEmpty + qb));
     }
-  } else if (warp < kLoadWarp) {
+  } else {
+    reg_alloc<kEpilogueRegs>();
     // ------------------------------------------------------------ epilogue
-    const int group = warp >> 2, quarter = warp & 3;     // group: the tiles and the accumulator it takes
+    const int group = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const int my = quarter * 32 + lane;                  // this thread's row of a tile
     const int eshift = entry_shift(p.block_shift);
+    const int64_t ld = p.ld;
+    const int recent = p.recent, page_shift = p.page_shift;
     bool ok = *abort_flag == 0;
     int tile_no = 0;
     for (int seg = 0; ok; ++seg) {
@@ -552,54 +568,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ntiles == 0) break;
       ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQFull + qb), (seg >> 1) & 1, ctl));
       if (!ok) break;
-      int32_t* out = p.rows + (wk.tok - p.tok0) * p.ld;
-      const float* ws = reinterpret_cast<const float*>(smem + L::kOffW) + qb * kCols;
+      const bool wide = ntok * Hp > kMine;
+      const int col0 = wide ? group * kMine : 0;
+      constexpr int kTok = kMine / Hp;                   // tokens of its columns
+      const int tok0 = col0 / Hp;
+      float w[kMine];
+      const float4* ws = reinterpret_cast<const float4*>(smem + L::kOffW + (qb * kCols + col0) * 4);
+#pragma unroll
+      for (int c = 0; c < kMine / 4; ++c) {
+        const float4 v = ws[c];
+        w[4 * c] = v.x;
+        w[4 * c + 1] = v.y;
+        w[4 * c + 2] = v.z;
+        w[4 * c + 3] = v.w;
+      }
+      int seen[kTok];                                    // rows that its tokens see
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) seen[i] = tok0 + i < ntok ? wk.n[tok0 + i] : 0;
+      int32_t* out = p.rows + (wk.tok + tok0 - p.tok0) * ld;
       for (int i = 0; ok && i < ntiles; ++i, ++tile_no) {
-        if ((tile_no & 1) != group) continue;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarAccFull + group), (tile_no >> 1) & 1, ctl));
+        const int acc = tile_no & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarAccFull + acc), (tile_no >> 1) & 1, ctl));
         if (!ok) break;
-        tc_fence_after();
-        const int j = (tile0 + i) * kTile + my;
-        float scale = 1.f;
-        if constexpr (kPaged)
-          scale = reinterpret_cast<const float*>(smem + L::kOffMeta)[(tile_no % L::kMeta) * 8 + (my >> p.page_shift)];
-        const uint32_t t_acc = tmem + lanes + static_cast<uint32_t>(group) * kCols;
-        // A token's score of this row, written as its block's.
-        auto put = [&](int tok, float s) {
-          const int n = wk.n[tok];
-          if (j - lane >= n) return;                     // (the same for the whole warp)
-          if constexpr (kPaged) s *= scale;
-          int32_t key = key_of(s);
-          if (j >= n - p.recent) key = kKeyAlways;
-          if (j >= n || (kPaged && scale < 0.f)) key = kKeyNever;
-          for (int off = 1; off < (1 << eshift); off <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, off));
-          if ((lane & ((1 << eshift) - 1)) == 0 && j < n)
-            out[static_cast<int64_t>(tok) * p.ld + (j >> eshift)] = key;
-        };
-        constexpr int kUnits = kCols / 64;
-        float2 a0, a1;
+        if (wide || acc == group) {
+          tc_fence_after();
+          const int j = (tile0 + i) * kTile + my;
+          float scale = 1.f;
+          if constexpr (kPaged) scale = reinterpret_cast<const float*>(smem + L::kOffMeta)[(tile_no % L::kMeta) * 8 + (my >> page_shift)];
+          // A token's score of this row, written as its block's.
+          auto put = [&](int tok, float s) {
+            const int n = seen[tok];
+            if (j - lane >= n) return;                   // (the same for the whole warp)
+            if constexpr (kPaged) s *= scale;
+            int32_t key = key_of(s);
+            if (j >= n - recent) key = kKeyAlways;
+            if (j >= n || (kPaged && scale < 0.f)) key = kKeyNever;
+            for (int off = 1; off < (1 << eshift); off <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, off));
+            if ((lane & ((1 << eshift) - 1)) == 0 && j < n) out[tok * ld + (j >> eshift)] = key;
+          };
+          const uint32_t t_acc = tmem + lanes + static_cast<uint32_t>(acc) * kCols + static_cast<uint32_t>(col0);
+          float2 a0 = {}, a1 = {};
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {               // 64 columns: a token or half of one, or several
-          if (u * 64 >= ntok * Hp) break;
-          float x[64];
-          tmem_ld32x2(t_acc + u * 64, t_acc + u * 64 + 32, *reinterpret_cast<float(*)[32]>(x),
-                      *reinterpret_cast<float(*)[32]>(x + 32));
-          const float4* w4 = reinterpret_cast<const float4*>(ws + u * 64);
+          for (int u = 0; u < kMine / 32; ++u) {
+            // (Columns behind the last token's are of no token; the last read frees the
+            // accumulator.)
+            if (col0 + u * 32 >= ntok * Hp) break;
+            float x[32];
+            tmem_ld32(t_acc + u * 32, x);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            if ((u * 64 + 4 * c) % Hp == 0) a0 = a1 = make_float2(0.f, 0.f);
-            const float4 wv = w4[c];
-            a0 = fma2(make_float2(wv.x, wv.y), make_float2(relu(x[4 * c]), relu(x[4 * c + 1])), a0);
-            a1 = fma2(make_float2(wv.z, wv.w), make_float2(relu(x[4 * c + 2]), relu(x[4 * c + 3])), a1);
-            if ((u * 64 + 4 * c + 4) % Hp == 0) {
-              const int tok = (u * 64 + 4 * c) / Hp;
-              if (tok < ntok) put(tok, (a0.x + a0.y) + (a1.x + a1.y));
+            for (int c = 0; c < 8; ++c) {
+              const int at = u * 32 + 4 * c;
+              if (at % Hp == 0) a0 = a1 = make_float2(0.f, 0.f);
+              a0 = fma2(make_float2(w[at], w[at + 1]), make_float2(relu(x[4 * c]), relu(x[4 * c + 1])), a0);
+              a1 = fma2(make_float2(w[at + 2], w[at + 3]), make_float2(relu(x[4 * c + 2]), relu(x[4 * c + 3])), a1);
+              if ((at + 4) % Hp == 0) put(at / Hp, (a0.x + a0.y) + (a1.x + a1.y));
             }
           }
+          tc_fence_before();
         }
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kBarAccEmpty + group));
+        if (lane == 0) mbar_arrive(bar(L::kBarAccEmpty + acc));
       }
       if (lane == 0) mbar_arrive(bar(L::kBarQEmpty + qb));
     }
