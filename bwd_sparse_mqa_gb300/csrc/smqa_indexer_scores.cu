@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(288, 2) smqa_indexer_scores_kernel(const IdxPa
       const bool ok_row = static_cast<unsigned>(r) < static_cast<unsigned>(p.S_kv);
       const unsigned mask = __ballot_sync(0xffffffffu, ok_row);
       if (i >= 2) {
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(L::kBarEmpty + st), ((i >> 1) - 1) & 1, ctl))) break;
+        if (!__all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarEmpty + st), ((i >> 1) - 1) & 1, ctl))) break;
       } else if (*abort_flag) {
         break;
       }
@@ -141,11 +141,11 @@ __global__ void __launch_bounds__(288, 2) smqa_indexer_scores_kernel(const IdxPa
       const uint32_t idesc = (idesc_bf16_f32(128, 16, false, false) & ~(0x3fu << 17)) | (static_cast<uint32_t>(heads >> 3) << 17);
       const uint64_t d_q = smem_desc(base + L::kOffQ, 16u, 1024u, kSwizzle128B);
       const uint64_t d_k = smem_desc(base + L::kOffK, 16u, 1024u, kSwizzle128B);
-      bool ok = mbar_wait(bar(L::kBarQ), 0, ctl);
+      bool ok = mbar_wait_soon(bar(L::kBarQ), 0, ctl);
       for (int i = 0; ok && i < nblk; ++i) {
         const int st = i & 1;
-        ok = (i < 2 || mbar_wait(bar(L::kBarAccEmpty + st), ((i >> 1) - 1) & 1, ctl)) &&
-             mbar_wait(bar(L::kBarFull + st), (i >> 1) & 1, ctl);
+        ok = (i < 2 || mbar_wait_soon(bar(L::kBarAccEmpty + st), ((i >> 1) - 1) & 1, ctl)) &&
+             mbar_wait_soon(bar(L::kBarFull + st), (i >> 1) & 1, ctl);
         if (!ok) break;
         fence_proxy_async_smem();                        // rows written by cp.async -> tensor core
         tc_fence_after();
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(288, 2) smqa_indexer_scores_kernel(const IdxPa
     for (int i = 0; ok && i < nblk; ++i) {
       const int st = i & 1, j = i * L::kBI + tid;
       const int r = j < p.topk ? __ldg(idx_row + j) : -1;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarAccFull + st), (i >> 1) & 1, ctl));
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarAccFull + st), (i >> 1) & 1, ctl));
       if (!ok) break;
       tc_fence_after();
       float2 a0 = {}, a1 = {};
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(384, 2)
       const float gj = there ? __ldg(g_row + j) : 0.f;
       const unsigned mask = __ballot_sync(0xffffffffu, there);
       if (i >= L::kStages) {
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(L::kBarKvEmpty + st), ((i / L::kStages) - 1) & 1, ctl))) break;
+        if (!__all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarKvEmpty + st), ((i / L::kStages) - 1) & 1, ctl))) break;
       } else if (*abort_flag) {
         break;
       }
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(384, 2)
       // Oldest work first: the gradients of block n2 once its gate operand is written and the
       // dk before has been read; L of block n1 once its rows are there and the L before has
       // been read.
-      bool ok = mbar_wait(bar(L::kBarQ), 0, ctl);
+      bool ok = mbar_wait_soon(bar(L::kBarQ), 0, ctl);
       int n1 = 0, n2 = 0;
       PollState ps = poll_start();
       uint32_t spins = 0;
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(384, 2)
     float* dk0 = dk + b * p.S_kv * static_cast<int64_t>(D) + d;
     bool ok = *abort_flag == 0;
     for (int i = 0; ok && i < nblk; ++i) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarDkFull), i & 1, ctl));
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarDkFull), i & 1, ctl));
       if (!ok) break;
       tc_fence_after();
       // (The block's rows were written before its L was formed, long before this.)
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(384, 2)
     float2 s0 = {}, s1 = {};
     bool ok = *abort_flag == 0;
     for (int i = 0; ok && i < nblk; ++i) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarLFull), i & 1, ctl));
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarLFull), i & 1, ctl));
       if (!ok) break;
       tc_fence_after();
       float x[64];
@@ -464,8 +464,8 @@ __global__ void __launch_bounds__(384, 2)
       tc_fence_before();
       mbar_arrive(bar(L::kBarLFree));
       // (This wait has completed, as the block's L needed its rows; it orders the reads.)
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarKvFull + i % L::kStages), (i / L::kStages) & 1, ctl));
-      if (ok && i > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarGFree), (i - 1) & 1, ctl));
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarKvFull + i % L::kStages), (i / L::kStages) & 1, ctl));
+      if (ok && i > 0) ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarGFree), (i - 1) & 1, ctl));
       if (!ok) break;
       const float4* gq = reinterpret_cast<const float4*>(smem + L::kOffG) + (i % L::kInfo) * (L::kBI / 4);
 #pragma unroll
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(384, 2)
       fence_proxy_async_smem();
       mbar_arrive(bar(L::kBarGFull));
     }
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarDone), 0, ctl));
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarDone), 0, ctl));
     if (ok) {
       tc_fence_after();
       if (h < p.H) dw[row0 + h] = (s0.x + s0.y) + (s1.x + s1.y);
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(384, 2)
     fence_proxy_async_smem();
     mbar_arrive(bar(L::kBarStaged));
     if (tid == 0) {
-      if (mbar_wait(bar(L::kBarStaged), 0, ctl) && *abort_flag == 0) {
+      if (mbar_wait_soon(bar(L::kBarStaged), 0, ctl) && *abort_flag == 0) {
         for (int cc = 0; cc < L::kChunks; ++cc)
           tma_store_2d(&tm_dq, base + L::kOffKv + static_cast<uint32_t>(cc) * L::kQChunkBytes, cc * 64, static_cast<int>(row0));
         bulk_commit_group();

@@ -233,6 +233,15 @@ __device__ __forceinline__ uint4 load(const uint4* p) {
   return v;
 }
 
+// As mbar_wait, for waits that are short as a rule: the wall clock, whose reading takes
+// some 1000 cycles, is not looked at before 64 tests.
+__device__ __forceinline__ bool mbar_wait_soon(uint32_t bar, uint32_t parity, const WaitCtl& c) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_test(bar, parity)) return true;
+  return mbar_wait(bar, parity, c);
+}
+
 // cp.async of 16 bytes, or of 16 zero bytes (nothing is read then).
 __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool copy) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),

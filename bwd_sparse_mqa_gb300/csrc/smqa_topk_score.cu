@@ -26,8 +26,13 @@
 // group: read from shared memory for every tile, 4 bytes a lane, they took as long as
 // the tensor core (1024 clocks a tile of 256 columns) from the bandwidth that it needs
 // for its operands.  A wide tile's columns are shared by the two warpgroups, narrow
-// tiles (up to 128 columns) go to them in turn.
+// tiles (up to 128 columns) go to them in turn.  The accumulator is given back before
+// the sums are made into keys and written (some 400 clocks a token).  Half of the ReLUs
+// are x + |x| with the weight halved: an addition, where a maximum takes twice as long
+// and waits for the unit of the integer operations.
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "smqa_topk.cuh"
 
@@ -107,6 +112,7 @@ __device__ __forceinline__ float relu(float x) {         // (a NaN stays one)
   asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float twice_relu(float x) { return x + fabsf(x); }  // (of -infinity: NaN)
 
 // Whether `ok` holds for all threads of barrier `id` (whole warps): they go on, or
 // leave, together.
@@ -275,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           part = end;
         }
       }
-      if (seg >= 2) ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQEmpty + (seg & 1)), ((seg >> 1) - 1) & 1, ctl));
+      if (seg >= 2) ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarQEmpty + (seg & 1)), ((seg >> 1) - 1) & 1, ctl));
       if (!ok) break;
       Work* wk = works + (seg & 1);
       const int tile0 = static_cast<int>(skip);
@@ -312,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < L::kPieces; ++c, ++e) {
           const int st = e % L::kStages;
           if (e >= L::kStages)
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(L::kBarKEmpty + st), ((e / L::kStages) - 1) & 1, ctl));
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarKEmpty + st), ((e / L::kStages) - 1) & 1, ctl));
           if (!ok) break;
           const uint32_t to = base + L::kOffK + static_cast<uint32_t>(st) * L::kPieceBytes;
           if constexpr (kPaged) {
@@ -342,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     const uint64_t d_k = smem_desc(base + L::kOffK, 16u, L::kAtom, L::kSwizzle);
     const uint64_t d_q = smem_desc(base + L::kOffQ, 16u, L::kAtom, L::kSwizzle);
-    auto wait = [&](int i, int phase) { return __all_sync(0xffffffffu, mbar_wait(bar(i), phase & 1, ctl)); };
+    auto wait = [&](int i, int phase) { return __all_sync(0xffffffffu, mbar_wait_soon(bar(i), phase & 1, ctl)); };
     bool ok = *abort_flag == 0;
     int e = 0, tile_no = 0;
     for (int seg = 0; ok; ++seg) {
@@ -439,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int e = 0;
     for (int seg = 0; ok; ++seg) {
       const int qb = seg & 1;
-      ok = bar_all(3, 128, mbar_wait(bar(L::kBarWork + qb), (seg >> 1) & 1, ctl));
+      ok = bar_all(3, 128, mbar_wait_soon(bar(L::kBarWork + qb), (seg >> 1) & 1, ctl));
       if (!ok) break;
       const Work& wk = works[qb];
       const int ntok = wk.ntok, ntiles = wk.ntiles, tile0 = wk.tile0;
@@ -514,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // where they are subnormal.
         for (int i = 0; ok && i < ntiles; ++i, ++e) {
           const int st = e % L::kStages;
-          const bool there = mbar_wait(bar(L::kBarKFull + st), (e / L::kStages) & 1, ctl);
+          const bool there = mbar_wait_soon(bar(L::kBarKFull + st), (e / L::kStages) & 1, ctl);
           const uint8_t* row = smem + L::kOffK + st * L::kPieceBytes + ht * L::kPitch;
           float s = 0.f;
 #pragma unroll
@@ -561,12 +567,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tile_no = 0;
     for (int seg = 0; ok; ++seg) {
       const int qb = seg & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarWork + qb), (seg >> 1) & 1, ctl));
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarWork + qb), (seg >> 1) & 1, ctl));
       if (!ok) break;
       const Work& wk = works[qb];
       const int ntiles = wk.ntiles, ntok = wk.ntok, tile0 = wk.tile0;
       if (ntiles == 0) break;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQFull + qb), (seg >> 1) & 1, ctl));
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarQFull + qb), (seg >> 1) & 1, ctl));
       if (!ok) break;
       const bool wide = ntok * Hp > kMine;
       const int col0 = wide ? group * kMine : 0;
@@ -579,8 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float4 v = ws[c];
         w[4 * c] = v.x;
         w[4 * c + 1] = v.y;
-        w[4 * c + 2] = v.z;
-        w[4 * c + 3] = v.w;
+        w[4 * c + 2] = 0.5f * v.z;                       // (for twice the ReLU)
+        w[4 * c + 3] = 0.5f * v.w;
       }
       int seen[kTok];                                    // rows that its tokens see
 #pragma unroll
@@ -588,46 +594,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       int32_t* out = p.rows + (wk.tok + tok0 - p.tok0) * ld;
       for (int i = 0; ok && i < ntiles; ++i, ++tile_no) {
         const int acc = tile_no & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarAccFull + acc), (tile_no >> 1) & 1, ctl));
+        ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarAccFull + acc), (tile_no >> 1) & 1, ctl));
         if (!ok) break;
         if (wide || acc == group) {
           tc_fence_after();
           const int j = (tile0 + i) * kTile + my;
           float scale = 1.f;
           if constexpr (kPaged) scale = reinterpret_cast<const float*>(smem + L::kOffMeta)[(tile_no % L::kMeta) * 8 + (my >> page_shift)];
-          // A token's score of this row, written as its block's.
-          auto put = [&](int tok, float s) {
-            const int n = seen[tok];
-            if (j - lane >= n) return;                   // (the same for the whole warp)
-            if constexpr (kPaged) s *= scale;
-            int32_t key = key_of(s);
-            if (j >= n - recent) key = kKeyAlways;
-            if (j >= n || (kPaged && scale < 0.f)) key = kKeyNever;
-            for (int off = 1; off < (1 << eshift); off <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, off));
-            if ((lane & ((1 << eshift) - 1)) == 0 && j < n) out[tok * ld + (j >> eshift)] = key;
-          };
           const uint32_t t_acc = tmem + lanes + static_cast<uint32_t>(acc) * kCols + static_cast<uint32_t>(col0);
-          float2 a0 = {}, a1 = {};
+          // The sums of its tokens (columns behind the last token's are of no token).
+          float sum[kTok] = {};
+          auto sums = [&](auto plain_tag) {
+            float2 a0 = {}, a1 = {};
 #pragma unroll
-          for (int u = 0; u < kMine / 32; ++u) {
-            // (Columns behind the last token's are of no token; the last read frees the
-            // accumulator.)
-            if (col0 + u * 32 >= ntok * Hp) break;
-            float x[32];
-            tmem_ld32(t_acc + u * 32, x);
+            for (int u = 0; u < kMine / 32; ++u) {
+              if (col0 + u * 32 >= ntok * Hp) break;     // (the sums behind are of no token)
+              float x[32];
+              tmem_ld32(t_acc + u * 32, x);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const int at = u * 32 + 4 * c;
-              if (at % Hp == 0) a0 = a1 = make_float2(0.f, 0.f);
-              a0 = fma2(make_float2(w[at], w[at + 1]), make_float2(relu(x[4 * c]), relu(x[4 * c + 1])), a0);
-              a1 = fma2(make_float2(w[at + 2], w[at + 3]), make_float2(relu(x[4 * c + 2]), relu(x[4 * c + 3])), a1);
-              if ((at + 4) % Hp == 0) put(at / Hp, (a0.x + a0.y) + (a1.x + a1.y));
+              for (int c = 0; c < 8; ++c) {
+                const int at = u * 32 + 4 * c;
+                if (at % Hp == 0) a0 = a1 = make_float2(0.f, 0.f);
+                a0 = fma2(make_float2(w[at], w[at + 1]), make_float2(relu(x[4 * c]), relu(x[4 * c + 1])), a0);
+                float y = x[4 * c + 2], z = x[4 * c + 3];
+                if constexpr (decltype(plain_tag)::value) {
+                  y = 2.f * relu(y);
+                  z = 2.f * relu(z);
+                } else {
+                  y = twice_relu(y);
+                  z = twice_relu(z);
+                }
+                a1 = fma2(make_float2(w[at + 2], w[at + 3]), make_float2(y, z), a1);
+                if ((at + 4) % Hp == 0) sum[at / Hp] = (a0.x + a0.y) + (a1.x + a1.y);
+              }
             }
+          };
+          sums(std::false_type{});
+          if constexpr (!kPaged) {
+            // (A logit of -infinity, of a key row that holds infinities: e4m3 has none.)
+            bool again = false;
+#pragma unroll
+            for (int k = 0; k < kTok; ++k) again = again || (tok0 + k < ntok && sum[k] != sum[k]);
+            if (__any_sync(0xffffffffu, again)) sums(std::true_type{});
           }
           tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kBarAccEmpty + acc));
+          // The tokens' scores of this row, written as their blocks'.  (All tokens side by
+          // side: one after another they took a latency each, more than the sums.)
+          int32_t key[kTok];
+#pragma unroll
+          for (int k = 0; k < kTok; ++k) {
+            key[k] = key_of(kPaged ? sum[k] * scale : sum[k]);
+            if (j >= seen[k] - recent) key[k] = kKeyAlways;
+            if (j >= seen[k] || (kPaged && scale < 0.f)) key[k] = kKeyNever;
+          }
+          for (int off = 1; off < (1 << eshift); off <<= 1)
+#pragma unroll
+            for (int k = 0; k < kTok; ++k) key[k] = max(key[k], __shfl_xor_sync(0xffffffffu, key[k], off));
+          int32_t* to = out + (j >> eshift);
+          const bool first = (lane & ((1 << eshift) - 1)) == 0;
+#pragma unroll
+          for (int k = 0; k < kTok; ++k)
+            if (first && j < seen[k]) to[k * ld] = key[k];  // (seen[k] = 0: no such token)
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kBarAccEmpty + acc));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kBarAccEmpty + acc));
       }
       if (lane == 0) mbar_arrive(bar(L::kBarQEmpty + qb));
     }
