@@ -5,16 +5,17 @@
 // The choice is that of the scores in real numbers, ties to the lowest position, so
 // that it does not depend on how a batch is cut or summed.  The score kernel's values
 // are off by E at most; with T the k-th largest of them, a block above T + 2E is
-// chosen and one below T - 2E is not.  The few between are scored again in fp32
-// fused multiply-adds, whose error is a fraction of E, and those that are still open
-// with each product (exact in fp32, as bf16 and e4m3 numbers are) added with its
-// rounding error kept in a second sum (two-sum), heads in fp64.
+// chosen and one below T - 2E is not.  The few between are scored again by sums of 16
+// products, added in pairs of fp32 numbers, whose error is a fraction of E, and those
+// that are still open with each product (exact in fp32, as those of bf16 and e4m3
+// numbers are) added with its rounding error kept in a second sum (two-sum).
 //
 // E = K sum_h |w_h| (c |q_h| + rho_h), K the largest length of a key row that the
 // token sees.  The tensor core drops from every product what lies 2^24 below the
 // largest term of its step, and no term or partial sum exceeds |q||k|: D products and
-// 16 step sums, c = (D + 16) 2^-24 (twice the products with two pieces of q; measured:
-// up to 2^-18.5 |q||k| at D = 128, one large product beside 127 small ones).  The sum
+// 16 step sums, c = (D + 16) 2^-24 (measured: up to 2^-18.5 |q||k| at D = 128, one large
+// product beside 127 small ones).  With two e4m3 pieces of q the sums of the small
+// pieces, up to 2^-4 |q||k|, come first: D / 16 more.  The sum
 // over heads adds (H/4 + 4) 2^-24; rho_h is what two e4m3 pieces leave of a query row
 // (0 with bf16 keys).
 #include <cuda_runtime.h>
@@ -229,13 +230,12 @@ struct Token {
     __syncthreads();
     // (1.01 for the rounding of these sums, 2^-110 for what underflows; a factor of 0
     // leaves scores of exactly 0.)
-    const float c_score = (static_cast<float>(kPaged ? 2 * D + 16 : D + 16) + static_cast<float>(p.H) * 0.25f + 4.f) * 0x1p-24f;
+    const float c_score = (static_cast<float>(kPaged ? D + D / 16 + 17 : D + 16) + static_cast<float>(p.H) * 0.25f + 4.f) * 0x1p-24f;
     const float tiny = top * 0x1p-110f;
     e_score = len * top == 0.f ? 0.f : 1.01f * top * (len * c_score + rest) + tiny;
     if (!(e_score < INFINITY)) e_score = INFINITY;
-    // Plain values: 16 products and their sum, D / 16 of these, then 16 roundings of the
-    // sum over heads and the scale.
-    e_plain = 1.01f * top * len * (static_cast<float>(17 + D / 16 + 16) * 0x1p-24f) + tiny;
+    // Plain values: 16 products and their sum (2^-23 of it), and a rounding of the score.
+    e_plain = 1.01f * top * len * (20.f * 0x1p-24f) + tiny;
     if (!(e_plain < INFINITY)) e_plain = INFINITY;
   }
 
@@ -292,17 +292,17 @@ struct Token {
       }
       __syncthreads();
       if (!kExact || shift > 0) {
-        // Plain: 16 heads x 8 rows by a warp, 16 elements at a time into fresh sums, which
-        // are added in fp32 (a running sum in the tensor core would lose bits at every step).
+        // Plain: 16 heads x 8 rows by a warp, 16 elements at a time into fresh sums of the
+        // tensor core (a running sum would lose bits at every step); what follows is in pairs.
         const int mt = (H + 15) / 16, nt = (rows + 7) / 8;
-        float* part = at<float>(L::kOffHist);            // [mt][kBatch]
+        float2* part = at<float2>(L::kOffHist);          // [mt][kBatch]
         for (int u = warp; u < mt * nt; u += L::kWarps) {
           const int h0 = u % mt * 16, r0 = u / mt * 8;
           const int hl = min(h0 + (lane & 15), H - 1);
           const uint32_t qa = smem_u32(smem) + L::kOffQ + hl * (D * 2);
           const uint32_t* kr = reinterpret_cast<const uint32_t*>(smem + L::kOffRow + (r0 + (lane >> 2)) * L::kPitch) + (lane & 3);
-          float sum[4] = {};
-#pragma unroll
+          Pair sum[4] = {};
+#pragma unroll 2
           for (int c = 0; c < D / 16; ++c) {
             uint32_t a0, a1, a2, a3;
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -316,31 +316,33 @@ struct Token {
                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(kr[8 * c]), "r"(kr[8 * c + 4]), "f"(0.f));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] += d[i];
+            for (int i = 0; i < 4; ++i) {
+              const Pair s = sum_of(sum[i].hi, d[i]);
+              sum[i] = Pair{s.hi, sum[i].lo + s.lo};
+            }
           }
           // Heads h0 + lane / 4 and 8 more, rows r0 + 2 (lane mod 4) and the next.
           const int ha = h0 + (lane >> 2), hb = ha + 8;
-          float x = 0.f, y = 0.f;
-          if (ha < H) {
-            x = at<float>(L::kOffW)[ha] * fmaxf(sum[0], 0.f);
-            y = at<float>(L::kOffW)[ha] * fmaxf(sum[1], 0.f);
-          }
-          if (hb < H) {
-            x = fmaf(at<float>(L::kOffW)[hb], fmaxf(sum[2], 0.f), x);
-            y = fmaf(at<float>(L::kOffW)[hb], fmaxf(sum[3], 0.f), y);
-          }
+          auto weighted = [&](Pair x, int h) {
+            x = normal(x.hi, x.lo);
+            return h < H && x.hi > 0.f ? times(x, at<float>(L::kOffW)[h]) : Pair{0.f, 0.f};
+          };
+          Pair x = add(weighted(sum[0], ha), weighted(sum[2], hb)), y = add(weighted(sum[1], ha), weighted(sum[3], hb));
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) {
-            x += __shfl_xor_sync(0xffffffffu, x, off);
-            y += __shfl_xor_sync(0xffffffffu, y, off);
+            x = add(x, Pair{__shfl_xor_sync(0xffffffffu, x.hi, off), __shfl_xor_sync(0xffffffffu, x.lo, off)});
+            y = add(y, Pair{__shfl_xor_sync(0xffffffffu, y.hi, off), __shfl_xor_sync(0xffffffffu, y.lo, off)});
           }
-          if (lane < 4) *reinterpret_cast<float2*>(part + u % mt * L::kBatch + r0 + 2 * lane) = make_float2(x, y);
+          if (lane < 4) *reinterpret_cast<float4*>(part + u % mt * L::kBatch + r0 + 2 * lane) = make_float4(x.hi, x.lo, y.hi, y.lo);
         }
         __syncthreads();
         if (tid < rows && scale[tid] >= 0.f) {
-          float x = 0.f;
-          for (int i = 0; i < mt; ++i) x += part[i * L::kBatch + tid];
-          x *= scale[tid];
+          Pair sum{0.f, 0.f};
+          for (int i = 0; i < mt; ++i) {
+            const float2 x = part[i * L::kBatch + tid];
+            sum = add(sum, Pair{x.x, x.y});
+          }
+          const float x = sum.hi * scale[tid];
           if constexpr (kExact) {
             if (x < floor) scale[tid] = -1.f;
           } else {
@@ -364,7 +366,7 @@ struct Token {
               s = sum;
             };
             auto pair = [](uint32_t v) { return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); };
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < 4; ++i) {
               const uint4 q = qr[(part * 4 + i) ^ (hq & 7)], k = kr[i];
               two_sum(s0, e0, mul2(pair(q.x), pair(k.x)));
@@ -1025,11 +1027,12 @@ cudaError_t launch_select(const TopkParams& p, cudaStream_t stream) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
-// Long rows, or few tokens: 1024 threads and one CTA per SM; else 256 and three.
+// Long rows, or few tokens with more than short ones: 1024 threads and one CTA per SM;
+// else 256 and three.
 template <int D, bool kPaged>
 cudaError_t launch_select(const TopkParams& p, cudaStream_t stream) {
-  return p.ld > SelLayout<D, 256>::kCap || p.toks <= kSMs ? launch_select<D, kPaged, 1024>(p, stream)
-                                                          : launch_select<D, kPaged, 256>(p, stream);
+  return p.ld > SelLayout<D, 256>::kCap || (p.toks <= kSMs && p.ld > 4096) ? launch_select<D, kPaged, 1024>(p, stream)
+                                                                          : launch_select<D, kPaged, 256>(p, stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -374,10 +374,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t kd = d_k + ((static_cast<uint32_t>(st) * L::kPieceBytes) >> 4);
           if constexpr (kPaged) {
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+            for (int part = 1; part >= 0; --part)        // (the small pieces first: see the error bound)
 #pragma unroll
               for (int k = 0; k < D / 32; ++k)
-                mma8_ss(d, kd + (k * 32u >> 4), qd + ((part * L::kQPartBytes + k * 32u) >> 4), id, (part | k) != 0);
+                mma8_ss(d, kd + (k * 32u >> 4), qd + ((part * L::kQPartBytes + k * 32u) >> 4), id, part == 0 || k != 0);
           } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
