@@ -272,9 +272,10 @@ struct Rope {
 };
 enum : int { kRopeNone = 0, kRopePairs = 1, kRopeHalves = 2 };
 
-// Elements 8 i .. 8 i + 7 of the rows from token t on (`shift`: log2 of D / 8).
+// Elements 8 i .. 8 i + 7 of the rows from token t on (`shift`: log2 of D / 8), of which
+// the row has v.
 template <int kRope>
-__device__ __forceinline__ void rotated(const uint4* src, int i, int t, int shift, const Rope& r, float (&x)[8]) {
+__device__ __forceinline__ void rotated(const uint4* src, uint4 v, int i, int t, int shift, const Rope& r, float (&x)[8]) {
   auto unpack = [](uint4 v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -283,7 +284,7 @@ __device__ __forceinline__ void rotated(const uint4* src, int i, int t, int shif
       f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
     }
   };
-  unpack(load(src + i), x);
+  unpack(v, x);
   const int at = ((i & ((1 << shift) - 1)) << 3) - r.offset;  // (a multiple of 8, as r.offset and r.dim / 2 are)
   if (static_cast<unsigned>(at) >= static_cast<unsigned>(r.dim)) return;
   const int half = r.dim >> 1;
@@ -327,29 +328,41 @@ __device__ __forceinline__ void rotated(const uint4* src, int i, int t, int shif
     }
   }
 }
+// f(i, the eight elements) for i, i + step, ... below n: the rows' loads four at a time,
+// before anything is made of them (8190 rows D=512: 13.0 us one at a time).
+template <int kRope, typename F>
+__device__ __forceinline__ void each_rotated(const uint4* src, int i, int step, int n, int t, int shift, const Rope& r, F f) {
+  constexpr int kAhead = 4;
+  for (; i < n; i += kAhead * step) {
+    uint4 v[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) v[k] = load(src + min(i + k * step, n - 1));
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (i + k * step >= n) break;
+      float x[8];
+      rotated<kRope>(src, v[k], i + k * step, t, shift, r, x);
+      f(i + k * step, x);
+    }
+  }
+}
 // As `largest` (the bits of an fp32 magnitude) and `encode`, of rotated rows.
 template <int kRope>
 __device__ __forceinline__ uint32_t largest_rotated(const uint4* src, int i, int step, int n, int t, int shift, const Rope& r) {
   uint32_t top = 0;
-#pragma unroll 2
-  for (; i < n; i += step) {
-    float x[8];
-    rotated<kRope>(src, i, t, shift, r, x);
+  each_rotated<kRope>(src, i, step, n, t, shift, r, [&](int, const float (&x)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const uint32_t b = __float_as_uint(x[k]) & 0x7fffffffu;
       top = max(top, b < 0x7f800000u ? b : 0u);
     }
-  }
+  });
   return top;
 }
 template <int kRope>
 __device__ __forceinline__ void encode_rotated(const uint4* src, uint2* dst, int i, int step, int n, float inv, int t,
                                                int shift, const Rope& r) {
-#pragma unroll 2
-  for (; i < n; i += step) {
-    float x[8];
-    rotated<kRope>(src, i, t, shift, r, x);
+  each_rotated<kRope>(src, i, step, n, t, shift, r, [&](int at, const float (&x)[8]) {
     uint32_t c[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -358,8 +371,8 @@ __device__ __forceinline__ void encode_rotated(const uint4* src, uint2* dst, int
       };
       c[k] = e4m3x2(scaled(x[2 * k]), scaled(x[2 * k + 1]));
     }
-    dst[i] = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-  }
+    dst[at] = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  });
 }
 // Codes times f = 2^-k.
 __device__ __forceinline__ void rescale(uint4* row, int i, int step, int n, float f) {

@@ -201,7 +201,7 @@ struct Token {
       if constexpr (kPaged) rest = fmaf(wh, sqrtf(sr), rest);
     }
     // The longest row of the tiles that the token sees.
-    const int tiles = (n + kTile - 1) / kTile;
+    const int tiles = 4 * ((n + kTile - 1) / kTile);     // (a bound per 32 rows)
     const float* norms = p.norms + (kPaged ? t - p.tok0 : static_cast<int64_t>(req)) * p.norm_ld;
     float top = 0.f;
     for (int i = tid; i < tiles; i += NT) top = fmaxf(top, load(norms + i));
@@ -1060,7 +1060,7 @@ struct TopkPlan {
 TopkPlan plan_topk(int64_t rows, int block_shift, int H, bool paged, int64_t B, int64_t S) {
   TopkPlan pl{};
   pl.ld = round_up((rows + (1 << entry_shift(block_shift)) - 1) >> entry_shift(block_shift), 4);
-  pl.norm_ld = (rows + kTile - 1) / kTile;
+  pl.norm_ld = 4 * ((rows + kTile - 1) / kTile);
   const int group = group_tokens(H);
   pl.units = B * ((S + group - 1) / group);              // (paged: B = 1, S = T)
   pl.chunk_units = std::min(pl.units, std::max<int64_t>(1, kChunkBytes / (pl.ld * 4) / group));

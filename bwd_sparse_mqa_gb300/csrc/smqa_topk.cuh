@@ -28,9 +28,9 @@ struct TopkParams {
   int64_t unit0, units;      // groups of consecutive tokens (of one batch element): the chunk's first, and their number
   int64_t tok0, toks;        // the chunk's tokens
   int64_t ld;                // entries of a token's row of scores
-  int64_t norm_ld;           // tiles of a token (paged) or a batch element
+  int64_t norm_ld;           // bounds of a token's rows (paged), or a batch element's
   int32_t* rows;             // [toks][ld] scores as ordered integers, of entry_rows rows each
-  float* norms;              // [toks or B][norm_ld] upper bounds of the key rows' lengths, by tile
+  float* norms;              // [toks or B][norm_ld] upper bounds of the key rows' lengths, one per 32 rows
   int32_t* out;              // [T, topk]
   int zero_padding;
   int* status;

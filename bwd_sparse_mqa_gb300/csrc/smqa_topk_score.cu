@@ -75,8 +75,7 @@ struct ScoreLayout {
   static constexpr uint32_t kOffW = kOffK + kStages * kPieceBytes;      // float [2][256]
   static constexpr uint32_t kOffMeta = kOffW + 2 * kCols * 4;           // float [kMeta][8]
   static constexpr uint32_t kOffWork = kOffMeta + kMeta * 8 * 4;        // Work [2]
-  static constexpr uint32_t kOffNorm = kOffWork + 2 * sizeof(Work);     // float [2][4]
-  static constexpr uint32_t kOffSum = kOffNorm + 32;                    // int64 [16], then the range's start
+  static constexpr uint32_t kOffSum = kOffWork + 2 * sizeof(Work);      // int64 [16], then the range's start
   static constexpr uint32_t kOffBar = kOffSum + 16 * 8 + 32;
   static constexpr int kBarKFull = 0;
   static constexpr int kBarKEmpty = kBarKFull + kStages;
@@ -113,21 +112,6 @@ __device__ __forceinline__ float relu(float x) {         // (a NaN stays one)
   return y;
 }
 __device__ __forceinline__ float twice_relu(float x) { return x + fabsf(x); }  // (of -infinity: NaN)
-
-// Whether `ok` holds for all threads of barrier `id` (whole warps): they go on, or
-// leave, together.
-__device__ __forceinline__ bool bar_all(int id, int threads, bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %3, 0;\n\t"
-      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(ok))
-      : "memory");
-  return r != 0;
-}
 
 __device__ __forceinline__ int tiles_for(const TopkParams& p, int n) { return n > p.topk ? (n + kTile - 1) / kTile : 0; }
 
@@ -402,10 +386,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     reg_dealloc<kOtherRegs>();
     // ------------------------------------------------------------ queries, weights, lengths
     const int ht = tid - 32 * kHelpWarp0, hw = warp - kHelpWarp0;  // thread of 128
-    float* norm_of = reinterpret_cast<float*>(smem + L::kOffNorm);
     if constexpr (!kPaged) {
-      // Bounds of the key rows' lengths, a tile at a time, over all CTAs.
-      const int tiles = static_cast<int>(p.norm_ld);
+      // Bounds of the key rows' lengths, 32 rows a warp, over all CTAs.
+      const int tiles = static_cast<int>(p.norm_ld) / 4;
       for (int64_t i = blockIdx.x; i < static_cast<int64_t>(p.B) * tiles; i += gridDim.x) {
         const int64_t b = i / tiles;
         const int j = static_cast<int>(i - b * tiles) * kTile + ht;
@@ -434,18 +417,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(s)));
-        if (lane == 0) norm_of[hw] = m;
-        bar_sync(2, 128);
-        if (ht == 0) p.norms[i] = fmaxf(fmaxf(norm_of[0], norm_of[1]), fmaxf(norm_of[2], norm_of[3]));
-        bar_sync(2, 128);
+        if (lane == 0) p.norms[i * 4 + hw] = m;
       }
     }
-    // (A wait that fails for one of these warps ends the work of all four.)
     bool ok = count_all > 0;
     int e = 0;
     for (int seg = 0; ok; ++seg) {
       const int qb = seg & 1;
-      ok = bar_all(3, 128, mbar_wait_soon(bar(L::kBarWork + qb), (seg >> 1) & 1, ctl));
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarWork + qb), (seg >> 1) & 1, ctl));
       if (!ok) break;
       const Work& wk = works[qb];
       const int ntok = wk.ntok, ntiles = wk.ntiles, tile0 = wk.tile0;
@@ -520,7 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // where they are subnormal.
         for (int i = 0; ok && i < ntiles; ++i, ++e) {
           const int st = e % L::kStages;
-          const bool there = mbar_wait_soon(bar(L::kBarKFull + st), (e / L::kStages) & 1, ctl);
+          ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarKFull + st), (e / L::kStages) & 1, ctl));
+          if (!ok) break;
           const uint8_t* row = smem + L::kOffK + st * L::kPieceBytes + ht * L::kPitch;
           float s = 0.f;
 #pragma unroll
@@ -541,15 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float scale = reinterpret_cast<const float*>(smem + L::kOffMeta)[(e % L::kMeta) * 8 + (ht >> p.page_shift)];
           s = sqrtf(s * 1.02f + 0x1p-16f) * 256.f * fmaxf(scale, 0.f);
           const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(s)));
-          if (lane == 0) {
-            mbar_arrive(bar(L::kBarKEmpty + st));
-            norm_of[(e & 1) * 4 + hw] = m;
-          }
-          ok = bar_all(2, 128, there);
-          if (ok && ht < ntok) {
-            const float* nm = norm_of + (e & 1) * 4;
-            p.norms[(tok + ht - p.tok0) * p.norm_ld + tile0 + i] = fmaxf(fmaxf(nm[0], nm[1]), fmaxf(nm[2], nm[3]));
-          }
+          if (lane == 0) mbar_arrive(bar(L::kBarKEmpty + st));
+          if (lane < ntok) p.norms[(tok + lane - p.tok0) * p.norm_ld + (tile0 + i) * 4 + hw] = m;
         }
       }
       if (lane == 0) mbar_arrive(bar(L::kBarQEmpty + qb));
