@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(bar(L::kBarKFull + i), 1);
-      mbar_init(bar(L::kBarKEmpty + i), kPaged ? 5 : 1);  // tensor core (and four warps that bound the rows' lengths)
+      mbar_init(bar(L::kBarKEmpty + i), kPaged ? 3 : 1);  // tensor core (and two warps that bound the rows' lengths)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(L::kBarAccFull + i), 1);
@@ -288,14 +288,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       left -= ntiles;
       skip = 0;
       part = end;
+      // Paged: lane = page of a tile.  The pages of the tile after next and the scales of the
+      // next one are asked for before a tile's copies are issued (one after another, the
+      // loads took 1200 cycles a tile).
+      auto page_of = [&](int i) {
+        const int col = ((tile0 + i) * kTile >> p.page_shift) + lane;
+        const bool in = i < ntiles && lane < (kTile >> p.page_shift) && col < p.max_pages;
+        return in ? load(p.table + static_cast<int64_t>(req) * p.max_pages + col) : -1;
+      };
+      auto is_page = [&](int page) { return static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages); };
+      auto scale_of = [&](int page) { return is_page(page) ? load(p.scales + page) : -1.f; };
+      int page = -1, next_page = -1;
+      float scale = -1.f;
+      if constexpr (kPaged) {
+        page = page_of(0);
+        next_page = page_of(1);
+        scale = scale_of(page);
+      }
       for (int i = 0; ok && i < ntiles; ++i, ++tile_no) {
         const int j0 = (tile0 + i) * kTile;
-        int page = -1;
-        bool live = true;
-        if constexpr (kPaged) {                          // lane = page of the tile
-          const int pages = kTile >> p.page_shift, col = (j0 >> p.page_shift) + lane;
-          page = lane < pages && col < p.max_pages ? load(p.table + static_cast<int64_t>(req) * p.max_pages + col) : -1;
-          live = static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages);
+        const bool live = !kPaged || is_page(page);
+        int later_page = -1;
+        float next_scale = -1.f;
+        if constexpr (kPaged) {
+          later_page = page_of(i + 2);
+          next_scale = scale_of(next_page);
         }
         const unsigned pages_there = __ballot_sync(0xffffffffu, live);
 #pragma unroll
@@ -310,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (-1 for a page that is not there: its rows get no copy, what lies in
             // their place is never used.)
             if (lane < 8)
-              reinterpret_cast<float*>(smem + L::kOffMeta)[(tile_no % L::kMeta) * 8 + lane] = live ? load(p.scales + page) : -1.f;
+              reinterpret_cast<float*>(smem + L::kOffMeta)[(tile_no % L::kMeta) * 8 + lane] = scale;
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(bar(L::kBarKFull + st), bytes * __popc(pages_there));
             __syncwarp();
@@ -320,6 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d(to, &tm_k, c * 64, req * p.S_kv + j0, bar(L::kBarKFull + st));
           }
         }
+        page = next_page;
+        next_page = later_page;
+        scale = next_scale;
       }
       if (!ok) break;
     }
@@ -493,36 +513,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kBarQFull + qb));
       if constexpr (kPaged) {
-        // Bounds of the key rows' lengths, from the tiles as they pass: thread = row.
+        // Bounds of the key rows' lengths, from the tiles as they pass: two warps take every
+        // other one, a thread two rows (a tile in turn by all four took 1250 cycles a tile,
+        // half of it the wait).
         // |code| 2^-8 is the fp16 number with the code's seven bits at 7-13; squares and
         // sums of 16 of them in fp16 are off by 2^-11 each step, and lose 2^-25 each
         // where they are subnormal.
         for (int i = 0; ok && i < ntiles; ++i, ++e) {
+          if ((e & 1) != (hw >> 1)) continue;
           const int st = e % L::kStages;
           ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarKFull + st), (e / L::kStages) & 1, ctl));
           if (!ok) break;
-          const uint8_t* row = smem + L::kOffK + st * L::kPieceBytes + ht * L::kPitch;
-          float s = 0.f;
+          float top = 0.f;
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            const int at = L::kPitch == 128 ? c ^ (ht & 7) : c ^ ((ht >> 1) & 3);
-            const uint4 v = *reinterpret_cast<const uint4*>(row + at * 16);
-            const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-            __half2 a = __float2half2_rn(0.f);
+          for (int half = 0; half < 2; ++half) {
+            const int r = (hw & 1) * 64 + half * 32 + lane;
+            const uint8_t* row = smem + L::kOffK + st * L::kPieceBytes + r * L::kPitch;
+            float s = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t x = (w4[k] & 0x007f007fu) << 7, y = (w4[k] & 0x7f007f00u) >> 1;
-              a = __hfma2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&x), a);
-              a = __hfma2(*reinterpret_cast<const __half2*>(&y), *reinterpret_cast<const __half2*>(&y), a);
+            for (int c = 0; c < D / 16; ++c) {
+              const int at = L::kPitch == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+              const uint4 v = *reinterpret_cast<const uint4*>(row + at * 16);
+              const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+              __half2 a = __float2half2_rn(0.f);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t x = (w4[k] & 0x007f007fu) << 7, y = (w4[k] & 0x7f007f00u) >> 1;
+                a = __hfma2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&x), a);
+                a = __hfma2(*reinterpret_cast<const __half2*>(&y), *reinterpret_cast<const __half2*>(&y), a);
+              }
+              const float2 f = __half22float2(a);
+              s += f.x + f.y;
             }
-            const float2 f = __half22float2(a);
-            s += f.x + f.y;
+            const float scale = reinterpret_cast<const float*>(smem + L::kOffMeta)[(e % L::kMeta) * 8 + (r >> p.page_shift)];
+            top = fmaxf(top, sqrtf(s * 1.02f + 0x1p-16f) * 256.f * fmaxf(scale, 0.f));
           }
-          const float scale = reinterpret_cast<const float*>(smem + L::kOffMeta)[(e % L::kMeta) * 8 + (ht >> p.page_shift)];
-          s = sqrtf(s * 1.02f + 0x1p-16f) * 256.f * fmaxf(scale, 0.f);
-          const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(s)));
+          top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
           if (lane == 0) mbar_arrive(bar(L::kBarKEmpty + st));
-          if (lane < ntok) p.norms[(tok + lane - p.tok0) * p.norm_ld + (tile0 + i) * 4 + hw] = m;
+          if (lane < ntok)
+            *reinterpret_cast<float2*>(p.norms + (tok + lane - p.tok0) * p.norm_ld + (tile0 + i) * 4 + (hw & 1) * 2) = make_float2(top, top);
         }
       }
       if (lane == 0) mbar_arrive(bar(L::kBarQEmpty + qb));
