@@ -52,7 +52,8 @@ struct SelLayout {
   static constexpr uint32_t kOffRow = kOffMark + kList * 4;   // bf16 [kBatch][D], padded
   static constexpr uint32_t kOffScale = kOffRow + kBatch * kPitch;  // float [kBatch]
   static constexpr uint32_t kOffW = kOffScale + kBatch * 4;   // float [128]
-  static constexpr uint32_t kOffRed = kOffW + 128 * 4;        // int [8][kWarps]
+  static constexpr uint32_t kOffLen = kOffW + 128 * 4;        // float [128]: lengths of the query rows
+  static constexpr uint32_t kOffRed = kOffLen + 128 * 4;      // int [8][kWarps]
   static constexpr uint32_t kOffMore = kOffRed + 8 * kWarps * 4;  // int [kWarps]
   static constexpr uint32_t kOffMisc = kOffMore + kWarps * 4;
   static constexpr uint32_t kOffBins = kOffMisc + 64;    // uint16 [kCap]
@@ -112,6 +113,7 @@ struct Token {
   int n, req;
   int tid, warp, lane;
   float e_score, e_plain;                                // error bounds of the score kernel's values, of plain ones
+  float longest;                                         // bound of the key rows' lengths
 
   template <typename T>
   __device__ __forceinline__ T* at(uint32_t off) const {
@@ -197,6 +199,7 @@ struct Token {
         if constexpr (kPaged) sr += __shfl_xor_sync(0xffffffffu, sr, off);
       }
       const float wh = c == 0 ? fabsf(w) * pow2f(-k) : 0.f;
+      if (there && c == 0) at<float>(L::kOffLen)[h] = 1.01f * sqrtf(sq) * pow2f(-k);
       len = fmaf(wh, sqrtf(sq), len);
       if constexpr (kPaged) rest = fmaf(wh, sqrtf(sr), rest);
     }
@@ -232,11 +235,65 @@ struct Token {
     // leaves scores of exactly 0.)
     const float c_score = (static_cast<float>(kPaged ? D + D / 16 + 17 : D + 16) + static_cast<float>(p.H) * 0.25f + 4.f) * 0x1p-24f;
     const float tiny = top * 0x1p-110f;
+    longest = top;
     e_score = len * top == 0.f ? 0.f : 1.01f * top * (len * c_score + rest) + tiny;
     if (!(e_score < INFINITY)) e_score = INFINITY;
     // Plain values: 16 products and their sum (2^-23 of it), and a rounding of the score.
     e_plain = 1.01f * top * len * (20.f * 0x1p-24f) + tiny;
     if (!(e_plain < INFINITY)) e_plain = INFINITY;
+  }
+
+  // Whether position j's score is exactly 0: its key row is 0, or every logit lies below 0
+  // by more than the error of its fp32 sum (D / 8 products in a row, then four adds).  By
+  // one thread: the row's bytes from the caches, the queries the same for all lanes.
+  __device__ __forceinline__ bool surely_zero(int j) const {
+    uint4 k[kPaged ? D / 16 : D / 8];
+    if constexpr (kPaged) {
+      const int pg = page_of(j);
+      if (pg < 0) return false;
+      const uint4* src = reinterpret_cast<const uint4*>(p.codes + ((static_cast<int64_t>(pg) << p.page_shift) + (j & ((1 << p.page_shift) - 1))) * D);
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) k[c] = load(src + c);
+    } else {
+      const uint4* src = reinterpret_cast<const uint4*>(p.k + (static_cast<int64_t>(req) * p.S_kv + j) * D);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) k[c] = load(src + c);
+    }
+    constexpr uint32_t kMagnitudes = kPaged ? 0x7f7f7f7fu : 0x7fff7fffu;
+    uint32_t any = 0;
+#pragma unroll
+    for (int c = 0; c < (kPaged ? D / 16 : D / 8); ++c) any |= (k[c].x | k[c].y | k[c].z | k[c].w) & kMagnitudes;
+    if (any == 0) return true;
+    // (Paged: the bound's lengths are scaled, the codes are not.)
+    float scale = 1.f;
+    if constexpr (kPaged) scale = load(p.scales + page_of(j));
+    for (int h = 0; h < p.H; ++h) {
+      const uint4* q = at<uint4>(L::kOffQ) + h * (D / 8);
+      float2 s[4] = {};
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 v = q[c ^ (h & 7)];
+        const uint32_t q4[4] = {v.x, v.y, v.z, v.w};
+        float2 kk[4];
+        if constexpr (kPaged) {
+          const uint32_t lo = (c & 1) ? k[c / 2].z : k[c / 2].x, hi = (c & 1) ? k[c / 2].w : k[c / 2].y;
+          kk[0] = e4m3x2_value(static_cast<uint16_t>(lo));
+          kk[1] = e4m3x2_value(static_cast<uint16_t>(lo >> 16));
+          kk[2] = e4m3x2_value(static_cast<uint16_t>(hi));
+          kk[3] = e4m3x2_value(static_cast<uint16_t>(hi >> 16));
+        } else {
+          const uint32_t w4[4] = {k[c].x, k[c].y, k[c].z, k[c].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) kk[i] = make_float2(__uint_as_float(w4[i] << 16), __uint_as_float(w4[i] & 0xffff0000u));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = fma2(make_float2(__uint_as_float(q4[i] << 16), __uint_as_float(q4[i] & 0xffff0000u)), kk[i], s[i]);
+      }
+      const float2 sum = add2(add2(s[0], s[1]), add2(s[2], s[3]));
+      const float bound = longest * at<float>(L::kOffLen)[h] * (static_cast<float>(D / 8 + 4) * 0x1p-24f);
+      if (!((sum.x + sum.y) * scale < -bound)) return false;
+    }
+    return true;
   }
 
   // Scores of the rows of candidates (blocks) cand(0 .. m - 1) once more, plain or exact:
@@ -683,6 +740,50 @@ __device__ __forceinline__ Cut any_cut(Token<D, kPaged, NT>& tk, const Keys<D, k
       for (int i = tk.tid; i < m; i += NT) keys.store(idx[i], mark[i] ? kKeyAlways : kKeyNever);
       return Cut{khi, khi, 0};
     }
+    // Many scores of exactly 0 (few heads, key rows of 0): those are settled without the
+    // exact sums, and the few others of the window against them.
+    if (level == 0 && tk.p.block_shift == 0) {
+      __syncthreads();
+      if (tk.tid == 0) misc[3] = 0;
+      __syncthreads();
+      int zeros = 0;
+      for (int c = tk.tid; c < keys.nb; c += NT) {
+        const int key = keys.fetch(c);
+        if (key < klo || key > khi) {
+          keys.store(c, key > khi ? kKeyAlways : kKeyNever);
+        } else if (tk.surely_zero(c)) {
+          ++zeros;
+          keys.store(c, 0);
+        } else {
+          const int i = atomicAdd(misc + 3, 1);
+          if (i < kList) idx[i] = c;
+          if (key == 0) keys.store(c, 1);                // (not a sure one)
+        }
+      }
+      int n0[1] = {zeros};
+      tk.template reduce<1, false>(n0);
+      const int some = misc[3];
+      if (n0[0] > 0 && some <= kList) {
+        exact_scores<D, kPaged, NT, false>(tk, some, -INFINITY);
+        const long long zero = key64_of(Pair{0.f, 0.f});
+        int by[2] = {0, 0};                              // above 0, equal
+        for (int i = tk.tid; i < some; i += NT) {
+          by[0] += val[i] > zero;
+          by[1] += val[i] == zero;
+        }
+        tk.template reduce<2, false>(by);
+        const int ties = n0[0] + by[1];
+        // Above 0 first, the zeros by number, below 0 last.
+        for (int i = tk.tid; i < some; i += NT) {
+          const long long x = val[i];
+          const int c = idx[i];
+          int before = x < zero ? ties : 0;
+          for (int k = 0; k < some; ++k) before += val[k] != zero && (val[k] > x || (val[k] == x && idx[k] < c));
+          keys.store(c, x == zero ? 0 : before < r ? kKeyAlways : kKeyNever);
+        }
+        return Cut{0, 0, max(0, min(r - by[0], ties))};
+      }
+    }
     // (base: of the values so far; the new ones' is T.)  As many candidates as the list
     // holds at a time.
     base += static_cast<double>(mid);
@@ -974,7 +1075,7 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : 3) smqa_topk_select_kerne
       for (int i = tid; i < p.topk; i += NT) out[i] = -1;
     return;
   }
-  Token<D, kPaged, NT> tk{p, smem, t, n, req, tid, tid >> 5, tid & 31, 0.f, 0.f};
+  Token<D, kPaged, NT> tk{p, smem, t, n, req, tid, tid >> 5, tid & 31, 0.f, 0.f, 0.f};
   if (n <= p.topk) {
     // All that the token sees.
     if constexpr (kPaged) {

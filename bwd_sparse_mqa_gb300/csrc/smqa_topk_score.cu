@@ -244,163 +244,163 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kLoadWarp && warp < kHelpWarp0) {
     reg_dealloc<kOtherRegs>();                           // (the warpgroup's other warps have no role)
     if (warp == kLoadWarp) {
-    // ------------------------------------------------------------ walk and copy
-    int64_t u = start[0], skip = start[1], left = count_all;
-    int part = 0, e = 0, tile_no = 0;                    // pieces and tiles so far
-    int64_t first;
-    int count = unit_tokens<kPaged>(p, u, kGroup, first);
-    bool ok = *abort_flag == 0;
-    for (int seg = 0;; ++seg) {
-      // The next part with tiles in the range.
-      int end = 0, req = 0, tiles = 0;
-      if (left > 0) {
-        while (true) {
-          if (part >= count) {
-            count = unit_tokens<kPaged>(p, ++u, kGroup, first);
-            part = 0;
+      // ------------------------------------------------------------ walk and copy
+      int64_t u = start[0], skip = start[1], left = count_all;
+      int part = 0, e = 0, tile_no = 0;                    // pieces and tiles so far
+      int64_t first;
+      int count = unit_tokens<kPaged>(p, u, kGroup, first);
+      bool ok = *abort_flag == 0;
+      for (int seg = 0;; ++seg) {
+        // The next part with tiles in the range.
+        int end = 0, req = 0, tiles = 0;
+        if (left > 0) {
+          while (true) {
+            if (part >= count) {
+              count = unit_tokens<kPaged>(p, ++u, kGroup, first);
+              part = 0;
+            }
+            tiles = part_tiles<kPaged>(p, first, count, part, end, req);
+            if (skip < tiles) break;
+            skip -= tiles;
+            part = end;
           }
-          tiles = part_tiles<kPaged>(p, first, count, part, end, req);
-          if (skip < tiles) break;
-          skip -= tiles;
-          part = end;
         }
-      }
-      if (seg >= 2) ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarQEmpty + (seg & 1)), ((seg >> 1) - 1) & 1, ctl));
-      if (!ok) break;
-      Work* wk = works + (seg & 1);
-      const int tile0 = static_cast<int>(skip);
-      const int ntiles = static_cast<int>(min(left, static_cast<int64_t>(tiles) - skip));
-      if (lane < kMaxGroup) {
-        int n = 0, r;
-        if (left > 0 && lane < end - part) n = visible<kPaged>(p, first + part + lane, r);
-        wk->n[lane] = n > p.topk ? n : 0;
-      }
-      if (lane == 0) {
-        wk->tok = first + part;
-        wk->ntok = end - part;
-        wk->tile0 = tile0;
-        wk->ntiles = left > 0 ? ntiles : 0;
-        wk->req = req;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::kBarWork + (seg & 1)));
-      if (left <= 0) break;
-      left -= ntiles;
-      skip = 0;
-      part = end;
-      // Paged: lane = page of a tile.  The pages of the tile after next and the scales of the
-      // next one are asked for before a tile's copies are issued (one after another, the
-      // loads took 1200 cycles a tile).
-      auto page_of = [&](int i) {
-        const int col = ((tile0 + i) * kTile >> p.page_shift) + lane;
-        const bool in = i < ntiles && lane < (kTile >> p.page_shift) && col < p.max_pages;
-        return in ? load(p.table + static_cast<int64_t>(req) * p.max_pages + col) : -1;
-      };
-      auto is_page = [&](int page) { return static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages); };
-      auto scale_of = [&](int page) { return is_page(page) ? load(p.scales + page) : -1.f; };
-      int page = -1, next_page = -1;
-      float scale = -1.f;
-      if constexpr (kPaged) {
-        page = page_of(0);
-        next_page = page_of(1);
-        scale = scale_of(page);
-      }
-      for (int i = 0; ok && i < ntiles; ++i, ++tile_no) {
-        const int j0 = (tile0 + i) * kTile;
-        const bool live = !kPaged || is_page(page);
-        int later_page = -1;
-        float next_scale = -1.f;
+        if (seg >= 2) ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarQEmpty + (seg & 1)), ((seg >> 1) - 1) & 1, ctl));
+        if (!ok) break;
+        Work* wk = works + (seg & 1);
+        const int tile0 = static_cast<int>(skip);
+        const int ntiles = static_cast<int>(min(left, static_cast<int64_t>(tiles) - skip));
+        if (lane < kMaxGroup) {
+          int n = 0, r;
+          if (left > 0 && lane < end - part) n = visible<kPaged>(p, first + part + lane, r);
+          wk->n[lane] = n > p.topk ? n : 0;
+        }
+        if (lane == 0) {
+          wk->tok = first + part;
+          wk->ntok = end - part;
+          wk->tile0 = tile0;
+          wk->ntiles = left > 0 ? ntiles : 0;
+          wk->req = req;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kBarWork + (seg & 1)));
+        if (left <= 0) break;
+        left -= ntiles;
+        skip = 0;
+        part = end;
+        // Paged: lane = page of a tile.  The pages of the tile after next and the scales of the
+        // next one are asked for before a tile's copies are issued (one after another, the
+        // loads took 1200 cycles a tile).
+        auto page_of = [&](int i) {
+          const int col = ((tile0 + i) * kTile >> p.page_shift) + lane;
+          const bool in = i < ntiles && lane < (kTile >> p.page_shift) && col < p.max_pages;
+          return in ? load(p.table + static_cast<int64_t>(req) * p.max_pages + col) : -1;
+        };
+        auto is_page = [&](int page) { return static_cast<unsigned>(page) < static_cast<unsigned>(p.n_pages); };
+        auto scale_of = [&](int page) { return is_page(page) ? load(p.scales + page) : -1.f; };
+        int page = -1, next_page = -1;
+        float scale = -1.f;
         if constexpr (kPaged) {
-          later_page = page_of(i + 2);
-          next_scale = scale_of(next_page);
+          page = page_of(0);
+          next_page = page_of(1);
+          scale = scale_of(page);
         }
-        const unsigned pages_there = __ballot_sync(0xffffffffu, live);
-#pragma unroll
-        for (int c = 0; c < L::kPieces; ++c, ++e) {
-          const int st = e % L::kStages;
-          if (e >= L::kStages)
-            ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarKEmpty + st), ((e / L::kStages) - 1) & 1, ctl));
-          if (!ok) break;
-          const uint32_t to = base + L::kOffK + static_cast<uint32_t>(st) * L::kPieceBytes;
+        for (int i = 0; ok && i < ntiles; ++i, ++tile_no) {
+          const int j0 = (tile0 + i) * kTile;
+          const bool live = !kPaged || is_page(page);
+          int later_page = -1;
+          float next_scale = -1.f;
           if constexpr (kPaged) {
-            const uint32_t bytes = static_cast<uint32_t>(D) << p.page_shift;
-            // (-1 for a page that is not there: its rows get no copy, what lies in
-            // their place is never used.)
-            if (lane < 8)
-              reinterpret_cast<float*>(smem + L::kOffMeta)[(tile_no % L::kMeta) * 8 + lane] = scale;
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(bar(L::kBarKFull + st), bytes * __popc(pages_there));
-            __syncwarp();
-            if (live) tma_load_2d(to + lane * bytes, &tm_k, 0, page << p.page_shift, bar(L::kBarKFull + st));
-          } else if (lane == 0) {
-            mbar_arrive_expect_tx(bar(L::kBarKFull + st), L::kPieceBytes);
-            tma_load_2d(to, &tm_k, c * 64, req * p.S_kv + j0, bar(L::kBarKFull + st));
+            later_page = page_of(i + 2);
+            next_scale = scale_of(next_page);
           }
-        }
-        page = next_page;
-        next_page = later_page;
-        scale = next_scale;
-      }
-      if (!ok) break;
-    }
-    // Copies in flight land before the CTA ends.
-    if (lane == 0)
-      for (int i = max(0, e - L::kStages); i < e; ++i)
-        mbar_wait_drain(bar(L::kBarKFull + i % L::kStages), (i / L::kStages) & 1);
-    __syncwarp();
-    } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issuer
-    const uint64_t d_k = smem_desc(base + L::kOffK, 16u, L::kAtom, L::kSwizzle);
-    const uint64_t d_q = smem_desc(base + L::kOffQ, 16u, L::kAtom, L::kSwizzle);
-    auto wait = [&](int i, int phase) { return __all_sync(0xffffffffu, mbar_wait_soon(bar(i), phase & 1, ctl)); };
-    bool ok = *abort_flag == 0;
-    int e = 0, tile_no = 0;
-    for (int seg = 0; ok; ++seg) {
-      const int qb = seg & 1;
-      ok = wait(L::kBarWork + qb, seg >> 1);
-      if (!ok) break;
-      const int ntiles = works[qb].ntiles, ntok = works[qb].ntok;
-      if (ntiles == 0) break;
-      ok = wait(L::kBarQFull + qb, seg >> 1);
-      const uint64_t qd = d_q + ((static_cast<uint32_t>(qb) * L::kQBytes) >> 4);
-      const uint32_t idesc = kPaged ? idesc_e4m3_f32(128, 16, false) : idesc_bf16_f32(128, 16, false, false);
-      const uint32_t id = (idesc & ~(0x3fu << 17)) | (static_cast<uint32_t>(ntok * Hp >> 3) << 17);
-      for (int i = 0; ok && i < ntiles; ++i, ++tile_no) {
-        const int acc = tile_no & 1;
-        if (tile_no >= 2) ok = wait(L::kBarAccEmpty + acc, (tile_no >> 1) - 1);
-        const uint32_t d = tmem + static_cast<uint32_t>(acc) * kCols;
-#pragma unroll
-        for (int c = 0; c < L::kPieces; ++c, ++e) {
-          const int st = e % L::kStages;
-          ok = ok && wait(L::kBarKFull + st, e / L::kStages);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t kd = d_k + ((static_cast<uint32_t>(st) * L::kPieceBytes) >> 4);
-          if constexpr (kPaged) {
-#pragma unroll
-            for (int part = 1; part >= 0; --part)        // (the small pieces first: see the error bound)
-#pragma unroll
-              for (int k = 0; k < D / 32; ++k)
-                mma8_ss(d, kd + (k * 32u >> 4), qd + ((part * L::kQPartBytes + k * 32u) >> 4), id, part == 0 || k != 0);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma16_ss(d, kd + (k * 32u >> 4), qd + ((c * L::kQPartBytes + k * 32u) >> 4), id, (c | k) != 0);
+          const unsigned pages_there = __ballot_sync(0xffffffffu, live);
+  #pragma unroll
+          for (int c = 0; c < L::kPieces; ++c, ++e) {
+            const int st = e % L::kStages;
+            if (e >= L::kStages)
+              ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarKEmpty + st), ((e / L::kStages) - 1) & 1, ctl));
+            if (!ok) break;
+            const uint32_t to = base + L::kOffK + static_cast<uint32_t>(st) * L::kPieceBytes;
+            if constexpr (kPaged) {
+              const uint32_t bytes = static_cast<uint32_t>(D) << p.page_shift;
+              // (-1 for a page that is not there: its rows get no copy, what lies in
+              // their place is never used.)
+              if (lane < 8)
+                reinterpret_cast<float*>(smem + L::kOffMeta)[(tile_no % L::kMeta) * 8 + lane] = scale;
+              __syncwarp();
+              if (lane == 0) mbar_arrive_expect_tx(bar(L::kBarKFull + st), bytes * __popc(pages_there));
+              __syncwarp();
+              if (live) tma_load_2d(to + lane * bytes, &tm_k, 0, page << p.page_shift, bar(L::kBarKFull + st));
+            } else if (lane == 0) {
+              mbar_arrive_expect_tx(bar(L::kBarKFull + st), L::kPieceBytes);
+              tma_load_2d(to, &tm_k, c * 64, req * p.S_kv + j0, bar(L::kBarKFull + st));
+            }
           }
-          mma_commit_elect(bar(L::kBarKEmpty + st));
+          page = next_page;
+          next_page = later_page;
+          scale = next_scale;
         }
         if (!ok) break;
-        mma_commit_elect(bar(L::kBarAccFull + acc));
-        if (static_cast<int>(blockIdx.x) == p.stall_cta && tile_no == 0) {  // test hook only
-          ok = __any_sync(0xffffffffu, stall_until_limit(ctl));
-          break;
-        }
       }
-      if (ok) mma_commit_elect(bar(L::kBarQEmpty + qb));
-    }
-    mma_commit_elect(bar(L::kBarDrain));
-    mbar_wait_drain(bar(L::kBarDrain), 0);
-    __syncwarp();
+      // Copies in flight land before the CTA ends.
+      if (lane == 0)
+        for (int i = max(0, e - L::kStages); i < e; ++i)
+          mbar_wait_drain(bar(L::kBarKFull + i % L::kStages), (i / L::kStages) & 1);
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------ MMA issuer
+      const uint64_t d_k = smem_desc(base + L::kOffK, 16u, L::kAtom, L::kSwizzle);
+      const uint64_t d_q = smem_desc(base + L::kOffQ, 16u, L::kAtom, L::kSwizzle);
+      auto wait = [&](int i, int phase) { return __all_sync(0xffffffffu, mbar_wait_soon(bar(i), phase & 1, ctl)); };
+      bool ok = *abort_flag == 0;
+      int e = 0, tile_no = 0;
+      for (int seg = 0; ok; ++seg) {
+        const int qb = seg & 1;
+        ok = wait(L::kBarWork + qb, seg >> 1);
+        if (!ok) break;
+        const int ntiles = works[qb].ntiles, ntok = works[qb].ntok;
+        if (ntiles == 0) break;
+        ok = wait(L::kBarQFull + qb, seg >> 1);
+        const uint64_t qd = d_q + ((static_cast<uint32_t>(qb) * L::kQBytes) >> 4);
+        const uint32_t idesc = kPaged ? idesc_e4m3_f32(128, 16, false) : idesc_bf16_f32(128, 16, false, false);
+        const uint32_t id = (idesc & ~(0x3fu << 17)) | (static_cast<uint32_t>(ntok * Hp >> 3) << 17);
+        for (int i = 0; ok && i < ntiles; ++i, ++tile_no) {
+          const int acc = tile_no & 1;
+          if (tile_no >= 2) ok = wait(L::kBarAccEmpty + acc, (tile_no >> 1) - 1);
+          const uint32_t d = tmem + static_cast<uint32_t>(acc) * kCols;
+  #pragma unroll
+          for (int c = 0; c < L::kPieces; ++c, ++e) {
+            const int st = e % L::kStages;
+            ok = ok && wait(L::kBarKFull + st, e / L::kStages);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kd = d_k + ((static_cast<uint32_t>(st) * L::kPieceBytes) >> 4);
+            if constexpr (kPaged) {
+  #pragma unroll
+              for (int part = 1; part >= 0; --part)        // (the small pieces first: see the error bound)
+  #pragma unroll
+                for (int k = 0; k < D / 32; ++k)
+                  mma8_ss(d, kd + (k * 32u >> 4), qd + ((part * L::kQPartBytes + k * 32u) >> 4), id, part == 0 || k != 0);
+            } else {
+  #pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma16_ss(d, kd + (k * 32u >> 4), qd + ((c * L::kQPartBytes + k * 32u) >> 4), id, (c | k) != 0);
+            }
+            mma_commit_elect(bar(L::kBarKEmpty + st));
+          }
+          if (!ok) break;
+          mma_commit_elect(bar(L::kBarAccFull + acc));
+          if (static_cast<int>(blockIdx.x) == p.stall_cta && tile_no == 0) {  // test hook only
+            ok = __any_sync(0xffffffffu, stall_until_limit(ctl));
+            break;
+          }
+        }
+        if (ok) mma_commit_elect(bar(L::kBarQEmpty + qb));
+      }
+      mma_commit_elect(bar(L::kBarDrain));
+      mbar_wait_drain(bar(L::kBarDrain), 0);
+      __syncwarp();
     }
   } else if (warp >= kHelpWarp0) {
     reg_dealloc<kOtherRegs>();

@@ -152,6 +152,26 @@ def test_values_that_are_no_numbers():
     assert torch.equal(indexer_topk(a[0], a[1], dirty, 64, first_position=100), seen)
 
 
+def test_queries_and_weights_that_are_no_numbers():
+    """The choice is then unspecified, but it is one: distinct positions that the token sees,
+    ascending, as many as it may have."""
+    q, w, k = _inputs(1, 40, 700, 16, 64, 12)
+    q[0, 1, 3, 5], q[0, 2, 0, 0], q[0, 3] = math.nan, math.inf, math.inf
+    w[0, 4, 2], w[0, 5, 1], w[0, 6] = math.nan, math.inf, -math.inf
+    q[0, 7], w[0, 8] = 3e38, 3e38
+    for topk, block in ((100, 1), (600, 1), (128, 32)):
+        got = indexer_topk(q, w, k, topk, block, check_status=True)
+        good = ref.flat(q, w, k, topk, block)
+        for t in range(40):
+            n = 660 + t + 1
+            mine = got[0, t][got[0, t] >= 0].tolist()
+            assert mine == sorted(set(mine)) and mine[-1] < n and got[0, t, len(mine):].eq(-1).all()
+            if block == 1:
+                assert len(mine) == min(topk, n)
+            if t == 0 or t > 8:
+                assert torch.equal(got[0, t].long(), good[0, t])
+
+
 @pytest.mark.parametrize("S_kv,topk,block", [(8193, 2048, 1), (20000, 2048, 1), (65536, 1000, 1), (70001, 2048, 1), (70001, 4096, 128)])
 def test_long_rows(S_kv, topk, block):
     q, w, k = _inputs(1, 3, S_kv, 16, 64, 2)
