@@ -106,6 +106,33 @@ __device__ __forceinline__ void mma16_ss(uint32_t d_tmem, uint64_t a_desc, uint6
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
 
+// 16 consecutive columns of the warp's lanes at t, and (kBoth) 16 at t + 64; one wait.
+template <bool kBoth>
+__device__ __forceinline__ void tmem_ld16_and_64(uint32_t t, float (&v)[32]) {
+  uint32_t r[32] = {};
+  if constexpr (kBoth)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+          "=r"(r[30]), "=r"(r[31])
+        : "r"(t), "r"(t + 64)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t)
+        : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 __device__ __forceinline__ float relu(float x) {         // (a NaN stays one)
   float y;
   asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
@@ -604,40 +631,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           float scale = 1.f;
           if constexpr (kPaged) scale = reinterpret_cast<const float*>(smem + L::kOffMeta)[(tile_no % L::kMeta) * 8 + (my >> page_shift)];
           const uint32_t t_acc = tmem + lanes + static_cast<uint32_t>(acc) * kCols + static_cast<uint32_t>(col0);
-          // The sums of its tokens (columns behind the last token's are of no token).
+          // The sums of its tokens, 16 columns of the first 64 beside 16 of the last (four
+          // chains of additions in a load's shadow, not two).
           float sum[kTok] = {};
-          auto sums = [&](auto plain_tag) {
-            float2 a0 = {}, a1 = {};
+          auto sums = [&](auto plain_tag, auto both_tag) {
+            constexpr bool kBoth = decltype(both_tag)::value;
+            float2 a[4];
+            auto four = [&](int at, const float* x, float2& u, float2& v) {
+              u = fma2(make_float2(w[at], w[at + 1]), make_float2(relu(x[0]), relu(x[1])), u);
+              float y, z;
+              if constexpr (decltype(plain_tag)::value) {
+                y = 2.f * relu(x[2]);
+                z = 2.f * relu(x[3]);
+              } else {
+                y = twice_relu(x[2]);
+                z = twice_relu(x[3]);
+              }
+              v = fma2(make_float2(w[at + 2], w[at + 3]), make_float2(y, z), v);
+            };
 #pragma unroll
-            for (int u = 0; u < kMine / 32; ++u) {
-              if (col0 + u * 32 >= ntok * Hp) break;     // (the sums behind are of no token)
+            for (int u = 0; u < 4; ++u) {
               float x[32];
-              tmem_ld32(t_acc + u * 32, x);
+              tmem_ld16_and_64<kBoth>(t_acc + u * 16, x);
 #pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const int at = u * 32 + 4 * c;
-                if (at % Hp == 0) a0 = a1 = make_float2(0.f, 0.f);
-                a0 = fma2(make_float2(w[at], w[at + 1]), make_float2(relu(x[4 * c]), relu(x[4 * c + 1])), a0);
-                float y = x[4 * c + 2], z = x[4 * c + 3];
-                if constexpr (decltype(plain_tag)::value) {
-                  y = 2.f * relu(y);
-                  z = 2.f * relu(z);
-                } else {
-                  y = twice_relu(y);
-                  z = twice_relu(z);
+              for (int c = 0; c < 4; ++c) {
+                const int at = u * 16 + 4 * c;
+                if (at % Hp == 0) a[0] = a[1] = a[2] = a[3] = make_float2(0.f, 0.f);
+                four(at, x + 4 * c, a[0], a[1]);
+                if constexpr (kBoth) four(64 + at, x + 16 + 4 * c, a[2], a[3]);
+                if ((at + 4) % (Hp < 64 ? Hp : 64) == 0) {
+                  const float first = (a[0].x + a[0].y) + (a[1].x + a[1].y), second = (a[2].x + a[2].y) + (a[3].x + a[3].y);
+                  if constexpr (Hp == 128) {
+                    sum[0] = first + second;
+                  } else {
+                    sum[at / Hp] = first;
+                    if constexpr (kBoth) sum[kTok / 2 + at / Hp] = second;
+                  }
                 }
-                a1 = fma2(make_float2(w[at + 2], w[at + 3]), make_float2(y, z), a1);
-                if ((at + 4) % Hp == 0) sum[at / Hp] = (a0.x + a0.y) + (a1.x + a1.y);
               }
             }
           };
-          sums(std::false_type{});
+          const bool both = ntok * Hp - col0 > 64;
+          if (both)
+            sums(std::false_type{}, std::true_type{});
+          else
+            sums(std::false_type{}, std::false_type{});
           if constexpr (!kPaged) {
             // (A logit of -infinity, of a key row that holds infinities: e4m3 has none.)
             bool again = false;
 #pragma unroll
             for (int k = 0; k < kTok; ++k) again = again || (tok0 + k < ntok && sum[k] != sum[k]);
-            if (__any_sync(0xffffffffu, again)) sums(std::true_type{});
+            if (__any_sync(0xffffffffu, again)) sums(std::true_type{}, std::true_type{});
           }
           tc_fence_before();
           __syncwarp();
