@@ -1129,7 +1129,9 @@ cudaError_t launch_select(const TopkParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 // Long rows, or few tokens with more than short ones: 1024 threads and one CTA per SM;
-// else 256 and three.
+// else 256 and three.  H = 64, D = 128, topk = 2048, us a call with 256 and with 1024: 16
+// paged tokens over 8192 positions 49 and 42, 150 over 12000 98 and 90; 300 over 12000 132
+// and 147, S = 8192 729 and 1156.
 template <int D, bool kPaged>
 cudaError_t launch_select(const TopkParams& p, cudaStream_t stream) {
   return p.ld > SelLayout<D, 256>::kCap || (p.toks <= kSMs && p.ld > 4096) ? launch_select<D, kPaged, 1024>(p, stream)
@@ -1140,7 +1142,9 @@ cudaError_t launch_select(const TopkParams& p, cudaStream_t stream) {
 // Host
 // ---------------------------------------------------------------------------
 constexpr int64_t kLim = int64_t{1} << 31;
-// Bytes of scores that a chunk of tokens may take.
+// Bytes of scores that a chunk of tokens may take: half of L2, from which the choice reads
+// them.  (S = 8192, H = 64, topk = 2048: 955 us with 16 MB, 728 with 64, 710 with 256 or 1024,
+// whose workspace a caller would have to hold.)
 constexpr int64_t kChunkBytes = int64_t{64} << 20;
 
 smqa_status refuse(smqa_status st, const char* why) {
@@ -1202,29 +1206,42 @@ smqa_status check_paged_topk(const smqa_paged_shape& s) {
   return SMQA_OK;
 }
 
-// Key rows as 8-bit or bf16 boxes of `box_rows` rows, swizzled as the tensor core reads them.
-bool encode_keys(CUtensorMap* m, const void* ptr, bool codes, int D, uint64_t rows, uint32_t box_rows) {
+// Boxes of 64 bf16 elements or D codes, swizzled as the tensor core reads them.
+bool encode(CUtensorMap* m, const void* ptr, bool codes, int D, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
   const auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
   if (!fn) {
     set_last_error("cuTensorMapEncodeTiled unavailable");
     return false;
   }
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), rows};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * (codes ? 1 : 2)};
-  const cuuint32_t box[2] = {codes ? static_cast<cuuint32_t>(D) : 64u, box_rows}, estr[2] = {1, 1};
-  auto encode = [&] {
-    return fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
+  const cuuint32_t estr[3] = {1, 1, 1};
+  auto call = [&] {
+    return fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, box,
               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, codes && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
-  CUresult r = encode();
-  if (r == CUDA_ERROR_INVALID_CONTEXT && make_context_current()) r = encode();
+  CUresult r = call();
+  if (r == CUDA_ERROR_INVALID_CONTEXT && make_context_current()) r = call();
   if (r != CUDA_SUCCESS) set_last_error("cuTensorMapEncodeTiled failed");
   return r == CUDA_SUCCESS;
 }
+// Key rows, `box_rows` at a time.
+bool encode_keys(CUtensorMap* m, const void* ptr, bool codes, int D, uint64_t rows, uint32_t box_rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), rows};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * (codes ? 1 : 2)};
+  const cuuint32_t box[2] = {codes ? static_cast<cuuint32_t>(D) : 64u, box_rows};
+  return encode(m, ptr, codes, D, 2, dims, strides, box);
+}
+// The queries [T, H, D], a group of tokens at a time, their heads padded with zeros.
+bool encode_queries(CUtensorMap* m, const void* ptr, int H, int D, uint64_t T) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), T};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(H) * D * 2};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(padded_heads(H)), static_cast<cuuint32_t>(group_tokens(H))};
+  return encode(m, ptr, false, D, 3, dims, strides, box);
+}
 
 // The chunks of one call, one after another.
-smqa_status run_topk(TopkParams p, const TopkPlan& pl, const CUtensorMap& tm, int D, bool paged, int64_t per_batch_units,
+smqa_status run_topk(TopkParams p, const TopkPlan& pl, const CUtensorMap& tm_k, const CUtensorMap& tm_q, int D, bool paged, int64_t per_batch_units,
                      void* workspace, cudaStream_t stream) {
   cudaError_t e;
   p.status = device_status_word(&e);
@@ -1246,7 +1263,7 @@ smqa_status run_topk(TopkParams p, const TopkPlan& pl, const CUtensorMap& tm, in
     p.units = std::min(pl.chunk_units, pl.units - u);
     p.tok0 = first_of(u);
     p.toks = first_of(u + p.units) - p.tok0;
-    e = launch_topk_score(tm, p, D, paged, stream);
+    e = launch_topk_score(tm_k, tm_q, p, D, paged, stream);
     if (e != cudaSuccess) return cuda_failure(e, "topk score launch");
     e = launch_topk_select(p, D, paged, stream);
     if (e != cudaSuccess) return cuda_failure(e, "topk select launch");
@@ -1294,8 +1311,10 @@ smqa_status smqa_indexer_topk(const void* index_q, const float* weights, const v
   const TopkPlan pl = plan_topk(s.S_kv, shift_of(block_size), s.H, false, s.B, s.S);
   st = check_workspace(workspace, workspace_bytes, pl.bytes);
   if (st != SMQA_OK) return st;
-  CUtensorMap tm;
-  if (!encode_keys(&tm, index_k, false, s.D, static_cast<uint64_t>(s.B) * s.S_kv, kTile)) return SMQA_ERR_CUDA;
+  CUtensorMap tm, tm_q;
+  if (!encode_keys(&tm, index_k, false, s.D, static_cast<uint64_t>(s.B) * s.S_kv, kTile) ||
+      !encode_queries(&tm_q, index_q, s.H, s.D, static_cast<uint64_t>(s.B) * s.S))
+    return SMQA_ERR_CUDA;
   TopkParams p{};
   p.q = static_cast<const __nv_bfloat16*>(index_q);
   p.w = weights;
@@ -1311,7 +1330,7 @@ smqa_status smqa_indexer_topk(const void* index_q, const float* weights, const v
   p.block_shift = shift_of(block_size);
   p.recent = recent;
   p.out = topk_idxs;
-  return run_topk(p, pl, tm, s.D, false, (s.S + group_tokens(s.H) - 1) / group_tokens(s.H), workspace, stream);
+  return run_topk(p, pl, tm, tm_q, s.D, false, (s.S + group_tokens(s.H) - 1) / group_tokens(s.H), workspace, stream);
 }
 
 size_t smqa_paged_indexer_topk_workspace_bytes(smqa_paged_shape s, int32_t block_size) {
@@ -1362,7 +1381,7 @@ smqa_status smqa_paged_indexer_topk(const void* index_q, const float* weights, c
   p.recent = recent;
   p.out = topk_idxs;
   p.zero_padding = (flags & SMQA_FLAG_ZERO_PADDING) ? 1 : 0;
-  return run_topk(p, pl, tm, s.D, true, pl.units, workspace, stream);
+  return run_topk(p, pl, tm, tm, s.D, true, pl.units, workspace, stream);
 }
 
 }  // extern "C"

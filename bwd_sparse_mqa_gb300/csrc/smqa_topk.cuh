@@ -48,7 +48,8 @@ __host__ __device__ inline int entry_shift(int block_shift) { return block_shift
 inline int padded_heads(int H) { return H <= 16 ? 16 : H <= 32 ? 32 : H <= 64 ? 64 : 128; }
 inline int group_tokens(int H) { return 256 / padded_heads(H); }
 
-cudaError_t launch_topk_score(const CUtensorMap& tm_k, const TopkParams& p, int D, bool paged, cudaStream_t stream);
+// (tm_q: contiguous keys only.)
+cudaError_t launch_topk_score(const CUtensorMap& tm_k, const CUtensorMap& tm_q, const TopkParams& p, int D, bool paged, cudaStream_t stream);
 cudaError_t launch_topk_select(const TopkParams& p, int D, bool paged, cudaStream_t stream);
 
 // Scores as integers that order like them, equal ones (0 and -0) alike; a NaN

@@ -19,17 +19,26 @@
 // buffers); key tiles come by TMA through a ring of 128-byte pieces.  Tokens that
 // see no more rows than they choose need no scores and are left out.
 //
-// 512 threads: warps 0-7 epilogue, 8 walks through the groups and issues the key
-// tiles' copies, 9 feeds the tensor core, 12-15 bring the queries and weights of the
-// next group and bound the key rows' lengths (which the choice's error bound needs).
-// An epilogue thread keeps the weights of its 128 columns in registers for a whole
-// group: read from shared memory for every tile, 4 bytes a lane, they took as long as
-// the tensor core (1024 clocks a tile of 256 columns) from the bandwidth that it needs
-// for its operands.  A wide tile's columns are shared by the two warpgroups, narrow
-// tiles (up to 128 columns) go to them in turn.  The accumulator is given back before
-// the sums are made into keys and written (some 400 clocks a token).  Half of the ReLUs
-// are x + |x| with the weight halved: an addition, where a maximum takes twice as long
-// and waits for the unit of the integer operations.
+// Warps: the epilogue's; one that issues the key tiles' copies; one that feeds the tensor
+// core; two that walk through the groups, a group ahead of the tensor core, and bring its
+// queries and weights; and with paged keys four that bound the key rows' lengths as the
+// tiles pass (which the choice's error bound needs; contiguous rows are bounded once, by
+// the two).  Described and fetched only behind a group's own copies, as it was, queries
+// came late: a part of 16 tiles waited 12000 clocks for them.
+//
+// What bounds it is the epilogue, not the tensor core (1024 clocks a tile of 256 columns;
+// with half of the products left out S = 8192 took 377 us of 385): a thread's chain of
+// barrier, loads, sums and stores.  With contiguous keys and up to 64 heads four warpgroups
+// share a tile's columns, 64 each, and hide each other's latencies (1000 queries over 32768
+// positions of 64 heads: 404 us with two of 128 columns, 325 with four; S = 8192 in four
+// chunks 401 and 323).  More than 64 heads need a thread that sums 128 columns; paged keys,
+// the two warpgroups' registers for the four warps that bound the rows.  Narrower tiles go
+// to the warpgroups in turn.  A thread keeps the weights of its columns in registers for a
+// whole group: read from shared memory for every tile, 4 bytes a lane, they took as long as
+// the tensor core from the bandwidth that it needs for its operands.  The accumulator is
+// given back before the sums are made into keys and written.  Half of the ReLUs are x + |x|
+// with the weight halved: an addition, where a maximum takes twice as long and waits for
+// the unit of the integer operations.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -40,14 +49,26 @@ namespace smqa {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kHelpWarp0 = 12;
 constexpr int kCols = 256;                               // accumulator columns
-constexpr int kMine = 128;                               // columns of an epilogue warpgroup
-// Registers of the epilogue's warpgroups and of the other two: their sum is what the
-// block is launched with.
-constexpr int kEpilogueRegs = 192, kOtherRegs = 64;
-static_assert(2 * kEpilogueRegs + 2 * kOtherRegs <= 512 && kLoadWarp == 8, "registers of the launch, roles by warpgroup");
+
+// The warps' roles.
+template <bool kPaged, int Hp>
+struct Roles {
+  static constexpr int kGroups = kPaged || Hp == 128 ? 2 : 4;  // epilogue warpgroups
+  static constexpr int kMine = kCols / kGroups;          // columns of one of them
+  static constexpr int kEpilogueWarps = 4 * kGroups;
+  static constexpr int kLoadWarp = kEpilogueWarps, kMmaWarp = kLoadWarp + 1;
+  static constexpr int kHelpWarp0 = kLoadWarp + 2, kHelpers = 2;
+  static constexpr int kBoundWarp0 = kLoadWarp + 4, kBounders = kPaged ? 4 : 0;
+  static constexpr int kThreads = 32 * (kBoundWarp0 + kBounders);
+  // Registers of the epilogue's warpgroups and of the others: their sum is what the block
+  // is launched with.
+  static constexpr int kEpilogueRegs = kGroups == 2 ? 192 : 104, kOtherRegs = 64;
+  static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+  static_assert(kThreads % 128 == 0 && (kThreads / 128 - kGroups) * kOtherRegs + kGroups * kEpilogueRegs <= kThreads / 128 * kLaunchRegs,
+                "registers of the launch, roles by warpgroup");
+};
+constexpr int kMaxWarps = 20;
 constexpr int kMaxGroup = 16;                            // tokens of a group
 
 // What the CTA does for one group (or the part of one that its range holds).
@@ -75,8 +96,8 @@ struct ScoreLayout {
   static constexpr uint32_t kOffW = kOffK + kStages * kPieceBytes;      // float [2][256]
   static constexpr uint32_t kOffMeta = kOffW + 2 * kCols * 4;           // float [kMeta][8]
   static constexpr uint32_t kOffWork = kOffMeta + kMeta * 8 * 4;        // Work [2]
-  static constexpr uint32_t kOffSum = kOffWork + 2 * sizeof(Work);      // int64 [16], then the range's start
-  static constexpr uint32_t kOffBar = kOffSum + 16 * 8 + 32;
+  static constexpr uint32_t kOffSum = kOffWork + 2 * sizeof(Work);      // int64 [kMaxWarps], then the range's start
+  static constexpr uint32_t kOffBar = kOffSum + kMaxWarps * 8 + 32;
   static constexpr int kBarKFull = 0;
   static constexpr int kBarKEmpty = kBarKFull + kStages;
   static constexpr int kBarAccFull = kBarKEmpty + kStages;  // [2]
@@ -84,7 +105,8 @@ struct ScoreLayout {
   static constexpr int kBarWork = kBarAccEmpty + 2;         // [2] work described
   static constexpr int kBarQFull = kBarWork + 2;            // [2] queries and weights there
   static constexpr int kBarQEmpty = kBarQFull + 2;          // [2]
-  static constexpr int kBarDrain = kBarQEmpty + 2;
+  static constexpr int kBarQFirst = kBarQEmpty + 2;         // paged: those of the first part
+  static constexpr int kBarDrain = kBarQFirst + 1;
   static constexpr int kNumBars = kBarDrain + 1;
   static constexpr uint32_t kOffCtl = kOffBar + 8 * kNumBars;  // TMEM base, abort flag
   static constexpr uint32_t kSmem = kOffCtl + 16 + 1024;
@@ -104,6 +126,14 @@ __device__ __forceinline__ void mma16_ss(uint32_t d_tmem, uint64_t a_desc, uint6
       "setp.ne.b32 p, %4, 0;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
 }
 
 // 16 consecutive columns of the warp's lanes at t, and (kBoth) 16 at t + 64; one wait.
@@ -185,9 +215,12 @@ __device__ __forceinline__ int64_t unit_tiles(const TopkParams& p, int64_t u, in
 }
 
 template <int D, bool kPaged, int Hp>
-__global__ void __launch_bounds__(kThreads, 1)
-    smqa_topk_score_kernel(const __grid_constant__ CUtensorMap tm_k, const TopkParams p) {
+__global__ void __launch_bounds__(Roles<kPaged, Hp>::kThreads, 1)
+    smqa_topk_score_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, const TopkParams p) {
   using L = ScoreLayout<D, kPaged>;
+  using Ro = Roles<kPaged, Hp>;
+  constexpr int kThreads = Ro::kThreads, kMine = Ro::kMine;
+  static_assert(kThreads <= 32 * kMaxWarps, "room for the warps' sums");
   constexpr int kGroup = kCols / Hp;
   extern __shared__ uint8_t smem_raw[];
   uint32_t base = smem_u32(smem_raw);
@@ -200,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffCtl + 4);
   const WaitCtl ctl{abort_flag, p.status, p.limit_ns};
   int64_t* warp_sum = reinterpret_cast<int64_t*>(smem + L::kOffSum);
-  int64_t* start = warp_sum + 16;                        // unit, tiles of it before the range, tiles of the range
+  int64_t* start = warp_sum + kMaxWarps;                        // unit, tiles of it before the range, tiles of the range
   Work* works = reinterpret_cast<Work*>(smem + L::kOffWork);
 
   if (tid == 0) {
@@ -210,16 +243,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(L::kBarAccFull + i), 1);
-      mbar_init(bar(L::kBarAccEmpty + i), 8);
+      mbar_init(bar(L::kBarAccEmpty + i), Ro::kEpilogueWarps);
       mbar_init(bar(L::kBarWork + i), 1);
-      mbar_init(bar(L::kBarQFull + i), 4);
-      mbar_init(bar(L::kBarQEmpty + i), 1 + 8 + 4);      // tensor core, epilogue, helpers
+      mbar_init(bar(L::kBarQFull + i), Ro::kHelpers + (kPaged ? 0 : 1));  // (1: the copy)
+      mbar_init(bar(L::kBarQEmpty + i), 1 + Ro::kEpilogueWarps + Ro::kBounders);  // (1: tensor core)
     }
+    mbar_init(bar(L::kBarQFirst), Ro::kHelpers + Ro::kBounders);
     mbar_init(bar(L::kBarDrain), 1);
     start[2] = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) tmem_alloc(base + L::kOffCtl, 2 * kCols);
+  if (warp == Ro::kMmaWarp) tmem_alloc(base + L::kOffCtl, 2 * kCols);
   // (So far beside the kernel before, whose results are read from here on.)
   grid_dependency_wait();
   grid_dependents_launch();
@@ -265,56 +299,84 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int64_t count_all = start[2];
+  // The barrier that a part's queries and weights arrive on, and its phase.
+  auto q_bar = [&](int seg) { return kPaged && seg == 0 ? L::kBarQFirst : L::kBarQFull + (seg & 1); };
+  auto q_phase = [&](int seg) { return !kPaged ? seg >> 1 : seg == 0 ? 0 : (seg - 1) >> 1; };
+  // Paged: two e4m3 pieces of each query row times 2^k, which its weight takes back, by
+  // warp `me` of n; four lanes share a row.  (A row with a NaN or an infinity becomes NaN.)
+  // The next rows are asked for before these are written.
+  auto bring = [&](int me, int n, int qb, int64_t tok, int ntok) {
+    float* ws = reinterpret_cast<float*>(smem + L::kOffW) + qb * kCols;
+    const uint32_t to = base + L::kOffQ + static_cast<uint32_t>(qb) * L::kQBytes;
+    constexpr int kSeg = D / 4;                          // elements per lane
+    const int part = lane & 3;
+    uint4 v[kSeg / 8], next[kSeg / 8];
+    float w = 0.f, next_w = 0.f;
+    auto ask = [&](int r0, uint4 (&x)[kSeg / 8], float& xw) {
+      const int r = r0 + (lane >> 2), h = r % Hp;
+      const bool there = r0 < ntok * Hp && h < p.H;
+#pragma unroll
+      for (int c = 0; c < kSeg / 8; ++c)
+        x[c] = there ? load(reinterpret_cast<const uint4*>(p.q + ((tok + r / Hp) * p.H + h) * D + part * kSeg) + c)
+                     : make_uint4(0, 0, 0, 0);
+      xw = there ? load(p.w + (tok + r / Hp) * p.H + h) : 0.f;
+    };
+    ask(me * 8, v, w);
+    for (int r0 = me * 8; r0 < ntok * Hp; r0 += 8 * n) {
+      ask(r0 + 8 * n, next, next_w);
+      const int r = r0 + (lane >> 2);
+      uint32_t m = 0;
+#pragma unroll
+      for (int c = 0; c < kSeg / 8; ++c)
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu),
+                                 __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu)));
+      m = max(m & 0xffffu, m >> 16);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int k = query_exponent(m);
+      const float f = m >= 0x7f80u ? __uint_as_float(0x7fffffffu) : pow2f(k);
+      if (part == 0) ws[r] = w * pow2f(-k);
+#pragma unroll
+      for (int c = 0; c < kSeg / 16; ++c) {              // 16 elements: 16 bytes of each piece
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k2 = 0; k2 < 4; ++k2) {
+          const uint4& x = v[2 * c + (k2 >> 1)];
+          const uint32_t a = (k2 & 1) ? x.z : x.x, b = (k2 & 1) ? x.w : x.y;
+          uint16_t h0, l0, h1, l1;
+          split_query(make_float2(__uint_as_float(a << 16) * f, __uint_as_float(a & 0xffff0000u) * f), h0, l0);
+          split_query(make_float2(__uint_as_float(b << 16) * f, __uint_as_float(b & 0xffff0000u) * f), h1, l1);
+          hi[k2] = h0 | (static_cast<uint32_t>(h1) << 16);
+          lo[k2] = l0 | (static_cast<uint32_t>(l1) << 16);
+        }
+        const int piece = part * (kSeg / 16) + c;
+        const uint32_t at = to + r * L::kPitch +
+                            ((L::kPitch == 128 ? piece ^ (r & 7) : piece ^ ((r >> 1) & 3)) << 4);
+        st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+        st_shared_v4(at + L::kQPartBytes, lo[0], lo[1], lo[2], lo[3]);
+      }
+#pragma unroll
+      for (int c = 0; c < kSeg / 8; ++c) v[c] = next[c];
+      w = next_w;
+    }
+    fence_proxy_async_smem();
+  };
 
-  if (count_all == 0 && (kPaged || warp < kHelpWarp0)) {
+  if (count_all == 0 && (kPaged || warp < Ro::kLoadWarp)) {
     // nothing to do
-  } else if (warp >= kLoadWarp && warp < kHelpWarp0) {
-    reg_dealloc<kOtherRegs>();                           // (the warpgroup's other warps have no role)
-    if (warp == kLoadWarp) {
-      // ------------------------------------------------------------ walk and copy
-      int64_t u = start[0], skip = start[1], left = count_all;
-      int part = 0, e = 0, tile_no = 0;                    // pieces and tiles so far
-      int64_t first;
-      int count = unit_tokens<kPaged>(p, u, kGroup, first);
+  } else if (warp >= Ro::kLoadWarp) {
+    reg_dealloc<Ro::kOtherRegs>();
+    auto wait = [&](int i, int phase) { return __all_sync(0xffffffffu, mbar_wait_soon(bar(i), phase & 1, ctl)); };
+    if (warp == Ro::kLoadWarp && count_all > 0) {
+      // ------------------------------------------------------------ copies of key tiles
       bool ok = *abort_flag == 0;
-      for (int seg = 0;; ++seg) {
-        // The next part with tiles in the range.
-        int end = 0, req = 0, tiles = 0;
-        if (left > 0) {
-          while (true) {
-            if (part >= count) {
-              count = unit_tokens<kPaged>(p, ++u, kGroup, first);
-              part = 0;
-            }
-            tiles = part_tiles<kPaged>(p, first, count, part, end, req);
-            if (skip < tiles) break;
-            skip -= tiles;
-            part = end;
-          }
-        }
-        if (seg >= 2) ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarQEmpty + (seg & 1)), ((seg >> 1) - 1) & 1, ctl));
+      int e = 0, tile_no = 0;                              // pieces and tiles so far
+      for (int seg = 0; ok; ++seg) {
+        ok = wait(L::kBarWork + (seg & 1), seg >> 1);
         if (!ok) break;
-        Work* wk = works + (seg & 1);
-        const int tile0 = static_cast<int>(skip);
-        const int ntiles = static_cast<int>(min(left, static_cast<int64_t>(tiles) - skip));
-        if (lane < kMaxGroup) {
-          int n = 0, r;
-          if (left > 0 && lane < end - part) n = visible<kPaged>(p, first + part + lane, r);
-          wk->n[lane] = n > p.topk ? n : 0;
-        }
-        if (lane == 0) {
-          wk->tok = first + part;
-          wk->ntok = end - part;
-          wk->tile0 = tile0;
-          wk->ntiles = left > 0 ? ntiles : 0;
-          wk->req = req;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kBarWork + (seg & 1)));
-        if (left <= 0) break;
-        left -= ntiles;
-        skip = 0;
-        part = end;
+        const Work& wk = works[seg & 1];
+        const int ntiles = wk.ntiles, tile0 = wk.tile0, req = wk.req;
+        if (ntiles == 0) break;
         // Paged: lane = page of a tile.  The pages of the tile after next and the scales of the
         // next one are asked for before a tile's copies are issued (one after another, the
         // loads took 1200 cycles a tile).
@@ -375,11 +437,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = max(0, e - L::kStages); i < e; ++i)
           mbar_wait_drain(bar(L::kBarKFull + i % L::kStages), (i / L::kStages) & 1);
       __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp == Ro::kMmaWarp && count_all > 0) {
       // ------------------------------------------------------------ MMA issuer
       const uint64_t d_k = smem_desc(base + L::kOffK, 16u, L::kAtom, L::kSwizzle);
       const uint64_t d_q = smem_desc(base + L::kOffQ, 16u, L::kAtom, L::kSwizzle);
-      auto wait = [&](int i, int phase) { return __all_sync(0xffffffffu, mbar_wait_soon(bar(i), phase & 1, ctl)); };
       bool ok = *abort_flag == 0;
       int e = 0, tile_no = 0;
       for (int seg = 0; ok; ++seg) {
@@ -388,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const int ntiles = works[qb].ntiles, ntok = works[qb].ntok;
         if (ntiles == 0) break;
-        ok = wait(L::kBarQFull + qb, seg >> 1);
+        ok = wait(q_bar(seg), q_phase(seg));
         const uint64_t qd = d_q + ((static_cast<uint32_t>(qb) * L::kQBytes) >> 4);
         const uint32_t idesc = kPaged ? idesc_e4m3_f32(128, 16, false) : idesc_bf16_f32(128, 16, false, false);
         const uint32_t id = (idesc & ~(0x3fu << 17)) | (static_cast<uint32_t>(ntok * Hp >> 3) << 17);
@@ -428,118 +489,140 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit_elect(bar(L::kBarDrain));
       mbar_wait_drain(bar(L::kBarDrain), 0);
       __syncwarp();
-    }
-  } else if (warp >= kHelpWarp0) {
-    reg_dealloc<kOtherRegs>();
-    // ------------------------------------------------------------ queries, weights, lengths
-    const int ht = tid - 32 * kHelpWarp0, hw = warp - kHelpWarp0;  // thread of 128
-    if constexpr (!kPaged) {
-      // Bounds of the key rows' lengths, 32 rows a warp, over all CTAs.
-      const int tiles = static_cast<int>(p.norm_ld) / 4;
-      for (int64_t i = blockIdx.x; i < static_cast<int64_t>(p.B) * tiles; i += gridDim.x) {
-        const int64_t b = i / tiles;
-        const int j = static_cast<int>(i - b * tiles) * kTile + ht;
-        float s = 0.f;
-        if (j < p.S_kv) {
-          const uint4* row = reinterpret_cast<const uint4*>(p.k + (b * p.S_kv + j) * D);
-#pragma unroll 8
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = load(row + c);
-            const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float a = __uint_as_float(w4[k] << 16), d = __uint_as_float(w4[k] & 0xffff0000u);
-              s = fmaf(a, a, fmaf(d, d, s));
-            }
-          }
-          // (An infinite row's scores are infinite or NaN, and need no bound.)
-          s = s < INFINITY ? sqrtf(s) * 1.0001f : s == INFINITY ? s : 0.f;
-          if (s == INFINITY) {                           // finite, but its square is not?
+    } else if (warp >= Ro::kHelpWarp0 && warp < Ro::kBoundWarp0) {
+      // ------------------------------------------------------------ walk, queries, weights
+      // (A part is described as soon as its buffers are free, a part ahead of the tensor core.)
+      const int hw = warp - Ro::kHelpWarp0;
+      if constexpr (!kPaged) {
+        // Bounds of the key rows' lengths, 32 rows a warp, over all CTAs.
+        const int64_t all = p.B * p.norm_ld, step = static_cast<int64_t>(gridDim.x) * Ro::kHelpers;
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * Ro::kHelpers + hw; i < all; i += step) {
+          const int64_t b = i / p.norm_ld;
+          const int j = static_cast<int>(i - b * p.norm_ld) * 32 + lane;
+          float s = 0.f;
+          if (j < p.S_kv) {
+            const uint4* row = reinterpret_cast<const uint4*>(p.k + (b * p.S_kv + j) * D);
+  #pragma unroll 8
             for (int c = 0; c < D / 8; ++c) {
               const uint4 v = load(row + c);
               const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-              for (int k = 0; k < 4; ++k)
-                if ((w4[k] & 0x7f80u) == 0x7f80u || (w4[k] & 0x7f800000u) == 0x7f800000u) s = 0.f;
+  #pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float a = __uint_as_float(w4[k] << 16), d = __uint_as_float(w4[k] & 0xffff0000u);
+                s = fmaf(a, a, fmaf(d, d, s));
+              }
+            }
+            // (An infinite row's scores are infinite or NaN, and need no bound.)
+            s = s < INFINITY ? sqrtf(s) * 1.0001f : s == INFINITY ? s : 0.f;
+            if (s == INFINITY) {                           // finite, but its square is not?
+              for (int c = 0; c < D / 8; ++c) {
+                const uint4 v = load(row + c);
+                const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+                for (int k = 0; k < 4; ++k)
+                  if ((w4[k] & 0x7f80u) == 0x7f80u || (w4[k] & 0x7f800000u) == 0x7f800000u) s = 0.f;
+              }
             }
           }
+          const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(s)));
+          if (lane == 0) p.norms[i] = m;
         }
-        const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(s)));
-        if (lane == 0) p.norms[i * 4 + hw] = m;
       }
-    }
-    bool ok = count_all > 0;
-    int e = 0;
-    for (int seg = 0; ok; ++seg) {
-      const int qb = seg & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarWork + qb), (seg >> 1) & 1, ctl));
-      if (!ok) break;
-      const Work& wk = works[qb];
-      const int ntok = wk.ntok, ntiles = wk.ntiles, tile0 = wk.tile0;
-      const int64_t tok = wk.tok;
-      if (ntiles == 0) break;
-      float* ws = reinterpret_cast<float*>(smem + L::kOffW) + qb * kCols;
-      const uint32_t to = base + L::kOffQ + static_cast<uint32_t>(qb) * L::kQBytes;
-      if constexpr (!kPaged) {
-        // The rows' 16-byte pieces, and the weights; zeros behind H.
-        for (int i = ht; i < ntok * Hp; i += 128) {
-          const int h = i % Hp;
-          ws[i] = h < p.H ? load(p.w + (tok + i / Hp) * p.H + h) : 0.f;
-        }
-        constexpr int kPer = D / 8;
-        for (int i = ht; i < ntok * Hp * kPer; i += 128) {
-          const int r = i / kPer, c = i % kPer, h = r % Hp;
-          const bool there = h < p.H;
-          const __nv_bfloat16* src = p.q + ((tok + r / Hp) * p.H + (there ? h : 0)) * D + c * 8;
-          cp_async_16_or_zero(to + (c >> 3) * L::kQPartBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), src, there);
-        }
-        cp_async_wait_all();
-      } else {
-        // Two e4m3 pieces of each row times 2^k, which its weight takes back: four lanes
-        // share a row.  (A row with a NaN or an infinity becomes NaN.)
-        constexpr int kSeg = D / 4;                      // elements per lane
-        for (int r0 = hw * 8; r0 < ntok * Hp; r0 += 32) {
-          const int r = r0 + (lane >> 2), h = r % Hp, part = lane & 3;
-          const bool there = h < p.H;
-          uint4 v[kSeg / 8];
-          uint32_t m = 0;
-#pragma unroll
-          for (int c = 0; c < kSeg / 8; ++c) {
-            v[c] = there ? load(reinterpret_cast<const uint4*>(p.q + ((tok + r / Hp) * p.H + h) * D + part * kSeg) + c)
-                         : make_uint4(0, 0, 0, 0);
-            m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu),
-                                     __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu)));
-          }
-          m = max(m & 0xffffu, m >> 16);
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          const int k = query_exponent(m);
-          const float f = m >= 0x7f80u ? __uint_as_float(0x7fffffffu) : pow2f(k);
-          if (part == 0) ws[r] = there ? load(p.w + (tok + r / Hp) * p.H + h) * pow2f(-k) : 0.f;
-#pragma unroll
-          for (int c = 0; c < kSeg / 16; ++c) {          // 16 elements: 16 bytes of each piece
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k2 = 0; k2 < 4; ++k2) {
-              const uint4& x = v[2 * c + (k2 >> 1)];
-              const uint32_t a = (k2 & 1) ? x.z : x.x, b = (k2 & 1) ? x.w : x.y;
-              uint16_t h0, l0, h1, l1;
-              split_query(make_float2(__uint_as_float(a << 16) * f, __uint_as_float(a & 0xffff0000u) * f), h0, l0);
-              split_query(make_float2(__uint_as_float(b << 16) * f, __uint_as_float(b & 0xffff0000u) * f), h1, l1);
-              hi[k2] = h0 | (static_cast<uint32_t>(h1) << 16);
-              lo[k2] = l0 | (static_cast<uint32_t>(l1) << 16);
+      bool ok = count_all > 0 && *abort_flag == 0;
+      int64_t u = start[0], skip = start[1], left = count_all, first = 0;
+      int issued = 0;                                      // copies of queries
+      int part = 0, count = ok ? unit_tokens<kPaged>(p, u, kGroup, first) : 0;
+      for (int seg = 0; ok; ++seg) {
+        const int qb = seg & 1;
+        if (hw == 0) {
+          // The next part with tiles in the range.
+          int end = 0, req = 0, tiles = 0;
+          if (left > 0) {
+            while (true) {
+              if (part >= count) {
+                count = unit_tokens<kPaged>(p, ++u, kGroup, first);
+                part = 0;
+              }
+              tiles = part_tiles<kPaged>(p, first, count, part, end, req);
+              if (skip < tiles) break;
+              skip -= tiles;
+              part = end;
             }
-            const int piece = part * (kSeg / 16) + c;
-            const uint32_t at = to + r * L::kPitch +
-                                ((L::kPitch == 128 ? piece ^ (r & 7) : piece ^ ((r >> 1) & 3)) << 4);
-            st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
-            st_shared_v4(at + L::kQPartBytes, lo[0], lo[1], lo[2], lo[3]);
           }
+          int n = 0, r;
+          if (left > 0 && lane < end - part) n = visible<kPaged>(p, first + part + lane, r);
+          if (seg >= 2) ok = wait(L::kBarQEmpty + qb, (seg >> 1) - 1);
+          if (!ok) break;
+          Work* wk = works + qb;
+          const int64_t ntiles = min(left, static_cast<int64_t>(tiles) - skip);
+          if (lane < kMaxGroup) wk->n[lane] = n > p.topk ? n : 0;
+          if (lane == 0) {
+            wk->tok = first + part;
+            wk->ntok = end - part;
+            wk->tile0 = static_cast<int>(skip);
+            wk->ntiles = left > 0 ? static_cast<int>(ntiles) : 0;
+            wk->req = req;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kBarWork + qb));
+          if (left <= 0) break;
+          left -= ntiles;
+          skip = 0;
+          part = end;
         }
+        ok = wait(L::kBarWork + qb, seg >> 1);
+        if (!ok) break;
+        const Work& wk = works[qb];
+        const int ntok = wk.ntok;
+        const int64_t tok = wk.tok;
+        if (wk.ntiles == 0) break;
+        if constexpr (!kPaged) {
+          // One copy of the group's rows for each 64 elements (zeros behind H; a group that is
+          // not full brings rows that no column takes), and the weights.
+          if (hw == 0 && lane == 0) {
+            mbar_arrive_expect_tx(bar(L::kBarQFull + qb), L::kQBytes);
+#pragma unroll
+            for (int c = 0; c < L::kQParts; ++c)
+              tma_load_3d(base + L::kOffQ + static_cast<uint32_t>(qb) * L::kQBytes + c * L::kQPartBytes, &tm_q, c * 64, 0,
+                          static_cast<int>(tok), bar(L::kBarQFull + qb));
+          }
+          __syncwarp();
+          issued = seg + 1;
+          float w[kCols / 64];
+#pragma unroll
+          for (int i = 0; i < kCols / 64; ++i) {
+            const int col = i * 64 + hw * 32 + lane, h = col % Hp;
+            w[i] = col < ntok * Hp && h < p.H ? load(p.w + (tok + col / Hp) * p.H + h) : 0.f;
+          }
+          float* ws = reinterpret_cast<float*>(smem + L::kOffW) + qb * kCols + hw * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < kCols / 64; ++i) ws[i * 64] = w[i];
+        } else {
+          bring(hw, seg == 0 ? Ro::kHelpers + Ro::kBounders : Ro::kHelpers, qb, tok, ntok);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(q_bar(seg)));
       }
-      fence_proxy_async_smem();
+      // Copies in flight land before the CTA ends.
+      if (hw == 0 && lane == 0)
+        for (int i = max(0, issued - 2); i < issued; ++i) mbar_wait_drain(bar(L::kBarQFull + (i & 1)), (i >> 1) & 1);
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::kBarQFull + qb));
-      if constexpr (kPaged) {
+    } else if (kPaged && warp >= Ro::kBoundWarp0) {
+      const int hw = warp - Ro::kBoundWarp0;
+      bool ok = *abort_flag == 0;
+      int e = 0;
+      for (int seg = 0; ok; ++seg) {
+        const int qb = seg & 1;
+        ok = wait(L::kBarWork + qb, seg >> 1);
+        if (!ok) break;
+        const Work& wk = works[qb];
+        const int ntok = wk.ntok, ntiles = wk.ntiles, tile0 = wk.tile0;
+        const int64_t tok = wk.tok;
+        if (ntiles == 0) break;
+        if (seg == 0) {
+          bring(Ro::kHelpers + hw, Ro::kHelpers + Ro::kBounders, 0, tok, ntok);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kBarQFirst));
+        }
         // Bounds of the key rows' lengths, from the tiles as they pass: two warps take every
         // other one, a thread two rows (a tile in turn by all four took 1250 cycles a tile,
         // half of it the wait).
@@ -580,11 +663,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < ntok)
             *reinterpret_cast<float2*>(p.norms + (tok + lane - p.tok0) * p.norm_ld + (tile0 + i) * 4 + (hw & 1) * 2) = make_float2(top, top);
         }
+        if (lane == 0) mbar_arrive(bar(L::kBarQEmpty + qb));
       }
-      if (lane == 0) mbar_arrive(bar(L::kBarQEmpty + qb));
     }
   } else {
-    reg_alloc<kEpilogueRegs>();
+    reg_alloc<Ro::kEpilogueRegs>();
     // ------------------------------------------------------------ epilogue
     const int group = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -601,10 +684,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Work& wk = works[qb];
       const int ntiles = wk.ntiles, ntok = wk.ntok, tile0 = wk.tile0;
       if (ntiles == 0) break;
-      ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarQFull + qb), (seg >> 1) & 1, ctl));
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(q_bar(seg)), q_phase(seg) & 1, ctl));
       if (!ok) break;
-      const bool wide = ntok * Hp > kMine;
-      const int col0 = wide ? group * kMine : 0;
+      // A tile's columns are shared by as many warpgroups, and so many sets of them take tiles
+      // in turn.
+      const int cols = ntok * Hp;
+      const int share = cols <= kMine ? 1 : cols <= 2 * kMine ? 2 : 4;
+      const int sets = Ro::kGroups / share, set = group / share;
+      const int col0 = (group - set * share) * kMine;
       constexpr int kTok = kMine / Hp;                   // tokens of its columns
       const int tok0 = col0 / Hp;
       float w[kMine];
@@ -625,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int acc = tile_no & 1;
         ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarAccFull + acc), (tile_no >> 1) & 1, ctl));
         if (!ok) break;
-        if (wide || acc == group) {
+        if ((tile_no & (sets - 1)) == set && col0 < cols) {
           tc_fence_after();
           const int j = (tile0 + i) * kTile + my;
           float scale = 1.f;
@@ -671,9 +758,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           };
-          const bool both = ntok * Hp - col0 > 64;
-          if (both)
-            sums(std::false_type{}, std::true_type{});
+          using Wide = std::bool_constant<kMine == 128>;
+          if (kMine == 128 && cols - col0 > 64)
+            sums(std::false_type{}, Wide{});
           else
             sums(std::false_type{}, std::false_type{});
           if constexpr (!kPaged) {
@@ -681,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool again = false;
 #pragma unroll
             for (int k = 0; k < kTok; ++k) again = again || (tok0 + k < ntok && sum[k] != sum[k]);
-            if (__any_sync(0xffffffffu, again)) sums(std::true_type{}, std::true_type{});
+            if (__any_sync(0xffffffffu, again)) sums(std::true_type{}, Wide{});
           }
           tc_fence_before();
           __syncwarp();
@@ -714,14 +801,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == Ro::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 2 * kCols);
   }
 }
 
 template <int D, bool kPaged, int Hp>
-cudaError_t launch(const CUtensorMap& tm_k, const TopkParams& p, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_q, const TopkParams& p, cudaStream_t stream) {
   using L = ScoreLayout<D, kPaged>;
   const auto kern = smqa_topk_score_kernel<D, kPaged, Hp>;
   static std::atomic<uint64_t> allowed{0};
@@ -732,28 +819,28 @@ cudaError_t launch(const CUtensorMap& tm_k, const TopkParams& p, cudaStream_t st
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(kSMs);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Roles<kPaged, Hp>::kThreads);
   cfg.dynamicSmemBytes = L::kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tm_k, p);
+  return cudaLaunchKernelEx(&cfg, kern, tm_k, tm_q, p);
 }
 template <int D, bool kPaged>
-cudaError_t launch(const CUtensorMap& tm_k, const TopkParams& p, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_q, const TopkParams& p, cudaStream_t stream) {
   switch (padded_heads(p.H)) {
-    case 16: return launch<D, kPaged, 16>(tm_k, p, stream);
-    case 32: return launch<D, kPaged, 32>(tm_k, p, stream);
-    case 64: return launch<D, kPaged, 64>(tm_k, p, stream);
-    default: return launch<D, kPaged, 128>(tm_k, p, stream);
+    case 16: return launch<D, kPaged, 16>(tm_k, tm_q, p, stream);
+    case 32: return launch<D, kPaged, 32>(tm_k, tm_q, p, stream);
+    case 64: return launch<D, kPaged, 64>(tm_k, tm_q, p, stream);
+    default: return launch<D, kPaged, 128>(tm_k, tm_q, p, stream);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_topk_score(const CUtensorMap& tm_k, const TopkParams& p, int D, bool paged, cudaStream_t stream) {
-  if (paged) return D == 64 ? launch<64, true>(tm_k, p, stream) : launch<128, true>(tm_k, p, stream);
-  return D == 64 ? launch<64, false>(tm_k, p, stream) : launch<128, false>(tm_k, p, stream);
+cudaError_t launch_topk_score(const CUtensorMap& tm_k, const CUtensorMap& tm_q, const TopkParams& p, int D, bool paged, cudaStream_t stream) {
+  if (paged) return D == 64 ? launch<64, true>(tm_k, tm_q, p, stream) : launch<128, true>(tm_k, tm_q, p, stream);
+  return D == 64 ? launch<64, false>(tm_k, tm_q, p, stream) : launch<128, false>(tm_k, tm_q, p, stream);
 }
 
 }  // namespace smqa

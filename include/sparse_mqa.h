@@ -574,7 +574,7 @@ smqa_status smqa_paged_fwd(const void* q, const void* kv_cache, const float* kv_
  * rows j <= that position (S_kv - S: the last S positions of a causal sequence;
  * S_kv: every row).  1 <= H <= 128, D in {64, 128}, B*S < 2^31, B*S_kv < 2^31,
  * block_size a power of two up to 128, topk a multiple of it.  Two launches for
- * every 512 MB of scores.
+ * every 64 MB of scores.
  *   workspace  256-byte aligned, smqa_indexer_topk_workspace_bytes(shape,
  *              block_size) bytes (0: unsupported); needs no initialisation; calls
  *              whose kernels may overlap must not share it
