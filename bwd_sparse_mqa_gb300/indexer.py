@@ -264,6 +264,8 @@ class IndexerScoresFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_scores):
+        if torch.is_grad_enabled():                      # (the gradients would pass for constants)
+            raise RuntimeError("indexer_scores is differentiable once (no create_graph)")
         index_q, weights, index_k, topk_indices = ctx.saved_tensors
         dq, dw, dk = indexer_scores_bwd(index_q, weights, index_k, topk_indices,
                                         grad_scores.to(_F32).contiguous(),
@@ -274,6 +276,9 @@ class IndexerScoresFunction(torch.autograd.Function):
 def indexer_scores(index_q: torch.Tensor, weights: torch.Tensor, index_k: torch.Tensor,
                    topk_indices: torch.Tensor, check_status: bool = False) -> torch.Tensor:
     """Differentiable indexer_scores_fwd: gradients with respect to index_q, weights
-    and index_k.  With ``check_status`` the forward and the backward each
-    synchronize and raise SMQAError if a kernel's bounded wait ran out."""
+    and index_k, once (create_graph raises).  With ``check_status`` the
+    forward and the backward each synchronize and raise SMQAError if a kernel's
+    bounded wait ran out.  A backward pass is captured with leaves that no other
+    live graph holds: PyTorch adds a leaf's gradient on the stream of the graph that
+    used it first."""
     return IndexerScoresFunction.apply(index_q, weights, index_k, topk_indices, check_status)

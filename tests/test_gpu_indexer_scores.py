@@ -204,6 +204,16 @@ def test_many_calls_streams_and_capture():
     assert device_status() == 0
 
 
+def test_no_second_derivative():
+    """Refused, not left out."""
+    q, w, k, idx, gr = (v.cuda() for v in _inputs(1, 4, 50, 16, 64, 10, 0.1, 2))
+    leaves = [v.detach().requires_grad_() for v in (q, w, k)]
+    s = indexer_scores(*leaves, idx)
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        torch.autograd.grad(s, leaves, gr, create_graph=True, retain_graph=True)
+    assert len(torch.autograd.grad(s, leaves, gr)) == 3
+
+
 def test_calls_from_threads_that_made_no_cuda_call():
     """As autograd's are: the calls make the device's context their own."""
     import threading

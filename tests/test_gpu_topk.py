@@ -41,6 +41,14 @@ def test_sizes(size):
     _check(*_inputs(B, S, S_kv, H, D, S_kv), topk)
 
 
+@pytest.mark.parametrize("H", [5, 16, 20, 32, 50, 64, 90])
+def test_every_size_of_a_group_of_tokens(H):
+    """Groups of 1 to 16 tokens: their columns go to one, two or all of the warps that sum them;
+    the last group of a batch element is followed by another element's tokens, or by none."""
+    for S in range(1, 18):
+        _check(*_inputs(2, S, 300 + 40 * S, H, 64 if S & 1 else 128, S), 40)
+
+
 @pytest.mark.parametrize("block", [2, 4, 8, 16, 32, 64, 128])
 @pytest.mark.parametrize("recent", [0, 1, 100])
 def test_blocks_and_recent_positions(block, recent):
