@@ -153,6 +153,30 @@ def test_chunks():
     _check(c, 64)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_calls_in_a_row(D):
+    """Key tiles that come early and late (another stream copies meanwhile): a warp that took one
+    round of the ring for another would give other positions or run out of its wait."""
+    c = _case([9000 + 37 * i for i in range(100)], [1] * 100, 64, D, 64, 11)
+    q, w, cache, scale, table, seq, req, pos = c
+    first = paged_indexer_topk(q, w, cache, scale, table, seq, req, pos, 256, check_status=True)
+    for t in (0, 41, 99):
+        one = [q[t:t + 1], w[t:t + 1], cache, scale, table, seq, req[t:t + 1], pos[t:t + 1]]
+        assert torch.equal(_check(one, 256)[0], first[t])
+    side = torch.cuda.Stream()
+    a = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    b = torch.empty_like(a)
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(400):
+        if i % 4 == 0:
+            with torch.cuda.stream(side):
+                b.copy_(a)
+        got = paged_indexer_topk(q, w, cache, scale, table, seq, req, pos, 256)
+        wrong += (got != first).sum()
+    torch.cuda.synchronize()
+    assert int(wrong) == 0 and device_status() == 0
+
+
 def test_server_steps():
     """Prompts, then decoding with one graph: rows and index keys written rotated, positions
     chosen, attention over them, a request finished and its pages used again."""
