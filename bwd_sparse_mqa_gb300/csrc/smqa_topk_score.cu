@@ -88,11 +88,7 @@ struct ScoreLayout {
   static constexpr uint32_t kQPartBytes = kCols * kPitch;
   static constexpr uint32_t kQBytes = kQParts * kQPartBytes;
   static constexpr int kStages = kQBytes == 65536 ? 5 : 8;
-  // Paged: each of the first kOwned stages belongs to one of the four warps that bound the
-  // rows' lengths, the others are shared by all four.  A warp so comes to a stage at every
-  // round of the ring: one that came at every other round only could take the round before
-  // for its own, since a barrier's one parity bit cannot tell them apart.
-  static constexpr int kOwned = kStages / 4 * 4;
+  static constexpr int kShared = kStages & 1 ? kStages - 1 : -1;  // paged: the stage of all warps that bound the rows
   static constexpr uint32_t kSwizzle = kPitch == 128 ? kSwizzle128B : kSwizzle64B;
   static constexpr uint32_t kAtom = 8 * kPitch;          // 8 rows
   static constexpr int kMeta = 16;                       // tiles whose page scales are kept
@@ -244,8 +240,8 @@ __global__ void __launch_bounds__(Roles<kPaged, Hp>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(bar(L::kBarKFull + i), 1);
-      // Tensor core (and the warps that bound the rows' lengths: one, or all four).
-      mbar_init(bar(L::kBarKEmpty + i), !kPaged ? 1 : i < L::kOwned ? 2 : 5);
+      // Tensor core (and the two or four warps that bound the rows' lengths).
+      mbar_init(bar(L::kBarKEmpty + i), !kPaged ? 1 : i == L::kShared ? 5 : 3);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(L::kBarAccFull + i), 1);
@@ -629,23 +625,27 @@ __global__ void __launch_bounds__(Roles<kPaged, Hp>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kBarQFirst));
         }
-        // Bounds of the key rows' lengths, from the tiles as they pass.
+        // Bounds of the key rows' lengths, from the tiles as they pass: two warps have the ring's
+        // even stages, two the odd ones, a thread two rows; the last of an odd number of stages
+        // is shared by all four.  (All four at every tile took 1250 cycles a tile, half of it
+        // the wait.  128 tokens over 32768 positions: 97 us with three stages to two, 98 with
+        // a stage per warp, which held it longer.)  A stage's warps come to it at every round
+        // of the ring: with the tiles in turn to the pairs they came at every other one, and
+        // a barrier's one parity bit cannot tell a round from the one before the last.
         // |code| 2^-8 is the fp16 number with the code's seven bits at 7-13; squares and
         // sums of 16 of them in fp16 are off by 2^-11 each step, and lose 2^-25 each
         // where they are subnormal.
         for (int i = 0; ok && i < ntiles; ++i, ++e) {
           const int st = e % L::kStages;
-          const bool owned = st < L::kOwned;
-          if (owned && (st & 3) != hw) continue;
+          const bool shared = st == L::kShared;
+          if (!shared && (st & 1) != (hw >> 1)) continue;
           ok = wait(L::kBarKFull + st, e / L::kStages);
           if (!ok) break;
-          // 32 rows at a time: all of the tile, or a quarter.
-          float top[4];
-          const int q0 = owned ? 0 : hw;
+          float top = 0.f;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (q > 0 && !owned) break;
-            const int r = (q0 + q) * 32 + lane;
+          for (int half = 0; half < 2; ++half) {
+            if (half == 1 && shared) break;
+            const int r = (shared ? hw * 32 : (hw & 1) * 64 + half * 32) + lane;
             const uint8_t* row = smem + L::kOffK + st * L::kPieceBytes + r * L::kPitch;
             float s = 0.f;
 #pragma unroll
@@ -664,16 +664,16 @@ __global__ void __launch_bounds__(Roles<kPaged, Hp>::kThreads, 1)
               s += f.x + f.y;
             }
             const float scale = reinterpret_cast<const float*>(smem + L::kOffMeta)[(e % L::kMeta) * 8 + (r >> p.page_shift)];
-            top[q] = sqrtf(s * 1.02f + 0x1p-16f) * 256.f * fmaxf(scale, 0.f);
-            top[q] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top[q])));
+            top = fmaxf(top, sqrtf(s * 1.02f + 0x1p-16f) * 256.f * fmaxf(scale, 0.f));
           }
+          top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
           if (lane == 0) mbar_arrive(bar(L::kBarKEmpty + st));
           if (lane < ntok) {
-            float* to = p.norms + (tok + lane - p.tok0) * p.norm_ld + (tile0 + i) * 4 + q0;
-            if (owned)
-              *reinterpret_cast<float4*>(to) = make_float4(top[0], top[1], top[2], top[3]);
+            float* to = p.norms + (tok + lane - p.tok0) * p.norm_ld + (tile0 + i) * 4;
+            if (shared)
+              to[hw] = top;
             else
-              *to = top[0];
+              *reinterpret_cast<float2*>(to + (hw & 1) * 2) = make_float2(top, top);
           }
         }
         if (lane == 0) mbar_arrive(bar(L::kBarQEmpty + qb));
