@@ -597,7 +597,8 @@ __device__ __forceinline__ int nth_of(Token<D, kPaged, NT>& tk, int* keys, int m
 }
 
 // Of idx[0 .. m), r are to be chosen: mark[i] = 1 for those with the best exact scores,
-// ties by number.
+// ties by number.  (Behind a barrier that all have passed since they last looked at misc[3]
+// and at the lists.)
 template <int D, bool kPaged, int NT>
 __device__ __noinline__ void settle(Token<D, kPaged, NT> tk, int m, int r) {
   using L = SelLayout<D, NT>;
@@ -996,15 +997,20 @@ __device__ __forceinline__ bool choose_ordinary(Token<D, kPaged, NT>& tk) {
   };
   if (tk.tid == 0) misc[3] = 0;
   __syncthreads();
-  int cnt[1] = {0};
+  int cnt[2] = {0, 0};
   for (int i = tk.tid; i < near; i += NT) {
     const int k = list[i], c = list[kList + i];
     cnt[0] += k > khi;
-    if (k >= klo && k <= khi) idx[atomicAdd(misc + 3, 1)] = c;
-    else decide(c, k > khi);
+    if (k >= klo && k <= khi) {
+      ++cnt[1];
+      idx[atomicAdd(misc + 3, 1)] = c;
+    } else {
+      decide(c, k > khi);
+    }
   }
-  tk.template reduce<1, false>(cnt);
-  const int m = misc[3], r = want - above - cnt[0];
+  tk.template reduce<2, false>(cnt);
+  // (Not from misc[3], which settle sets back before its first barrier.)
+  const int m = cnt[1], r = want - above - cnt[0];
   if (m == r) {
     for (int i = tk.tid; i < m; i += NT) decide(idx[i], true);
   } else if (klo == khi) {                               // (exact scores that tie)
