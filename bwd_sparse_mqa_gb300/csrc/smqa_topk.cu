@@ -1148,6 +1148,9 @@ cudaError_t launch_select(const TopkParams& p, cudaStream_t stream) {
 // Host
 // ---------------------------------------------------------------------------
 constexpr int64_t kLim = int64_t{1} << 31;
+// Entries of a list, and positions that a token may see: the kernels' loops over them step by
+// up to 1024 threads, in 32 bits.
+constexpr int64_t kMaxCount = kLim - 2048;
 // Bytes of scores that a chunk of tokens may take: half of L2, from which the choice reads
 // them.  (S = 8192, H = 64, topk = 2048: 955 us with 16 MB, 728 with 64, 710 with 256 or 1024,
 // whose workspace a caller would have to hold.)
@@ -1185,8 +1188,9 @@ TopkPlan plan_topk(int64_t rows, int block_shift, int H, bool paged, int64_t B, 
 smqa_status check_choice(int topk, int block_size, int recent) {
   if (topk <= 0 || block_size <= 0 || recent < 0) return refuse(SMQA_ERR_INVALID_ARG, "non-positive size in topk");
   const int bs = shift_of(block_size);
-  if (bs < 0 || topk % block_size != 0)
-    return refuse(SMQA_ERR_UNSUPPORTED, "unsupported topk (need block_size a power of two up to 128, topk a multiple of it)");
+  if (bs < 0 || topk % block_size != 0 || topk > kMaxCount)
+    return refuse(SMQA_ERR_UNSUPPORTED,
+                  "unsupported topk (need block_size a power of two up to 128, topk a multiple of it, up to 2^31 - 2048)");
   // (The last `recent` positions touch this many blocks at most.)
   if (recent > 0 && (static_cast<int64_t>(recent) - 2 + block_size) / block_size + 1 > topk / block_size)
     return refuse(SMQA_ERR_INVALID_ARG, "recent positions take more blocks than topk has");
@@ -1195,9 +1199,10 @@ smqa_status check_choice(int topk, int block_size, int recent) {
 smqa_status check_flat(const smqa_shape& s) {
   if (s.B <= 0 || s.S <= 0 || s.S_kv <= 0 || s.H <= 0 || s.D <= 0)
     return refuse(SMQA_ERR_INVALID_ARG, "non-positive size in shape");
-  if (s.H > 128 || (s.D != 64 && s.D != 128) || s.S_kv > kLim - 256 || static_cast<int64_t>(s.B) * s.S_kv >= kLim ||
+  if (s.H > 128 || (s.D != 64 && s.D != 128) || s.S_kv > kMaxCount || static_cast<int64_t>(s.B) * s.S_kv >= kLim ||
       static_cast<int64_t>(s.B) * s.S >= kLim)
-    return refuse(SMQA_ERR_UNSUPPORTED, "unsupported indexer shape (need 1<=H<=128, D in {64,128}, B*S, B*S_kv < 2^31)");
+    return refuse(SMQA_ERR_UNSUPPORTED,
+                  "unsupported indexer shape (need 1<=H<=128, D in {64,128}, B*S, B*S_kv < 2^31, S_kv <= 2^31 - 2048)");
   return SMQA_OK;
 }
 smqa_status check_paged_topk(const smqa_paged_shape& s) {
@@ -1205,10 +1210,10 @@ smqa_status check_paged_topk(const smqa_paged_shape& s) {
     return refuse(SMQA_ERR_INVALID_ARG, "non-positive size in paged shape");
   if (s.H > 128 || (s.D != 64 && s.D != 128) || shift_of(s.page_size) < 4 ||
       static_cast<int64_t>(s.n_pages) * s.page_size >= kLim ||
-      static_cast<int64_t>(s.max_pages) * s.page_size > kLim - 256)
+      static_cast<int64_t>(s.max_pages) * s.page_size > kMaxCount)
     return refuse(SMQA_ERR_UNSUPPORTED,
                   "unsupported paged indexer shape (need 1<=H<=128, D in {64,128}, page_size in {16,32,64,128}, "
-                  "n_pages * page_size < 2^31, max_pages * page_size <= 2^31 - 256)");
+                  "n_pages * page_size < 2^31, max_pages * page_size <= 2^31 - 2048)");
   return SMQA_OK;
 }
 

@@ -573,8 +573,8 @@ smqa_status smqa_paged_fwd(const void* q, const void* kv_cache, const float* kv_
  * Query s of a batch element stands at position first_position + s and sees the
  * rows j <= that position (S_kv - S: the last S positions of a causal sequence;
  * S_kv: every row).  1 <= H <= 128, D in {64, 128}, B*S < 2^31, B*S_kv < 2^31,
- * block_size a power of two up to 128, topk a multiple of it.  Two launches for
- * every 64 MB of scores.
+ * S_kv and topk up to 2^31 - 2048, block_size a power of two up to 128, topk a
+ * multiple of it.  Two launches for every 64 MB of scores.
  *   workspace  256-byte aligned, smqa_indexer_topk_workspace_bytes(shape,
  *              block_size) bytes (0: unsupported); needs no initialisation; calls
  *              whose kernels may overlap must not share it
@@ -595,6 +595,8 @@ smqa_status smqa_indexer_topk(const void* index_q, const float* weights, const v
  *             seq_lens[req], on pages that the table has
  *   topk_idxs [T,topk]  positions in the token's own request.  Rows of padding
  *             tokens are left as they were, or -1 with SMQA_FLAG_ZERO_PADDING.
+ * page_size in {16,32,64,128}, n_pages * page_size < 2^31, max_pages * page_size and
+ * topk up to 2^31 - 2048.
  */
 size_t smqa_paged_indexer_topk_workspace_bytes(smqa_paged_shape shape, int32_t block_size);
 smqa_status smqa_paged_indexer_topk(const void* index_q, const float* weights, const void* k_cache,
