@@ -118,6 +118,10 @@ bool encode_bf16_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t ou
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Entries of a token's list: the kernels' loops over them step by up to 384 threads (or take
+// blocks of 128 ahead), in 32 bits.
+constexpr int64_t kMaxList = (int64_t{1} << 31) - 2048;
+
 smqa_status check_shape(const smqa_shape& s) {
   if (s.B <= 0 || s.S <= 0 || s.S_kv <= 0 || s.H <= 0 || s.D <= 0 || s.topk <= 0) {
     std::snprintf(g_last_error, sizeof g_last_error, "non-positive size in shape");
@@ -127,9 +131,9 @@ smqa_status check_shape(const smqa_shape& s) {
   if (s.H > 128 || (s.D != 64 && s.D != 512) ||
       static_cast<int64_t>(s.B) * s.S_kv * s.D >= lim ||
       static_cast<int64_t>(s.B) * s.S * s.H >= lim ||
-      static_cast<int64_t>(s.B) * s.S >= (lim >> 1)) {
+      static_cast<int64_t>(s.B) * s.S >= (lim >> 1) || s.topk > kMaxList) {
     std::snprintf(g_last_error, sizeof g_last_error,
-                  "unsupported shape (need 1<=H<=128, D in {64,512}, sizes < 2^31)");
+                  "unsupported shape (need 1<=H<=128, D in {64,512}, sizes < 2^31, topk <= 2^31 - 2048)");
     return SMQA_ERR_UNSUPPORTED;
   }
   return SMQA_OK;
@@ -519,9 +523,9 @@ smqa_status indexer_impl(const void* q, const float* w, const void* k, const int
   if (s.H > 128 || (s.D != 64 && s.D != 128) ||
       static_cast<int64_t>(s.B) * s.S_kv * s.D >= lim ||
       static_cast<int64_t>(s.B) * s.S * s.H * s.D >= lim ||
-      static_cast<int64_t>(s.B) * s.S * s.topk >= lim) {
+      static_cast<int64_t>(s.B) * s.S * s.topk >= lim || s.topk > kMaxList) {
     std::snprintf(g_last_error, sizeof g_last_error,
-                  "unsupported indexer shape (need 1<=H<=128, D in {64,128}, sizes < 2^31)");
+                  "unsupported indexer shape (need 1<=H<=128, D in {64,128}, sizes < 2^31, topk <= 2^31 - 2048)");
     return SMQA_ERR_UNSUPPORTED;
   }
   if (!batched && s.B != 1) {
@@ -573,9 +577,9 @@ smqa_status scores_shape(const smqa_shape& s) {
   }
   const int64_t lim = int64_t{1} << 31;
   if (s.H > 128 || (s.D != 64 && s.D != 128) || static_cast<int64_t>(s.B) * s.S_kv >= lim ||
-      static_cast<int64_t>(s.B) * s.S * s.H >= lim || s.topk > lim - 128) {
+      static_cast<int64_t>(s.B) * s.S * s.H >= lim || s.topk > kMaxList) {
     std::snprintf(g_last_error, sizeof g_last_error,
-                  "unsupported indexer shape (need 1<=H<=128, D in {64,128}, B*S*H, B*S_kv, topk < 2^31)");
+                  "unsupported indexer shape (need 1<=H<=128, D in {64,128}, B*S*H, B*S_kv < 2^31, topk <= 2^31 - 2048)");
     return SMQA_ERR_UNSUPPORTED;
   }
   return SMQA_OK;

@@ -31,8 +31,8 @@
  *     read it with smqa_device_status().  The word is sticky: while it is set,
  *     the forward and backward-main kernels skip their work (their outputs
  *     are left undefined) until smqa_device_status(1) clears it.
- *   - Supported shapes: 1 <= H <= 128, D in {64, 512}, topk >= 1, B, S,
- *     S_kv >= 1, B*S_kv*D < 2^31, B*S*H < 2^31.  Anything else returns
+ *   - Supported shapes: 1 <= H <= 128, D in {64, 512}, 1 <= topk <= 2^31 - 2048,
+ *     B, S, S_kv >= 1, B*S_kv*D < 2^31, B*S*H < 2^31.  Anything else returns
  *     SMQA_ERR_UNSUPPORTED.
  */
 #ifndef SPARSE_MQA_H_
@@ -331,7 +331,7 @@ smqa_status smqa_bwd_sink_grad(const float* attn_sink, const float* lse, const f
  *   index_q      bf16 [S, H, D]       weights      fp32 [S, H]
  *   index_k      bf16 [S_kv, D]       topk_indices int32 [S, topk]
  *   grad_scores  fp32 [S, topk]       dq           bf16 [S, H, D] (output)
- * shape.B must be 1; 1 <= H <= 128, D in {64, 128}.  The logits are formed
+ * shape.B must be 1; 1 <= H <= 128, D in {64, 128}, topk up to 2^31 - 2048.  The logits are formed
  * in fp32 by the tensor core, so where <q, k_j> lies within fp32 rounding of
  * 0 the gate may differ from an exact evaluation.  grad_scores enter the
  * tensor core as bf16.  Device pointers; asynchronous on `stream`; nothing
@@ -362,7 +362,7 @@ smqa_status smqa_batched_indexer_bwd(const void* index_q, const float* weights,
  * and -inf where the index lies outside [0, S_kv).
  *   index_q      bf16 [B,S,H,D]       weights fp32 [B,S,H]     index_k bf16 [B,S_kv,D]
  *   topk_indices int32 [B,S,topk]     scores  fp32 [B,S,topk]
- * 1 <= H <= 128, D in {64, 128}.  Logits and sums are fp32.
+ * 1 <= H <= 128, D in {64, 128}, topk up to 2^31 - 2048.  Logits and sums are fp32.
  *
  * The backward takes grad_scores fp32 [B,S,topk] (masked slots' are not looked
  * at; a slot listed twice counts twice; the ReLU's slope at 0 is 0) and writes
