@@ -1072,7 +1072,9 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : 3) smqa_topk_select_kerne
   const int64_t t = p.tok0 + blockIdx.x;
   grid_dependency_wait();
   grid_dependents_launch();
-  if (*reinterpret_cast<volatile int*>(p.status) != 0) return;  // (scores are missing)
+  // Scores are missing where a wait ran out.  (Of all threads together: another stream's kernel
+  // may set the word between two threads' looks at it, and the others would go on without them.)
+  if (__syncthreads_or(*reinterpret_cast<volatile int*>(p.status)) != 0) return;
   int req;
   const int n = visible<kPaged>(p, t, req);
   int32_t* out = p.out + t * p.topk;

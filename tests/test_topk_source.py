@@ -1,4 +1,5 @@
-"""What the choice's source must keep to: a counter in shared memory that threads read is not set
+"""What the choice's source must keep to.  Its threads leave together or not at all: those that go
+on would use what the others were to write.  And a counter in shared memory that threads read is not set
 back before a barrier behind those reads (a warp that came late would read 0 and take another way
 than the others, through other barriers)."""
 import os
@@ -35,6 +36,13 @@ def test_the_counter_is_read_before_it_is_set_back():
     kinds = [k for k, _ in _events(re.sub(r"//[^\n]*", "", code))]
     assert kinds.count("read") >= 2 and kinds.count("reset") >= 5
     assert _early_resets(code) == []
+
+
+def test_the_status_word_is_looked_at_together():
+    with open(os.path.join(CSRC, "smqa_topk.cu")) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    looks = [line for line in code.splitlines() if re.search(r"\*>\(p\.status\)", line)]
+    assert looks and all("__syncthreads_or" in line for line in looks)
 
 
 def test_the_check_itself():
