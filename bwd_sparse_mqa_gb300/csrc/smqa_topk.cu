@@ -380,9 +380,11 @@ struct Token {
           }
           // Heads h0 + lane / 4 and 8 more, rows r0 + 2 (lane mod 4) and the next.
           const int ha = h0 + (lane >> 2), hb = ha + 8;
+          // (A logit that is NaN or +infinity makes its row's sum one that is no number, which put leaves
+          // out: such a row ranks below its block's others, or above, and its block is not here.)
           auto weighted = [&](Pair x, int h) {
-            x = normal(x.hi, x.lo);
-            return h < H && x.hi > 0.f ? times(x, at<float>(L::kOffW)[h]) : Pair{0.f, 0.f};
+            const Pair y = normal(x.hi, x.lo);
+            return h < H && x.hi != -INFINITY && !(y.hi <= 0.f) ? times(y, at<float>(L::kOffW)[h]) : Pair{0.f, 0.f};
           };
           Pair x = add(weighted(sum[0], ha), weighted(sum[2], hb)), y = add(weighted(sum[1], ha), weighted(sum[3], hb));
 #pragma unroll
@@ -445,12 +447,14 @@ struct Token {
           Pair sum{0.f, 0.f};
           for (int h = lane; h < H; h += 32) {
             Pair d{0.f, 0.f};
+            float all = 0.f;                             // (where it is -infinity, d is no number)
 #pragma unroll
             for (int i = 0; i < kParts; ++i) {
               const float2 x = at<float2>(L::kOffHist)[(r * kParts + i) * heads + h];
               d = add(d, Pair{x.x, x.y});
+              all += x.x;
             }
-            if (d.hi > 0.f) sum = add(sum, times(d, at<float>(L::kOffW)[h]));
+            if (all != -INFINITY && !(d.hi <= 0.f)) sum = add(sum, times(d, at<float>(L::kOffW)[h]));
           }
 #pragma unroll
           for (int off = 16; off > 0; off >>= 1)

@@ -57,3 +57,52 @@ def test_every_paged_call_is_the_same(R, n, topk):
     for _ in range(1000):
         wrong += (paged_indexer_topk(*args) != first).sum()
     assert int(wrong) == 0 and device_status() == 0
+
+
+def _close_scores(n, H, D, seed):
+    """Keys that differ in a few last bits and scores of one sign: every block's best row is scored again."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q = (torch.rand(1, 3, H, D, generator=g, device="cuda") + 0.5).bfloat16()
+    k = (torch.rand(D, generator=g, device="cuda") + 1.0).bfloat16().expand(1, n, D).clone()
+    at = torch.randint(0, D, (n,), generator=g, device="cuda")
+    k.view(torch.int16)[0, torch.arange(n, device="cuda"), at] += torch.randint(-2, 3, (n,), generator=g, device="cuda", dtype=torch.int16)
+    w = torch.rand(1, 3, H, generator=g, device="cuda") + 0.5
+    return q, w, k, g
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("H,D", [(16, 64), (64, 128)])
+@pytest.mark.parametrize("n,block", [(2600, 8), (9000, 2), (9000, 64)])
+def test_rows_that_are_no_numbers_in_blocks_scored_again(bad, H, D, n, block):
+    """A row of a NaN logit ranks last, one of an infinite logit where its weights' signs put it; the
+    rest of its block decides with the numbers that it has."""
+    q, w, k, g = _close_scores(n, H, D, n + H)
+    rows = torch.randperm(n, generator=g, device="cuda")[:n // 20]
+    k[0, rows, torch.randint(0, D, (len(rows),), generator=g, device="cuda")] = bad
+    w[0, 1] *= -1
+    w[0, 2, ::2] *= -1
+    for topk in (4 * block, 20 * block, 40 * block):
+        got = indexer_topk(q, w, k, topk, block, check_status=True)
+        want = ref.flat(q, w, k, topk, block)
+        assert torch.equal(got.long(), want), (topk, (got.long() != want).sum(2).tolist())
+
+
+@pytest.mark.parametrize("D,block", [(64, 8), (128, 16), (128, 64)])
+def test_nan_codes_in_blocks_scored_again(D, block):
+    n, page, H = 3000, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(D + block)
+    code = torch.randint(0x38, 0x3a, (-(-n // page), page, D), generator=g, device="cuda").to(torch.uint8)  # (1 and 1.125)
+    code[:, :, 1:] = code[0, 0, 1:]
+    code[:, :, 0] = torch.randint(8, 16, code.shape[:2], generator=g, device="cuda").to(torch.uint8)  # (2^-6 and up)
+    code.view(-1, D)[torch.randperm(n, generator=g, device="cuda")[:n // 20], 5] = 0x7f
+    cache, scales = code.view(torch.float8_e4m3fn), torch.full((code.shape[0],), 0.5, device="cuda")
+    table = torch.randperm(code.shape[0], generator=g, device="cuda").int()[None]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = (torch.rand(2, H, D, generator=g, device="cuda") + 0.5).bfloat16()
+    w = torch.rand(2, H, generator=g, device="cuda") + 0.5
+    w[1] *= -1
+    args = (q, w, cache, scales, table, i32([n]), i32([0, 0]), i32([n - 2, n - 1]))
+    for blocks in (3, 9):
+        got = paged_indexer_topk(*args, blocks * block, block, check_status=True)
+        want = ref.paged(q, w, cache.double(), scales.double(), *args[4:], blocks * block, block)
+        assert torch.equal(got.long(), want), (blocks, (got.long() != want).sum(1).tolist())
