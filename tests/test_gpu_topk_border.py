@@ -71,7 +71,7 @@ def _close_scores(n, H, D, seed):
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
-@pytest.mark.parametrize("H,D", [(16, 64), (64, 128)])
+@pytest.mark.parametrize("H,D", [(1, 64), (16, 64), (24, 128), (64, 128)])
 @pytest.mark.parametrize("n,block", [(2600, 8), (9000, 2), (9000, 64)])
 def test_rows_that_are_no_numbers_in_blocks_scored_again(bad, H, D, n, block):
     """A row of a NaN logit ranks last, one of an infinite logit where its weights' signs put it; the
