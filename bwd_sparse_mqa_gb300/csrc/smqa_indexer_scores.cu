@@ -175,6 +175,11 @@ __global__ void __launch_bounds__(288, 2) smqa_indexer_scores_kernel(const IdxPa
       ok = __all_sync(0xffffffffu, mbar_wait_soon(bar(L::kBarAccFull + st), (i >> 1) & 1, ctl));
       if (!ok) break;
       tc_fence_after();
+      auto relu = [](float v) {                          // (a NaN stays one)
+        float y;
+        asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(v));
+        return y;
+      };
       float2 a0 = {}, a1 = {};
       for (int c = 0; c < heads; c += 32) {
         float x[32];
@@ -183,20 +188,29 @@ __global__ void __launch_bounds__(288, 2) smqa_indexer_scores_kernel(const IdxPa
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float4 w = w4[k];
-          auto relu = [](float v) {                      // (a NaN stays one)
-            float y;
-            asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(v));
-            return y;
-          };
           a0 = fma2(make_float2(w.x, w.y), make_float2(relu(x[4 * k]), relu(x[4 * k + 1])), a0);
           a1 = fma2(make_float2(w.z, w.w), make_float2(relu(x[4 * k + 2]), relu(x[4 * k + 3])), a1);
         }
+      }
+      float s = (a0.x + a0.y) + (a1.x + a1.y);
+      if (heads != p.H && __any_sync(0xffffffffu, s != s)) {
+        // Without the heads behind H (0 times an infinity is no number), in four chains as above.
+        float a[4] = {};
+#pragma unroll 1
+        for (int c = 0; c < p.H; c += 32) {
+          float x[32];
+          tmem_ld32(tmem + lanes + st * 128 + c, x);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (c + k < p.H) a[k & 3] = fmaf(ws[c + k], relu(x[k]), a[k & 3]);
+        }
+        s = (a[0] + a[1]) + (a[2] + a[3]);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kBarAccEmpty + st));
       if (j < p.topk)
-        out[j] = static_cast<unsigned>(r) < static_cast<unsigned>(p.S_kv) ? (a0.x + a0.y) + (a1.x + a1.y) : -INFINITY;
+        out[j] = static_cast<unsigned>(r) < static_cast<unsigned>(p.S_kv) ? s : -INFINITY;
     }
     if (ok)
       for (int j = nblk * L::kBI + tid; j < p.topk; j += 128) out[j] = -INFINITY;
