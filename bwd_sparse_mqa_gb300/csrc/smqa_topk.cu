@@ -8,7 +8,9 @@
 // chosen and one below T - 2E is not.  The few between are scored again by sums of 16
 // products, added in pairs of fp32 numbers, whose error is a fraction of E, and those
 // that are still open with each product (exact in fp32, as those of bf16 and e4m3
-// numbers are) added with its rounding error kept in a second sum (two-sum).
+// numbers are) added with its rounding error kept in a second sum (two-sum).  That sum is
+// fp32, of eight errors of 2^-24 of their chain each: the last values are off by 2^-41 of
+// sum_h |w_h||q_h||k| at most.
 //
 // E = K sum_h |w_h| (c |q_h| + rho_h), K the largest length of a key row that the
 // token sees.  The tensor core drops from every product what lies 2^24 below the
@@ -198,10 +200,13 @@ struct Token {
         sq += __shfl_xor_sync(0xffffffffu, sq, off);
         if constexpr (kPaged) sr += __shfl_xor_sync(0xffffffffu, sr, off);
       }
-      const float wh = c == 0 ? fabsf(w) * pow2f(-k) : 0.f;
+      // (What fp32 or the tensor core may lose of a weight below 2^-126 or of a query element below
+      // that: the weight counts as 2^-126 at least, the row's length as 2^-88 more, and a sum over
+      // heads that are not 0 is not 0.)
+      const float wa = c == 0 && w != 0.f && m != 0 ? fmaxf(fabsf(w), 0x1p-126f) : 0.f, wh = wa * pow2f(-k);
       if (there && c == 0) at<float>(L::kOffLen)[h] = 1.01f * sqrtf(sq) * pow2f(-k);
-      len = fmaf(wh, sqrtf(sq), len);
-      if constexpr (kPaged) rest = fmaf(wh, sqrtf(sr), rest);
+      len = fmaf(wh, sqrtf(sq), fmaf(wa, 0x1p-88f, wa > 0.f ? len + 0x1p-126f : len));
+      rest = kPaged ? fmaf(wh, sqrtf(sr), rest) : rest + wa;
     }
     // The longest row of the tiles that the token sees.
     const int tiles = 4 * ((n + kTile - 1) / kTile);     // (a bound per 32 rows)
@@ -211,7 +216,7 @@ struct Token {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       len += __shfl_xor_sync(0xffffffffu, len, off);
-      if constexpr (kPaged) rest += __shfl_xor_sync(0xffffffffu, rest, off);
+      rest += __shfl_xor_sync(0xffffffffu, rest, off);
     }
     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
     float* red = at<float>(L::kOffRed);
@@ -227,19 +232,22 @@ struct Token {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       len += __shfl_xor_sync(0xffffffffu, len, off);
-      if constexpr (kPaged) rest += __shfl_xor_sync(0xffffffffu, rest, off);
+      rest += __shfl_xor_sync(0xffffffffu, rest, off);
     }
     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
     __syncthreads();
-    // (1.01 for the rounding of these sums, 2^-110 for what underflows; a factor of 0
-    // leaves scores of exactly 0.)
+    // (1.01 for the rounding of these sums.  What underflows, with bf16 keys: D products, of which the
+    // tensor core may take those below 2^-126 for 0, and key elements, as 2^-100 more of length; with
+    // e4m3 keys: 2^-150 of a head's weight, times 2^12 |k|.  Only where all weights and queries or
+    // all key rows are 0, all scores are exactly 0.)
     const float c_score = (static_cast<float>(kPaged ? D + D / 16 + 17 : D + 16) + static_cast<float>(p.H) * 0.25f + 4.f) * 0x1p-24f;
-    const float tiny = top * 0x1p-110f;
-    longest = top;
-    e_score = len * top == 0.f ? 0.f : 1.01f * top * (len * c_score + rest) + tiny;
+    const float tiny = (kPaged ? top * 0x1p-110f : rest * 0x1p-116f) + 0x1p-140f;
+    const bool zero = len == 0.f || top == 0.f;
+    longest = kPaged ? top : top + 0x1p-100f;
+    e_score = zero ? 0.f : 1.01f * longest * (kPaged ? len * c_score + rest : len * c_score) + tiny;
     if (!(e_score < INFINITY)) e_score = INFINITY;
     // Plain values: 16 products and their sum (2^-23 of it), and a rounding of the score.
-    e_plain = 1.01f * top * len * (20.f * 0x1p-24f) + tiny;
+    e_plain = zero ? 0.f : 1.01f * longest * len * (20.f * 0x1p-24f) + tiny;
     if (!(e_plain < INFINITY)) e_plain = INFINITY;
   }
 
@@ -290,7 +298,7 @@ struct Token {
         for (int i = 0; i < 4; ++i) s[i] = fma2(make_float2(__uint_as_float(q4[i] << 16), __uint_as_float(q4[i] & 0xffff0000u)), kk[i], s[i]);
       }
       const float2 sum = add2(add2(s[0], s[1]), add2(s[2], s[3]));
-      const float bound = longest * at<float>(L::kOffLen)[h] * (static_cast<float>(D / 8 + 4) * 0x1p-24f);
+      const float bound = longest * (at<float>(L::kOffLen)[h] + 0x1p-126f) * (static_cast<float>(D / 8 + 4) * 0x1p-24f) + 0x1p-140f;
       if (!((sum.x + sum.y) * scale < -bound)) return false;
     }
     return true;

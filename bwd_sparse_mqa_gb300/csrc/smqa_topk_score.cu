@@ -534,15 +534,23 @@ __global__ void __launch_bounds__(Roles<kPaged, Hp>::kThreads, 1)
                 s = fmaf(a, a, fmaf(d, d, s));
               }
             }
-            // (An infinite row's scores are infinite or NaN, and need no bound.)
-            s = s < INFINITY ? sqrtf(s) * 1.0001f : s == INFINITY ? s : 0.f;
-            if (s == INFINITY) {                           // finite, but its square is not?
+            if (s >= 0x1p-90f && s < INFINITY) {
+              s = sqrtf(s) * 1.0001f;
+            } else {
+              // Squares that leave fp32's range: once more, the row times 2^70 or 2^-70.  (A row of
+              // infinities has scores that are infinite, NaN or 0, and needs no bound.)
+              const float f = s < 1.f ? 0x1p70f : 0x1p-70f;
+              s = 0.f;
+  #pragma unroll 1
               for (int c = 0; c < D / 8; ++c) {
                 const uint4 v = load(row + c);
                 const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-                for (int k = 0; k < 4; ++k)
-                  if ((w4[k] & 0x7f80u) == 0x7f80u || (w4[k] & 0x7f800000u) == 0x7f800000u) s = 0.f;
+                for (int k = 0; k < 4; ++k) {
+                  const float a = __uint_as_float(w4[k] << 16) * f, d = __uint_as_float(w4[k] & 0xffff0000u) * f;
+                  s = fmaf(a, a, fmaf(d, d, s));
+                }
               }
+              s = s < INFINITY ? __fmul_ru(sqrtf(s) * 1.0001f, 1.f / f) : 0.f;
             }
           }
           const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(s)));

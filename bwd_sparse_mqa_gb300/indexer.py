@@ -74,7 +74,9 @@ def indexer_topk(index_q: torch.Tensor, weights: torch.Tensor, index_k: torch.Te
     ``block_size`` positions rank by their best row.  The last ``recent`` positions
     a query sees always are among its choice.  Returns topk_idxs [B,S,topk] int32:
     the topk / block_size best blocks' positions, ascending, then -1.  The choice
-    is that of the scores as real numbers, ties to the lowest block.
+    is that of the scores as real numbers, ties to the lowest block (scores closer
+    than 2^-40 sum_h |w_h||q_h||k_j| may count as equal; the C header has the limits
+    of magnitudes).
 
     ``out`` takes the result, ``workspace`` (uint8 CUDA tensor) is reused when
     large enough.  With ``check_status`` the call synchronizes and raises

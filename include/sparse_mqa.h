@@ -563,12 +563,15 @@ smqa_status smqa_paged_fwd(const void* q, const void* kv_cache, const float* kv_
  *   topk_idxs  [B,S,topk] int32  their positions, ascending, those that the token
  *                            does not see left out, then -1
  * The choice is that of the scores as real numbers, ties to the lowest block: it
- * does not depend on the order of a sum, on the batch or on the device.  A token
- * that sees topk positions or fewer gets all of them.  The `recent` last positions
- * that a token sees rank above all others (they count among topk; the blocks that
- * they can touch must not exceed topk / block_size).  A NaN ranks below every
- * number.  index_q and weights must be finite (else the choice is unspecified, but
- * still of positions that the token sees), and |q.k|, sum_h |w q.k| below 2^127.
+ * does not depend on the order of a sum, on the batch or on the device.  (Scores
+ * that differ, but by less than 2^-40 sum_h |w_h||q_h||k_j| or 2^-126 (1 + sum_h
+ * |w_h|), may count as the other way round or as equal, the same in every call.)
+ * A token that sees topk positions or fewer gets all of them.  The `recent` last
+ * positions that a token sees rank above all others (they count among topk; the
+ * blocks that they can touch must not exceed topk / block_size).  A NaN ranks below
+ * every number.  index_q and weights must be finite, and sum_i |q_hi k_ji| and
+ * sum_h,i |w_h q_hi k_ji| below 2^126 (else the choice is unspecified, but still of
+ * positions that the token sees; infinities in index_k rank as the scores they give).
  *   index_q   bf16 [B,S,H,D]   weights fp32 [B,S,H]   index_k bf16 [B,S_kv,D]
  * Query s of a batch element stands at position first_position + s and sees the
  * rows j <= that position (S_kv - S: the last S positions of a causal sequence;
@@ -595,6 +598,8 @@ smqa_status smqa_indexer_topk(const void* index_q, const float* weights, const v
  *             seq_lens[req], on pages that the table has
  *   topk_idxs [T,topk]  positions in the token's own request.  Rows of padding
  *             tokens are left as they were, or -1 with SMQA_FLAG_ZERO_PADDING.
+ * The limits of magnitudes hold for the codes as well as for the codes times their
+ * scales, and |w_h q_hi| < 2^126; 2^-126 is times the scale where that is above 1.
  * page_size in {16,32,64,128}, n_pages * page_size < 2^31, max_pages * page_size and
  * topk up to 2^31 - 2048.
  */
