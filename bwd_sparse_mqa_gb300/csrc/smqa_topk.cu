@@ -770,7 +770,7 @@ __device__ __forceinline__ Cut any_cut(Token<D, kPaged, NT>& tk, const Keys<D, k
         } else {
           const int i = atomicAdd(misc + 3, 1);
           if (i < kList) idx[i] = c;
-          if (key == 0) keys.store(c, 1);                // (not a sure one)
+          if (key == 0) keys.store(c, khi != 0 ? khi : klo);  // (not a sure one; within the window)
         }
       }
       int n0[1] = {zeros};
