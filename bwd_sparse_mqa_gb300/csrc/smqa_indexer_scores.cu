@@ -18,8 +18,9 @@
 //
 // Backward, one CTA per token, two per SM.  Per block of 64 slots: gather (warps 4-5);
 // tensor core (warp 6): L = Q.K^T (M = 128 head rows, N = 64, K = D), and once the gate
-// operand G[h,j] = [L > 0] w[h] g[j] is written in bf16 (the one rounding on the way to
-// dq and dk, 2^-8 of each term at most), dq += G.K into an accumulator that lives for the token,
+// operand G[h,j] = [L > 0] w[h] g[j] is written in bf16 (the type of the products' other
+// factors, and the one rounding on the way to dq and dk: 2^-8 of each term at most),
+// dq += G.K into an accumulator that lives for the token,
 // and dk^T = Q^T.G (M = D, N = 64, K = 128 heads; both operands read MN-major from where
 // they lie); gate (warps 0-3): thread = head row, which also sums dw in fp32; drain
 // (warps 8-11): thread = element of D, adds dk^T to the fp32 accumulator in global

@@ -1149,9 +1149,10 @@ cudaError_t launch_select(const TopkParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 // Long rows, or few tokens with more than short ones: 1024 threads and one CTA per SM;
-// else 256 and three.  H = 64, D = 128, topk = 2048, us a call with 256 and with 1024: 16
-// paged tokens over 8192 positions 49 and 42, 150 over 12000 98 and 90; 300 over 12000 132
-// and 147, S = 8192 729 and 1156.
+// else 256 and three.  H = 64, D = 128, topk = 2048, us a call with 256 and with 1024 (nothing
+// in L2): 16 paged tokens over 8192 positions 58 and 52, 150 over 12000 103 and 95; 300 over
+// 12000 140 and 161, S = 8192 673 and 1101.  (A row's pitch is the table's width with paged
+// keys: the host does not know the lengths.)
 template <int D, bool kPaged>
 cudaError_t launch_select(const TopkParams& p, cudaStream_t stream) {
   return p.ld > SelLayout<D, 256>::kCap || (p.toks <= kSMs && p.ld > 4096) ? launch_select<D, kPaged, 1024>(p, stream)
@@ -1166,8 +1167,8 @@ constexpr int64_t kLim = int64_t{1} << 31;
 // up to 1024 threads, in 32 bits.
 constexpr int64_t kMaxCount = kLim - 2048;
 // Bytes of scores that a chunk of tokens may take: half of L2, from which the choice reads
-// them.  (S = 8192, H = 64, topk = 2048: 955 us with 16 MB, 728 with 64, 710 with 256 or 1024,
-// whose workspace a caller would have to hold.)
+// them, or one group's.  (S = 8192, H = 64, topk = 2048: 902 us with 16 MB, 673 with 64, 640 with
+// 256, whose workspace a caller would have to hold.)
 constexpr int64_t kChunkBytes = int64_t{64} << 20;
 
 smqa_status refuse(smqa_status st, const char* why) {

@@ -26,9 +26,9 @@
 // the two).  Described and fetched only behind a group's own copies, as it was, queries
 // came late: a part of 16 tiles waited 12000 clocks for them.
 //
-// What bounds it is the epilogue, not the tensor core (1024 clocks a tile of 256 columns;
-// with half of the products left out S = 8192 took 377 us of 385): a thread's chain of
-// barrier, loads, sums and stores.  With contiguous keys and up to 64 heads four warpgroups
+// What bounds it is the epilogue, more than the tensor core (1024 clocks a tile of 256
+// columns; without half of the products 1000 queries over 32768 positions took 310 us of
+// 322, 2 x 4096 tokens 184 of 211): a thread's chain of barrier, loads, sums and stores.  With contiguous keys and up to 64 heads four warpgroups
 // share a tile's columns, 64 each, and hide each other's latencies (1000 queries over 32768
 // positions of 64 heads: 404 us with two of 128 columns, 325 with four; S = 8192 in four
 // chunks 401 and 323).  More than 64 heads need a thread that sums 128 columns; paged keys,

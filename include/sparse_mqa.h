@@ -577,7 +577,8 @@ smqa_status smqa_paged_fwd(const void* q, const void* kv_cache, const float* kv_
  * rows j <= that position (S_kv - S: the last S positions of a causal sequence;
  * S_kv: every row).  1 <= H <= 128, D in {64, 128}, B*S < 2^31, B*S_kv < 2^31,
  * S_kv and topk up to 2^31 - 2048, block_size a power of two up to 128, topk a
- * multiple of it.  Two launches for every 64 MB of scores.
+ * multiple of it.  Two launches for every 64 MB of scores (4 bytes per token and
+ * block of up to 32 positions), or for every 256 / H tokens where those take more.
  *   workspace  256-byte aligned, smqa_indexer_topk_workspace_bytes(shape,
  *              block_size) bytes (0: unsupported); needs no initialisation; calls
  *              whose kernels may overlap must not share it
@@ -598,6 +599,10 @@ smqa_status smqa_indexer_topk(const void* index_q, const float* weights, const v
  *             seq_lens[req], on pages that the table has
  *   topk_idxs [T,topk]  positions in the token's own request.  Rows of padding
  *             tokens are left as they were, or -1 with SMQA_FLAG_ZERO_PADDING.
+ * Row pitch, chunks and workspace follow max_pages * page_size, not the lengths (which
+ * the host does not know; 4 bytes more per 32 positions bound the rows' lengths): 1024
+ * prompt tokens over 8192 positions take 175 us with a table of 8192 positions and 474
+ * with one of 131072.
  * The limits of magnitudes hold for the codes as well as for the codes times their
  * scales, and |w_h q_hi| < 2^126; 2^-126 is times the scale where that is above 1.
  * page_size in {16,32,64,128}, n_pages * page_size < 2^31, max_pages * page_size and
